@@ -73,6 +73,13 @@ for _n in ("fp8_fp4", "fp8_fp8", "fp4_fp4"):
         _SIGS[f"mx_gemm_{_n}{_v}"] = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P]
         _SIGS[f"mx_gemm_{_n}{_v}_strided_batched"] = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I,
                                                       _I, _I, _I, _I, _I, _I, _I, _P]
+# Attention operators (include/mx_attention.h): an argument struct and the stream.
+for _n in ("mx_qk_norm_rope", "mx_qk_norm_rope_backward", "mx_kv_append_fp4", "mx_attn_fp4"):
+    _SIGS[_n] = [ctypes.c_char_p, _P]
+_SIGS["mx_qk_norm_rope_backward_workspace_size"] = [_I, _I, _I, _I]
+_SIGS["mx_attn_fp4_workspace_size"] = [_I, _I, _I, _I, _I]
+_INT64_RESULTS = ("mx_gemm_splitk_workspace_size", "mx_qk_norm_rope_backward_workspace_size",
+                  "mx_attn_fp4_workspace_size")
 
 
 def load(path: str | None = None) -> ctypes.CDLL:
@@ -90,7 +97,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         fn.restype = ctypes.c_int
     lib.mx_status_str.argtypes = [ctypes.c_int]
     lib.mx_status_str.restype = ctypes.c_char_p
-    lib.mx_gemm_splitk_workspace_size.restype = ctypes.c_int64
+    for name in _INT64_RESULTS:
+        getattr(lib, name).restype = ctypes.c_int64
     _lib = lib
     return lib
 
@@ -610,3 +618,17 @@ def mx_gemm_e5m2_e4m3_splitk(a, a_s, b, b_s, c, workspace, stream=None):
     _check("mx_gemm_e5m2_e4m3_splitk",
            load().mx_gemm_e5m2_e4m3_splitk(_ptr(a), _ptr(a_s), _ptr(b), _ptr(b_s), _ptr(c), M, N,
                                            K, _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+# The attention operators (include/mx_attention.h) are in attention.py, imported when first used.
+_ATTENTION = ("MxKvCacheFp4", "mx_attn_fp4", "mx_attn_fp4_workspace_size", "mx_kv_append_fp4",
+              "mx_qk_norm_rope", "mx_qk_norm_rope_backward",
+              "mx_qk_norm_rope_backward_workspace_size")
+
+
+def __getattr__(name):
+    if name not in _ATTENTION:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import attention
+    globals().update({n: getattr(attention, n) for n in _ATTENTION})
+    return globals()[name]

@@ -1,0 +1,60 @@
+// Device pieces shared by the attention operators' kernels.
+#pragma once
+
+#include "attn_internal.h"
+#include "mx_quant.h"
+
+namespace mx {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+// s_waitcnt operand that waits for every vector-memory access of the wavefront and nothing else.
+constexpr int kVmcntZero = 0x0F70;
+
+constexpr float kNaN = __builtin_nanf("");
+constexpr float kInf = __builtin_inff();
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Two fp32 rounded to nearest even into packed bf16 (v_cvt_pk_bf16_f32; NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  const v2f v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// Called by every thread of a workgroup once its stores of a partial result are issued: makes
+// them visible to the whole device and counts the workgroup in at `counter`.  Returns (to every
+// thread) whether it is the last of `expected`; the last one then sees what all others stored,
+// and has put the counter back to zero.
+//   (1) Every wavefront waits until its own stores are complete; (2) past the barrier the whole
+//   workgroup's are; (3) thread 0's device-scope release writes them back past this XCD's L2
+//   before its arrival can be seen; (4) the last arrival's acquire drops what this XCD's caches
+//   may hold stale, before the barrier lets any thread load.
+__device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t expected, uint32_t* flag) {
+  __builtin_amdgcn_s_waitcnt(kVmcntZero);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    __builtin_amdgcn_s_waitcnt(kVmcntZero);
+    const uint32_t n = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+    const bool last = n + 1 == expected;
+    if (last) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    *flag = last;
+  }
+  __syncthreads();
+  return *flag != 0u;
+}
+
+}  // namespace
+}  // namespace mx

@@ -1,0 +1,101 @@
+// Internal interface between the C-ABI layer of the attention operators (attn_api.cpp) and their
+// gfx950 kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <cstdint>
+
+namespace mx {
+
+// Position rotation (see mx_attention.h).  positions == nullptr: none.
+struct Rotation {
+  const int32_t* positions;
+  const float* cos;          // [rows, rot / 2]
+  const float* sin;
+  uint32_t rows;
+  int rot;
+  bool interleaved;
+};
+
+// One tensor of bf16 heads [tokens, heads, head_dim] and where its rows lie (element strides).
+struct HeadRows {
+  uint16_t* p;
+  int64_t token_stride, head_stride;
+};
+
+struct NormRopeProblem {
+  HeadRows x[2], out[2];     // queries, keys (heads[1] == 0: no keys)
+  const uint16_t* weight[2]; // bf16 [head_dim] or nullptr
+  Rotation rot;
+  uint32_t tokens, heads[2];
+  int head_dim;
+  float eps;
+};
+hipError_t launch_qk_norm_rope(const NormRopeProblem& p, hipStream_t stream);
+
+struct NormRopeBackProblem {
+  HeadRows dy[2], x[2], dx[2];
+  const uint16_t* weight[2];
+  float* dweight[2];         // fp32 [head_dim] or nullptr
+  Rotation rot;
+  uint32_t tokens, heads[2];
+  int head_dim;
+  float eps;
+  uint32_t* counters;        // two, zero between calls
+  float* parts;              // [groups][head_dim]
+};
+// Workgroups that the gradients' rows are dealt to; each leaves one partial weight gradient.
+constexpr int kNormBackGroups = 512;
+constexpr int64_t kNormBackCounterBytes = 256;
+hipError_t launch_qk_norm_rope_backward(const NormRopeBackProblem& p, hipStream_t stream);
+
+struct KvCache {
+  uint8_t *k, *ks, *v, *vs;
+  int64_t code_page, code_head, scale_page, scale_head;   // byte strides
+  uint32_t pages, heads, page_size;
+  int head_dim;
+};
+
+struct KvAppendProblem {
+  KvCache cache;
+  HeadRows k, v;
+  const int64_t* slots;
+  Rotation rot;
+  uint16_t *k_out, *v_out;   // or nullptr
+  uint32_t tokens;
+};
+hipError_t launch_kv_append_fp4(const KvAppendProblem& p, hipStream_t stream);
+
+struct AttnProblem {
+  KvCache cache;
+  HeadRows q, out;
+  float* lse;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* starts;     // or nullptr: max_q rows each
+  int64_t table_stride;
+  int32_t table_width;
+  uint32_t page_div;         // ceil(2^32 / (page_size / 16)): n / (page_size / 16) as a high product
+  int32_t batch, total_q, max_q, group;
+  float scale_log2;          // scale * log2(e)
+  bool causal;
+  int32_t window;
+  uint32_t* counters;        // one per (sequence, key/value head) (and row block), zero between calls
+  float* parts;
+};
+
+// How a problem's rows are dealt out, by its sizes alone.  A sequence's rows for one key/value
+// head are its (query, grouped head) pairs, max_q * group of them at most.
+struct AttnPlan {
+  bool few;                  // few rows: the cache is what costs (attn_few.hip), else attn_many.hip
+  int row_tiles;             // few: 16-row tiles held at once (1, 2 or 4)
+  int groups;                // few: workgroups that the cached tokens are dealt to
+  int row_blocks, splits;    // many: blocks of rows for each (sequence, head), parts of the keys
+  int64_t counter_bytes, bytes;
+};
+AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim);
+
+hipError_t launch_attn_few(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream);
+hipError_t launch_attn_many(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream);
+
+}  // namespace mx

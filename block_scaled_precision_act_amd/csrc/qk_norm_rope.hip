@@ -1,0 +1,275 @@
+// Per-head norm of queries and keys with the position rotation in the same pass, and its
+// gradients, for gfx950.
+//
+// Forward, for a head x of D values at position p, in fp32:
+//   r = rsqrt(mean(x^2) + eps), n = x r w, y = R(p) n, rounded once to bf16.
+// Backward (the rotation's transpose turns back): n' = R(p)^T dy, g = n' w,
+//   dx = r (g - x r^2 mean(g x)),  dw = sum over rows of n' x r.
+//
+// Both are bound by HBM: every input read once, every output written once.  D / 8 lanes own a row,
+// 8 values each, chosen so that a lane holds both members of its rotated pairs: values
+// [4 j, 4 j + 4) and [rot/2 + 4 j, ...) for pairs half a rotation apart, 8 neighbours for
+// interleaved pairs and for what lies past `rot`.  So the rotation needs no exchange, the row sums
+// are log2(D / 8) lane exchanges, and loads are 8 bytes a lane in runs of at least 32 bytes.
+#include "attn_common.h"
+
+namespace mx {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Sum over the LR lanes that own a row.
+template <int LR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < LR; m *= 2) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+// Which 8 values of a row lane j owns: [c0, c0 + 4) and [c1, c1 + 4).
+struct LaneChunks {
+  int c0, c1;
+  bool turned;     // the lane's values are rotated, by table entries [4 j, 4 j + 4)
+};
+
+template <bool INTER>
+__device__ __forceinline__ LaneChunks lane_chunks(int j, int rot) {
+  const int half = rot >> 1;
+  const bool turned = 8 * j < rot;
+  if (INTER || !turned) return {8 * j, 8 * j + 4, turned};
+  return {4 * j, half + 4 * j, true};
+}
+
+// Turns the lane's pairs by (c, s): (a, b) -> (a c - b s, b c + a s).
+template <bool INTER>
+__device__ __forceinline__ void turn(float (&x)[8], const float4& c, const float4& s) {
+  const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + 4;
+    const float a = x[ia], b = x[ib];
+    x[ia] = a * cc[i] - b * ss[i];
+    x[ib] = b * cc[i] + a * ss[i];
+  }
+}
+
+__device__ __forceinline__ void widen(const uint2& lo, const uint2& hi, float (&x)[8]) {
+  x[0] = bf16_lo(lo.x); x[1] = bf16_hi(lo.x); x[2] = bf16_lo(lo.y); x[3] = bf16_hi(lo.y);
+  x[4] = bf16_lo(hi.x); x[5] = bf16_hi(hi.x); x[6] = bf16_lo(hi.y); x[7] = bf16_hi(hi.y);
+}
+
+__device__ __forceinline__ void load8(const uint16_t* row, const LaneChunks& lc, float (&x)[8]) {
+  widen(*reinterpret_cast<const uint2*>(row + lc.c0), *reinterpret_cast<const uint2*>(row + lc.c1),
+        x);
+}
+
+__device__ __forceinline__ void store8(uint16_t* row, const LaneChunks& lc, const float (&x)[8]) {
+  *reinterpret_cast<uint2*>(row + lc.c0) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  *reinterpret_cast<uint2*>(row + lc.c1) = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// A token's table entries of lane j; a position outside the table sets `bad`.
+__device__ __forceinline__ void load_turn(const Rotation& r, uint32_t t, int j, bool turned,
+                                          float4* c, float4* s, bool* bad) {
+  *c = make_float4(1.f, 1.f, 1.f, 1.f);
+  *s = make_float4(0.f, 0.f, 0.f, 0.f);
+  *bad = false;
+  if (!r.positions) return;
+  const uint32_t pos = static_cast<uint32_t>(r.positions[t]);
+  *bad = pos >= r.rows;
+  if (turned && !*bad) {
+    const int64_t at = static_cast<int64_t>(pos) * (r.rot >> 1) + 4 * j;
+    *c = *reinterpret_cast<const float4*>(r.cos + at);
+    *s = *reinterpret_cast<const float4*>(r.sin + at);
+  }
+}
+
+template <int LR, bool INTER, int U>
+__global__ __launch_bounds__(kThreads) void norm_rope_kernel(const NormRopeProblem p) {
+  constexpr int D = 8 * LR, RG = kThreads / LR;
+  const int j = threadIdx.x % LR;
+  const LaneChunks lc = lane_chunks<INTER>(j, p.rot.rot);
+  const uint32_t heads = p.heads[0] + p.heads[1], total = p.tokens * heads;
+  const uint32_t first = blockIdx.x * (RG * U) + threadIdx.x / LR;
+  float w[2][8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (p.weight[i]) load8(p.weight[i], lc, w[i]);
+  uint32_t t[U], h[U];
+  float x[U][8];
+  t[0] = first / heads;
+  h[0] = first - t[0] * heads;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (u > 0) {
+      const uint32_t n = h[u - 1] + RG, q = n / heads;
+      t[u] = t[u - 1] + q;
+      h[u] = n - q * heads;
+    }
+    if (first + u * RG < total) {
+      const int i = h[u] >= p.heads[0];
+      const HeadRows& r = p.x[i];
+      load8(r.p + t[u] * r.token_stride + (h[u] - (i ? p.heads[0] : 0)) * r.head_stride, lc, x[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    // Lanes of a row are active together: `total` counts whole rows.
+    if (first + u * RG >= total) break;
+    const int i = h[u] >= p.heads[0];
+    float4 c, s;
+    bool bad;
+    load_turn(p.rot, t[u], j, lc.turned, &c, &s, &bad);
+    if (p.weight[i]) {
+      float sq = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq += x[u][e] * x[u][e];
+      const float r = rsqrtf(row_sum<LR>(sq) * (1.f / D) + p.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] = x[u][e] * r * w[i][e];
+    }
+    turn<INTER>(x[u], c, s);
+    if (bad) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] = kNaN;
+    }
+    const HeadRows& o = p.out[i];
+    store8(o.p + t[u] * o.token_stride + (h[u] - (i ? p.heads[0] : 0)) * o.head_stride, lc, x[u]);
+  }
+}
+
+// Workgroups [0, groups_q) take the queries' rows, the rest the keys'; rows are dealt round robin,
+// RG at a time.  A lane sums its 8 weight gradients over its rows in fp32 (at most a few hundred
+// rows a chain), the workgroup's lanes are summed through LDS, and the last workgroup of a tensor
+// to arrive sums all its workgroups' partials in their order, so the result does not depend on
+// which one that is.
+template <int LR, bool INTER>
+__global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRopeBackProblem p,
+                                                                  uint32_t groups_q,
+                                                                  uint32_t groups_k) {
+  constexpr int D = 8 * LR, RG = kThreads / LR;
+  __shared__ float sums[RG * D];
+  __shared__ uint32_t flag;
+  const int i = blockIdx.x >= groups_q;
+  const uint32_t group = blockIdx.x - (i ? groups_q : 0), groups = i ? groups_k : groups_q;
+  const int j = threadIdx.x % LR, rg = threadIdx.x / LR;
+  const LaneChunks lc = lane_chunks<INTER>(j, p.rot.rot);
+  const uint32_t heads = p.heads[i], total = p.tokens * heads;
+  const bool norm = p.weight[i] != nullptr;
+  float w[8], acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = 1.f, acc[e] = 0.f;
+  if (norm) load8(p.weight[i], lc, w);
+  for (uint64_t row = static_cast<uint64_t>(group) * RG + rg; row < total; row += static_cast<uint64_t>(groups) * RG) {
+    const uint32_t t = static_cast<uint32_t>(row) / heads, h = static_cast<uint32_t>(row) - t * heads;
+    float dy[8], x[8];
+    load8(p.dy[i].p + t * p.dy[i].token_stride + h * p.dy[i].head_stride, lc, dy);
+    if (norm) load8(p.x[i].p + t * p.x[i].token_stride + h * p.x[i].head_stride, lc, x);
+    float4 c, s;
+    bool bad;
+    load_turn(p.rot, t, j, lc.turned, &c, &s, &bad);
+    turn<INTER>(dy, c, make_float4(-s.x, -s.y, -s.z, -s.w));
+    if (bad) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dy[e] = kNaN;
+    }
+    if (norm) {
+      float sq = 0.f, gx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sq += x[e] * x[e];
+        gx += dy[e] * w[e] * x[e];
+      }
+      const float r = rsqrtf(row_sum<LR>(sq) * (1.f / D) + p.eps);
+      const float m = row_sum<LR>(gx) * (1.f / D) * r * r;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        acc[e] += dy[e] * (x[e] * r);
+        dy[e] = r * (dy[e] * w[e] - x[e] * m);
+      }
+    }
+    store8(p.dx[i].p + t * p.dx[i].token_stride + h * p.dx[i].head_stride, lc, dy);
+  }
+  if (!p.dweight[i]) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[rg * D + (e < 4 ? lc.c0 + e : lc.c1 + e - 4)] = acc[e];
+  __syncthreads();
+  float* const parts = p.parts + static_cast<int64_t>(blockIdx.x) * D;
+  if (threadIdx.x < D) {
+    float v = 0.f;
+#pragma unroll 8
+    for (int g = 0; g < RG; ++g) v += sums[g * D + threadIdx.x];
+    parts[threadIdx.x] = v;
+  }
+  if (!arrive_last(p.counters + i, groups, &flag)) return;
+  // The last workgroup: D / 4 lanes by kThreads * 4 / D runs of partials, then the runs' sums.
+  constexpr int L4 = D / 4, RUNS = kThreads / L4;
+  const float* all = p.parts + static_cast<int64_t>(i ? groups_q : 0) * D;
+  const int d4 = threadIdx.x % L4, run = threadIdx.x / L4;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (uint32_t g = run; g < groups; g += RUNS) {
+    const float4 a = *reinterpret_cast<const float4*>(all + static_cast<int64_t>(g) * D + 4 * d4);
+    v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+  }
+  *reinterpret_cast<float4*>(&sums[run * D + 4 * d4]) = v;
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float z = 0.f;
+    for (int g = 0; g < RUNS; ++g) z += sums[g * D + threadIdx.x];
+    p.dweight[i][threadIdx.x] = z;
+  }
+}
+
+template <int LR>
+hipError_t launch_forward(const NormRopeProblem& p, hipStream_t stream) {
+  constexpr int U = 2, RG = kThreads / LR;
+  const uint64_t rows = static_cast<uint64_t>(p.tokens) * (p.heads[0] + p.heads[1]);
+  const dim3 grid(static_cast<unsigned>((rows + RG * U - 1) / (RG * U)));
+  if (p.rot.interleaved)
+    hipLaunchKernelGGL((norm_rope_kernel<LR, true, U>), grid, dim3(kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((norm_rope_kernel<LR, false, U>), grid, dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <int LR>
+hipError_t launch_backward(const NormRopeBackProblem& p, hipStream_t stream) {
+  constexpr uint64_t RG = kThreads / LR;
+  // Workgroups in proportion to the rows, no more than there are runs of RG rows; one for a
+  // weight gradient without rows, which it writes as zero.
+  uint32_t groups[2];
+  const uint64_t heads = p.heads[0] + p.heads[1];
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t rows = static_cast<uint64_t>(p.tokens) * p.heads[i];
+    const uint64_t share = heads ? (kNormBackGroups - 1) * p.heads[i] / heads : 0;
+    const uint64_t most = (rows + RG - 1) / RG;
+    groups[i] = static_cast<uint32_t>(most < share ? most : share);
+    if (groups[i] == 0 && (rows > 0 || p.dweight[i])) groups[i] = 1;
+  }
+  if (groups[0] + groups[1] == 0) return hipSuccess;
+  const dim3 grid(groups[0] + groups[1]);
+  if (p.rot.interleaved)
+    hipLaunchKernelGGL((norm_rope_back_kernel<LR, true>), grid, dim3(kThreads), 0, stream, p,
+                       groups[0], groups[1]);
+  else
+    hipLaunchKernelGGL((norm_rope_back_kernel<LR, false>), grid, dim3(kThreads), 0, stream, p,
+                       groups[0], groups[1]);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(const NormRopeProblem& p, hipStream_t stream) {
+  if (p.head_dim == 64) return launch_forward<8>(p, stream);
+  if (p.head_dim == 128) return launch_forward<16>(p, stream);
+  return launch_forward<32>(p, stream);
+}
+
+hipError_t launch_qk_norm_rope_backward(const NormRopeBackProblem& p, hipStream_t stream) {
+  if (p.head_dim == 64) return launch_backward<8>(p, stream);
+  if (p.head_dim == 128) return launch_backward<16>(p, stream);
+  return launch_backward<32>(p, stream);
+}
+
+}  // namespace mx

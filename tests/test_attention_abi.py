@@ -1,0 +1,228 @@
+"""The attention operators' C ABI on the host, with no GPU: the library exports what
+include/mx_attention.h declares, and every argument error is a status before any device work."""
+import os
+import re
+import struct
+
+import pytest
+import torch
+
+import block_scaled_precision_act_amd as mx
+from block_scaled_precision_act_amd import attention as at
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = open(os.path.join(ROOT, "include", "mx_attention.h")).read()
+A = 1 << 20            # a fake aligned address: never dereferenced by these calls
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(mx.LIB_PATH):
+        from block_scaled_precision_act_amd import build
+        build.build()
+    return mx.load()
+
+
+def _fields(name):
+    """Field names of a struct of the header, in order, with their types' struct codes."""
+    body = re.search(r"typedef struct %s \{(.*?)\} %s;" % (name, name), HEADER, re.S).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    out = []
+    for decl in body.split(";"):
+        decl = decl.strip()
+        if not decl:
+            continue
+        if "*" in decl:
+            out.append((decl.split("*")[-1].strip(), "Q"))
+            continue
+        kind, names = decl.split(" ", 1)
+        out += [(n.strip(), {"int64_t": "q", "double": "d"}[kind]) for n in names.split(",")]
+    return out
+
+
+STRUCTS = {"mx_kv_cache_fp4": at._CACHE, "mx_qk_norm_rope_args": at._NORM_ROPE,
+           "mx_qk_norm_rope_backward_args": at._NORM_ROPE_BACK, "mx_kv_append_fp4_args": at._APPEND,
+           "mx_attn_fp4_args": at._ATTN}
+
+
+@pytest.mark.parametrize("name", STRUCTS)
+def test_the_binding_packs_the_headers_structs(name):
+    fields = _fields(name)
+    flat = struct.Struct("=" + "".join(c for _, c in fields))
+    assert flat.size == 8 * len(fields) == STRUCTS[name].size
+    assert re.sub(r"(\d+)(\w)", lambda m: m[2] * int(m[1]), STRUCTS[name].format[1:]) == flat.format[1:]
+
+
+def test_library_exports_and_binding_covers_every_declared_symbol(lib):
+    names = sorted(set(re.findall(r"^\s*(?:int|int64_t)\s+(mx_\w+)\s*\(", HEADER, re.M)))
+    assert names == ["mx_attn_fp4", "mx_attn_fp4_workspace_size", "mx_kv_append_fp4", "mx_qk_norm_rope",
+                     "mx_qk_norm_rope_backward", "mx_qk_norm_rope_backward_workspace_size"]
+    for n in names:
+        assert hasattr(lib, n) and n in mx._SIGS and callable(getattr(mx, n))
+
+
+def _pack(name, values):
+    fields = _fields(name)
+    assert set(values) <= {n for n, _ in fields}
+    return STRUCTS[name].pack(*(values.get(n, 0) for n, _ in fields))
+
+
+CACHE = dict(k=A, k_scale=A, v=A, v_scale=A, pages=10, kv_heads=2, page_size=16, head_dim=128,
+             code_page_stride=2 * 16 * 64, code_head_stride=16 * 64, scale_page_stride=2 * 16 * 4,
+             scale_head_stride=16 * 4)
+NORM = dict(q=A, k=A, q_out=A, k_out=A, q_weight=A, k_weight=A, positions=A, cos=A, sin=A,
+            q_token_stride=1024, q_head_stride=128, k_token_stride=1024, k_head_stride=128,
+            q_out_token_stride=512, q_out_head_stride=128, k_out_token_stride=256, k_out_head_stride=128,
+            tokens=3, q_heads=4, k_heads=2, head_dim=128, table_rows=64, rot=128, interleaved=0, eps=1e-6)
+ATTN = dict(q=A, out=A, page_table=A, seq_lens=A, workspace=A, workspace_bytes=1 << 30, q_token_stride=512,
+            q_head_stride=128, out_token_stride=512, out_head_stride=128, table_stride=8, table_width=8,
+            batch=2, total_q=2, max_q=1, q_heads=4, causal=1, window=0, scale=0.1)
+APPEND = dict(k=A, v=A, slots=A, positions=A, cos=A, sin=A, k_out=A, v_out=A, k_token_stride=256,
+              k_head_stride=128, v_token_stride=256, v_head_stride=128, tokens=3, table_rows=9, rot=64)
+
+
+def _cache_address(keep, **change):
+    import ctypes
+    buf = ctypes.create_string_buffer(_pack("mx_kv_cache_fp4", {**CACHE, **change}))
+    keep.append(buf)
+    return ctypes.addressof(buf)
+
+
+def _no_gpu_status():
+    return mx.MX_ERR_DEVICE if not torch.cuda.is_available() else None
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(head_dim=96), mx.MX_ERR_SHAPE), (dict(tokens=-1), mx.MX_ERR_SHAPE), (dict(eps=-1.0), mx.MX_ERR_SHAPE),
+    (dict(eps=float("nan")), mx.MX_ERR_SHAPE), (dict(tokens=1 << 30), mx.MX_ERR_SHAPE),
+    (dict(rot=24), mx.MX_ERR_SHAPE), (dict(rot=144), mx.MX_ERR_SHAPE), (dict(rot=0), mx.MX_ERR_SHAPE),
+    (dict(cos=0), mx.MX_ERR_NULL), (dict(sin=A + 8), mx.MX_ERR_ALIGN), (dict(q=0), mx.MX_ERR_NULL),
+    (dict(q_out=0), mx.MX_ERR_NULL), (dict(k_out=0), mx.MX_ERR_NULL), (dict(q=A + 2), mx.MX_ERR_ALIGN),
+    (dict(q_token_stride=1026), mx.MX_ERR_ALIGN), (dict(k_head_stride=-128), mx.MX_ERR_STRIDE),
+    (dict(q_out_head_stride=64), mx.MX_ERR_STRIDE), (dict(k_out_token_stride=0), mx.MX_ERR_STRIDE),
+    (dict(q_weight=A + 4), mx.MX_ERR_ALIGN), (dict(tokens=0, q=0, k_out=0), mx.MX_OK),
+    (dict(k=0, k_out=0, k_heads=99), "device"), (dict(q_token_stride=0), "device"), ({}, "device"),
+    (dict(positions=0, cos=0, sin=0, rot=7), "device")])
+def test_norm_rope(lib, change, status):
+    if status == "device":
+        if torch.cuda.is_available():
+            pytest.skip("a GPU is visible: fake addresses must not reach it")
+        status = mx.MX_ERR_DEVICE
+    assert lib.mx_qk_norm_rope(_pack("mx_qk_norm_rope_args", {**NORM, **change}), None) == status
+    assert lib.mx_qk_norm_rope(None, None) == mx.MX_ERR_NULL
+
+
+def test_norm_rope_backward(lib):
+    f = lib.mx_qk_norm_rope_backward
+    need = mx.mx_qk_norm_rope_backward_workspace_size(3, 4, 2, 128)
+    assert need > 0 and mx.mx_qk_norm_rope_backward_workspace_size(0, 4, 2, 128) == 0
+    assert mx.mx_qk_norm_rope_backward_workspace_size(3, 4, 2, 100) == 0
+    strides = {f"{t}_{s}_stride": n for t in ("dq_out", "dk_out", "q", "k", "dq", "dk")
+               for s, n in (("token", 512), ("head", 128))}
+    good = dict(dq_out=A, dk_out=A, q=A, k=A, dq=A, dk=A, q_weight=A, k_weight=A, dq_weight=A, dk_weight=A,
+                positions=A, cos=A, sin=A, workspace=A, workspace_bytes=need, tokens=3, q_heads=4, k_heads=2,
+                head_dim=128, table_rows=9, rot=64, eps=1e-6, **strides)
+
+    def status(**change):
+        return f(_pack("mx_qk_norm_rope_backward_args", {**good, **change}), None)
+
+    assert f(None, None) == mx.MX_ERR_NULL
+    assert status(workspace=0) == mx.MX_ERR_WORKSPACE
+    assert status(workspace_bytes=need - 1) == mx.MX_ERR_WORKSPACE
+    assert status(workspace=A + 128) == mx.MX_ERR_WORKSPACE
+    assert status(q_weight=0) == mx.MX_ERR_NULL                     # a gradient of no weight
+    assert status(dk=0) == mx.MX_ERR_NULL and status(dq_out=0) == mx.MX_ERR_NULL
+    assert status(dq_head_stride=64) == mx.MX_ERR_STRIDE
+    assert status(dq_out_token_stride=514) == mx.MX_ERR_ALIGN
+    assert status(dq_weight=A + 2) == mx.MX_ERR_ALIGN
+    assert status(tokens=0, dq_weight=0, dk_weight=0, q=0) == mx.MX_OK
+    if not torch.cuda.is_available():
+        assert status() == mx.MX_ERR_DEVICE
+        assert status(dq_weight=0, dk_weight=0, workspace=0) == mx.MX_ERR_DEVICE
+        assert status(tokens=0, q=0) == mx.MX_ERR_DEVICE           # writes zero weight gradients
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(head_dim=32), mx.MX_ERR_SHAPE), (dict(page_size=24), mx.MX_ERR_SHAPE), (dict(page_size=0), mx.MX_ERR_SHAPE),
+    (dict(pages=1 << 27), mx.MX_ERR_SHAPE), (dict(pages=-1), mx.MX_ERR_SHAPE), (dict(kv_heads=0), mx.MX_ERR_SHAPE),
+    (dict(k=0), mx.MX_ERR_NULL), (dict(v_scale=0), mx.MX_ERR_NULL), (dict(v=A + 8), mx.MX_ERR_ALIGN),
+    (dict(k_scale=A + 4), mx.MX_ERR_ALIGN), (dict(code_page_stride=2 * 16 * 64 + 8), mx.MX_ERR_ALIGN),
+    (dict(scale_head_stride=72), mx.MX_ERR_ALIGN), (dict(code_head_stride=512), mx.MX_ERR_STRIDE),
+    (dict(scale_page_stride=-64), mx.MX_ERR_STRIDE), (dict(code_page_stride=0), mx.MX_ERR_STRIDE)])
+def test_cache_refusals(lib, change, status):
+    keep = []
+    c = _cache_address(keep, **change)
+    assert lib.mx_kv_append_fp4(_pack("mx_kv_append_fp4_args", {**APPEND, "cache": c}), None) == status
+    assert lib.mx_attn_fp4(_pack("mx_attn_fp4_args", {**ATTN, "cache": c}), None) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(cache=0), mx.MX_ERR_NULL), (dict(tokens=-1), mx.MX_ERR_SHAPE), (dict(tokens=1 << 31), mx.MX_ERR_SHAPE),
+    (dict(slots=0), mx.MX_ERR_NULL), (dict(k=0), mx.MX_ERR_NULL), (dict(v=A + 8), mx.MX_ERR_ALIGN),
+    (dict(k_token_stride=260), mx.MX_ERR_ALIGN), (dict(v_head_stride=-1), mx.MX_ERR_STRIDE),
+    (dict(rot=100), mx.MX_ERR_SHAPE), (dict(sin=0), mx.MX_ERR_NULL), (dict(k_out=A + 8), mx.MX_ERR_ALIGN),
+    (dict(slots=A + 4), mx.MX_ERR_ALIGN), (dict(tokens=0, k=0, slots=0), mx.MX_OK), ({}, "device")])
+def test_append(lib, change, status):
+    if status == "device":
+        if torch.cuda.is_available():
+            pytest.skip("a GPU is visible: fake addresses must not reach it")
+        status = mx.MX_ERR_DEVICE
+    keep = []
+    args = {**APPEND, "cache": _cache_address(keep), **change}
+    assert lib.mx_kv_append_fp4(_pack("mx_kv_append_fp4_args", args), None) == status
+    assert lib.mx_kv_append_fp4(None, None) == mx.MX_ERR_NULL
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(cache=0), mx.MX_ERR_NULL), (dict(q_heads=3), mx.MX_ERR_SHAPE), (dict(q_heads=0), mx.MX_ERR_SHAPE),
+    (dict(batch=-1), mx.MX_ERR_SHAPE), (dict(batch=70000), mx.MX_ERR_SHAPE), (dict(max_q=2), mx.MX_ERR_SHAPE),
+    (dict(window=3, causal=0), mx.MX_ERR_SHAPE), (dict(window=-3), mx.MX_ERR_SHAPE),
+    (dict(scale=float("nan")), mx.MX_ERR_SHAPE), (dict(table_width=1 << 28, table_stride=1 << 28), mx.MX_ERR_SHAPE),
+    (dict(table_stride=7), mx.MX_ERR_STRIDE), (dict(table_stride=-8), mx.MX_ERR_STRIDE),
+    (dict(page_table=0), mx.MX_ERR_NULL), (dict(seq_lens=0), mx.MX_ERR_NULL), (dict(q=0), mx.MX_ERR_NULL),
+    (dict(out=0), mx.MX_ERR_NULL), (dict(q=A + 8), mx.MX_ERR_ALIGN), (dict(out_token_stride=516), mx.MX_ERR_ALIGN),
+    (dict(out_head_stride=120), mx.MX_ERR_STRIDE), (dict(workspace=0), mx.MX_ERR_WORKSPACE),
+    (dict(workspace_bytes=1000), mx.MX_ERR_WORKSPACE), (dict(workspace=A + 16), mx.MX_ERR_WORKSPACE),
+    (dict(batch=0, total_q=0, q=0), mx.MX_OK), (dict(total_q=0, q_starts=A, q=0), mx.MX_OK),
+    ({}, "device"), (dict(q_token_stride=0), "device"), (dict(q_starts=A, total_q=1), "device")])
+def test_attn(lib, change, status):
+    if status == "device":
+        if torch.cuda.is_available():
+            pytest.skip("a GPU is visible: fake addresses must not reach it")
+        status = mx.MX_ERR_DEVICE
+    keep = []
+    args = {**ATTN, "cache": _cache_address(keep), **change}
+    assert lib.mx_attn_fp4(_pack("mx_attn_fp4_args", args), None) == status
+    assert lib.mx_attn_fp4(None, None) == mx.MX_ERR_NULL
+
+
+def test_attn_page_number_arithmetic_bound(lib):
+    # pages of 2^20 tokens: a table this wide would make the page number's high product inexact
+    keep = []
+    big = dict(pages=1, page_size=1 << 20, code_page_stride=1 << 30, code_head_stride=1 << 26,
+               scale_page_stride=1 << 30, scale_head_stride=1 << 24)
+    args = {**ATTN, "cache": _cache_address(keep, **big), "table_width": 2, "table_stride": 2}
+    assert lib.mx_attn_fp4(_pack("mx_attn_fp4_args", args), None) == mx.MX_ERR_SHAPE
+
+
+def test_attn_workspace_size(lib):
+    size = mx.mx_attn_fp4_workspace_size
+    assert size(1, 1, 32, 8, 128) > 0 and size(1, 1, 32, 8, 128) == size(1, 1, 40, 8, 128)
+    assert size(4, 8192, 32, 8, 128) == 0                 # enough blocks of rows: no parts to join
+    for bad in ((0, 1, 32, 8, 128), (1, 0, 32, 8, 128), (1, 1, 30, 8, 128), (1, 1, 32, 8, 80), (70000, 1, 32, 8, 128)):
+        assert size(*bad) == 0
+
+
+def test_host_tensors_are_refused_before_any_library_call():
+    x = torch.zeros((2, 4, 128), dtype=torch.bfloat16)
+    u = [torch.zeros((2, 2, 16, n), dtype=torch.uint8) for n in (64, 4)]
+    for call in (lambda: mx.mx_qk_norm_rope(x, None, None, None, None, x, None),
+                 lambda: mx.mx_qk_norm_rope_backward(x, None, x, None, None, None, None, x, None),
+                 lambda: mx.MxKvCacheFp4(u[0], u[1], u[0], u[1])):
+        with pytest.raises(mx.MxError) as e:
+            call()
+        assert e.value.status == mx.MX_ERR_DEVICE
+    for call in (lambda: mx.mx_kv_append_fp4(u[0], x, x, torch.zeros(2, dtype=torch.int64)),
+                 lambda: mx.mx_attn_fp4(u[0], x, None, None, x, None)):
+        with pytest.raises(TypeError):
+            call()
