@@ -18,11 +18,28 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sum over the LR lanes that own a row.
+// From this many rows on a row's owners take four heads at once (more loads in flight); below, the
+// rows alone do not fill the chip.
+constexpr uint64_t kManyRows = 32768;
+
+// Sum over the LR lanes that own a row, by DPP: quads, then mirrors of 8 and 16 lanes (whose quads
+// and halves already hold equal sums), then the two rows of 16.  All lanes are active.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(
+                 static_cast<int>(__float_as_uint(v)), CTRL, 0xF, 0xF, false)));
+}
+
 template <int LR>
 __device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < LR; m *= 2) v += __shfl_xor(v, m, 64);
+  v = dpp_add<0xB1>(v);                       // quad_perm [1,0,3,2]
+  v = dpp_add<0x4E>(v);                       // quad_perm [2,3,0,1]
+  v = dpp_add<0x141>(v);                      // row_half_mirror
+  if constexpr (LR >= 16) v = dpp_add<0x140>(v);   // row_mirror
+  if constexpr (LR >= 32) {
+    const v2u r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   return v;
 }
 
@@ -84,57 +101,56 @@ __device__ __forceinline__ void load_turn(const Rotation& r, uint32_t t, int j, 
   }
 }
 
+// A row's owners handle U heads of one token (one tensor's), all loaded before the first is used;
+// the token's table entries are loaded once.  Units of a token: its queries' heads by U, then its
+// keys'.
 template <int LR, bool INTER, int U>
-__global__ __launch_bounds__(kThreads) void norm_rope_kernel(const NormRopeProblem p) {
+__global__ __launch_bounds__(kThreads) void norm_rope_kernel(const NormRopeProblem p,
+                                                             uint32_t units_q, uint32_t units) {
   constexpr int D = 8 * LR, RG = kThreads / LR;
   const int j = threadIdx.x % LR;
   const LaneChunks lc = lane_chunks<INTER>(j, p.rot.rot);
-  const uint32_t heads = p.heads[0] + p.heads[1], total = p.tokens * heads;
-  const uint32_t first = blockIdx.x * (RG * U) + threadIdx.x / LR;
-  float w[2][8];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (p.weight[i]) load8(p.weight[i], lc, w[i]);
-  uint32_t t[U], h[U];
-  float x[U][8];
-  t[0] = first / heads;
-  h[0] = first - t[0] * heads;
+  const uint32_t unit = blockIdx.x * RG + threadIdx.x / LR;
+  // Owners past the last unit repeat it (the row sums need every lane) and write nothing.
+  const uint32_t all = p.tokens * units, at = min(unit, all - 1);
+  const uint32_t t = at / units, part = at - t * units;
+  const int i = part >= units_q;
+  const uint32_t h0 = (part - (i ? units_q : 0)) * U, heads = p.heads[i];
+  const HeadRows& in = p.x[i];
+  const uint16_t* src = in.p + t * in.token_stride + h0 * in.head_stride;
+  uint2 lo[U], hi[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (u > 0) {
-      const uint32_t n = h[u - 1] + RG, q = n / heads;
-      t[u] = t[u - 1] + q;
-      h[u] = n - q * heads;
-    }
-    if (first + u * RG < total) {
-      const int i = h[u] >= p.heads[0];
-      const HeadRows& r = p.x[i];
-      load8(r.p + t[u] * r.token_stride + (h[u] - (i ? p.heads[0] : 0)) * r.head_stride, lc, x[u]);
-    }
+    const uint16_t* row = src + (h0 + u < heads ? u : 0) * in.head_stride;
+    lo[u] = *reinterpret_cast<const uint2*>(row + lc.c0);
+    hi[u] = *reinterpret_cast<const uint2*>(row + lc.c1);
   }
+  float w[8];
+  const bool norm = p.weight[i] != nullptr;
+  if (norm) load8(p.weight[i], lc, w);
+  float4 c, s;
+  bool bad;
+  load_turn(p.rot, t, j, lc.turned, &c, &s, &bad);
+  const HeadRows& o = p.out[i];
+  uint16_t* dst = o.p + t * o.token_stride + h0 * o.head_stride;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    // Lanes of a row are active together: `total` counts whole rows.
-    if (first + u * RG >= total) break;
-    const int i = h[u] >= p.heads[0];
-    float4 c, s;
-    bool bad;
-    load_turn(p.rot, t[u], j, lc.turned, &c, &s, &bad);
-    if (p.weight[i]) {
+    float x[8];
+    widen(lo[u], hi[u], x);
+    if (norm) {
       float sq = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sq += x[u][e] * x[u][e];
+      for (int e = 0; e < 8; ++e) sq += x[e] * x[e];
       const float r = rsqrtf(row_sum<LR>(sq) * (1.f / D) + p.eps);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] = x[u][e] * r * w[i][e];
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
     }
-    turn<INTER>(x[u], c, s);
+    turn<INTER>(x, c, s);
     if (bad) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] = kNaN;
+      for (int e = 0; e < 8; ++e) x[e] = kNaN;
     }
-    const HeadRows& o = p.out[i];
-    store8(o.p + t[u] * o.token_stride + (h[u] - (i ? p.heads[0] : 0)) * o.head_stride, lc, x[u]);
+    if (h0 + u < heads && unit < all) store8(dst + u * o.head_stride, lc, x);
   }
 }
 
@@ -143,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(const NormRopeProbl
 // rows a chain), the workgroup's lanes are summed through LDS, and the last workgroup of a tensor
 // to arrive sums all its workgroups' partials in their order, so the result does not depend on
 // which one that is.
-template <int LR, bool INTER>
+template <int LR, bool INTER, int U>
 __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRopeBackProblem p,
                                                                   uint32_t groups_q,
                                                                   uint32_t groups_k) {
@@ -154,41 +170,64 @@ __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRope
   const uint32_t group = blockIdx.x - (i ? groups_q : 0), groups = i ? groups_k : groups_q;
   const int j = threadIdx.x % LR, rg = threadIdx.x / LR;
   const LaneChunks lc = lane_chunks<INTER>(j, p.rot.rot);
-  const uint32_t heads = p.heads[i], total = p.tokens * heads;
+  const uint32_t heads = p.heads[i], units = (heads + U - 1) / U, all = p.tokens * units;
   const bool norm = p.weight[i] != nullptr;
   float w[8], acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) w[e] = 1.f, acc[e] = 0.f;
   if (norm) load8(p.weight[i], lc, w);
-  for (uint64_t row = static_cast<uint64_t>(group) * RG + rg; row < total; row += static_cast<uint64_t>(groups) * RG) {
-    const uint32_t t = static_cast<uint32_t>(row) / heads, h = static_cast<uint32_t>(row) - t * heads;
-    float dy[8], x[8];
-    load8(p.dy[i].p + t * p.dy[i].token_stride + h * p.dy[i].head_stride, lc, dy);
-    if (norm) load8(p.x[i].p + t * p.x[i].token_stride + h * p.x[i].head_stride, lc, x);
+  const HeadRows &gy = p.dy[i], &in = p.x[i], &gx = p.dx[i];
+  // Every owner walks the same number of units (the row sums need every lane); past the last one it
+  // repeats it, writes nothing and adds nothing.
+  for (uint32_t base = group * RG; base < all; base += groups * RG) {
+    const uint32_t at = min(base + rg, all - 1);
+    const bool real = base + rg < all;
+    const uint32_t t = at / units, h0 = (at - t * units) * U;
+    uint2 ylo[U], yhi[U], xlo[U], xhi[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t h = h0 + u < heads ? h0 + u : h0;
+      const uint16_t* row = gy.p + t * gy.token_stride + h * gy.head_stride;
+      ylo[u] = *reinterpret_cast<const uint2*>(row + lc.c0);
+      yhi[u] = *reinterpret_cast<const uint2*>(row + lc.c1);
+      if (norm) {
+        row = in.p + t * in.token_stride + h * in.head_stride;
+        xlo[u] = *reinterpret_cast<const uint2*>(row + lc.c0);
+        xhi[u] = *reinterpret_cast<const uint2*>(row + lc.c1);
+      }
+    }
     float4 c, s;
     bool bad;
     load_turn(p.rot, t, j, lc.turned, &c, &s, &bad);
-    turn<INTER>(dy, c, make_float4(-s.x, -s.y, -s.z, -s.w));
-    if (bad) {
+    s = make_float4(-s.x, -s.y, -s.z, -s.w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dy[e] = kNaN;
-    }
-    if (norm) {
-      float sq = 0.f, gx = 0.f;
+    for (int u = 0; u < U; ++u) {
+      const bool live = real && h0 + u < heads;
+      float dy[8];
+      widen(ylo[u], yhi[u], dy);
+      turn<INTER>(dy, c, s);
+      if (bad) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sq += x[e] * x[e];
-        gx += dy[e] * w[e] * x[e];
+        for (int e = 0; e < 8; ++e) dy[e] = kNaN;
       }
-      const float r = rsqrtf(row_sum<LR>(sq) * (1.f / D) + p.eps);
-      const float m = row_sum<LR>(gx) * (1.f / D) * r * r;
+      if (norm) {
+        float x[8], sq = 0.f, dot = 0.f;
+        widen(xlo[u], xhi[u], x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        acc[e] += dy[e] * (x[e] * r);
-        dy[e] = r * (dy[e] * w[e] - x[e] * m);
+        for (int e = 0; e < 8; ++e) {
+          sq += x[e] * x[e];
+          dot += dy[e] * w[e] * x[e];
+        }
+        const float r = rsqrtf(row_sum<LR>(sq) * (1.f / D) + p.eps);
+        const float m = row_sum<LR>(dot) * (1.f / D) * r * r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (live) acc[e] += dy[e] * (x[e] * r);
+          dy[e] = r * (dy[e] * w[e] - x[e] * m);
+        }
       }
+      if (live) store8(gx.p + t * gx.token_stride + (h0 + u) * gx.head_stride, lc, dy);
     }
-    store8(p.dx[i].p + t * p.dx[i].token_stride + h * p.dx[i].head_stride, lc, dy);
   }
   if (!p.dweight[i]) return;
 #pragma unroll
@@ -204,12 +243,12 @@ __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRope
   if (!arrive_last(p.counters + i, groups, &flag)) return;
   // The last workgroup: D / 4 lanes by kThreads * 4 / D runs of partials, then the runs' sums.
   constexpr int L4 = D / 4, RUNS = kThreads / L4;
-  const float* all = p.parts + static_cast<int64_t>(i ? groups_q : 0) * D;
+  const float* parts_i = p.parts + static_cast<int64_t>(i ? groups_q : 0) * D;
   const int d4 = threadIdx.x % L4, run = threadIdx.x / L4;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (uint32_t g = run; g < groups; g += RUNS) {
-    const float4 a = *reinterpret_cast<const float4*>(all + static_cast<int64_t>(g) * D + 4 * d4);
+    const float4 a = *reinterpret_cast<const float4*>(parts_i + static_cast<int64_t>(g) * D + 4 * d4);
     v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
   }
   *reinterpret_cast<float4*>(&sums[run * D + 4 * d4]) = v;
@@ -221,41 +260,55 @@ __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRope
   }
 }
 
+template <int LR, int U>
+hipError_t launch_forward_u(const NormRopeProblem& p, hipStream_t stream) {
+  constexpr uint64_t RG = kThreads / LR;
+  const uint32_t units_q = (p.heads[0] + U - 1) / U, units = units_q + (p.heads[1] + U - 1) / U;
+  const dim3 grid(static_cast<unsigned>((static_cast<uint64_t>(p.tokens) * units + RG - 1) / RG));
+  if (p.rot.interleaved)
+    hipLaunchKernelGGL((norm_rope_kernel<LR, true, U>), grid, dim3(kThreads), 0, stream, p, units_q,
+                       units);
+  else
+    hipLaunchKernelGGL((norm_rope_kernel<LR, false, U>), grid, dim3(kThreads), 0, stream, p, units_q,
+                       units);
+  return hipGetLastError();
+}
+
 template <int LR>
 hipError_t launch_forward(const NormRopeProblem& p, hipStream_t stream) {
-  constexpr int U = 2, RG = kThreads / LR;
   const uint64_t rows = static_cast<uint64_t>(p.tokens) * (p.heads[0] + p.heads[1]);
-  const dim3 grid(static_cast<unsigned>((rows + RG * U - 1) / (RG * U)));
+  return rows >= kManyRows ? launch_forward_u<LR, 4>(p, stream) : launch_forward_u<LR, 1>(p, stream);
+}
+
+template <int LR, int U>
+hipError_t launch_backward_u(const NormRopeBackProblem& p, hipStream_t stream) {
+  constexpr uint64_t RG = kThreads / LR;
+  // Workgroups in proportion to the rows, no more than there are runs of RG units; one for a
+  // weight gradient without rows, which it writes as zero.
+  uint32_t groups[2];
+  const uint64_t heads = p.heads[0] + p.heads[1];
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t units = static_cast<uint64_t>(p.tokens) * ((p.heads[i] + U - 1) / U);
+    const uint64_t share = heads ? (kNormBackGroups - 1) * p.heads[i] / heads : 0;
+    const uint64_t most = (units + RG - 1) / RG;
+    groups[i] = static_cast<uint32_t>(most < share ? most : share);
+    if (groups[i] == 0 && (units > 0 || p.dweight[i])) groups[i] = 1;
+  }
+  if (groups[0] + groups[1] == 0) return hipSuccess;
+  const dim3 grid(groups[0] + groups[1]);
   if (p.rot.interleaved)
-    hipLaunchKernelGGL((norm_rope_kernel<LR, true, U>), grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((norm_rope_back_kernel<LR, true, U>), grid, dim3(kThreads), 0, stream, p,
+                       groups[0], groups[1]);
   else
-    hipLaunchKernelGGL((norm_rope_kernel<LR, false, U>), grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((norm_rope_back_kernel<LR, false, U>), grid, dim3(kThreads), 0, stream, p,
+                       groups[0], groups[1]);
   return hipGetLastError();
 }
 
 template <int LR>
 hipError_t launch_backward(const NormRopeBackProblem& p, hipStream_t stream) {
-  constexpr uint64_t RG = kThreads / LR;
-  // Workgroups in proportion to the rows, no more than there are runs of RG rows; one for a
-  // weight gradient without rows, which it writes as zero.
-  uint32_t groups[2];
-  const uint64_t heads = p.heads[0] + p.heads[1];
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t rows = static_cast<uint64_t>(p.tokens) * p.heads[i];
-    const uint64_t share = heads ? (kNormBackGroups - 1) * p.heads[i] / heads : 0;
-    const uint64_t most = (rows + RG - 1) / RG;
-    groups[i] = static_cast<uint32_t>(most < share ? most : share);
-    if (groups[i] == 0 && (rows > 0 || p.dweight[i])) groups[i] = 1;
-  }
-  if (groups[0] + groups[1] == 0) return hipSuccess;
-  const dim3 grid(groups[0] + groups[1]);
-  if (p.rot.interleaved)
-    hipLaunchKernelGGL((norm_rope_back_kernel<LR, true>), grid, dim3(kThreads), 0, stream, p,
-                       groups[0], groups[1]);
-  else
-    hipLaunchKernelGGL((norm_rope_back_kernel<LR, false>), grid, dim3(kThreads), 0, stream, p,
-                       groups[0], groups[1]);
-  return hipGetLastError();
+  const uint64_t rows = static_cast<uint64_t>(p.tokens) * (p.heads[0] + p.heads[1]);
+  return rows >= kManyRows ? launch_backward_u<LR, 4>(p, stream) : launch_backward_u<LR, 1>(p, stream);
 }
 
 }  // namespace
