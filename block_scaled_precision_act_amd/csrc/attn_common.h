@@ -29,20 +29,32 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// Called by every thread of a workgroup once its stores of a partial result are issued: makes
-// them visible to the whole device and counts the workgroup in at `counter`.  Returns (to every
-// thread) whether it is the last of `expected`; the last one then sees what all others stored,
-// and has put the counter back to zero.
-//   (1) Every wavefront waits until its own stores are complete; (2) past the barrier the whole
-//   workgroup's are; (3) thread 0's device-scope release writes them back past this XCD's L2
-//   before its arrival can be seen; (4) the last arrival's acquire drops what this XCD's caches
-//   may hold stale, before the barrier lets any thread load.
+// Stores of partial results that other workgroups will read: device scope, so they are written
+// through this XCD's L2 to where every XCD sees them.  (Plain stores would need the L2 written back
+// before the handoff, and that L2 also holds whatever else the kernel writes: with the gradients of
+// 16384 x 40 heads in it, 1024 workgroups' write-backs cost 44 us.)
+__device__ __forceinline__ void store_shared(float* p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void store_shared4(float* p, float a, float b, float c, float d) {
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  __hip_atomic_store(q, __builtin_bit_cast(uint64_t, v2u{__float_as_uint(a), __float_as_uint(b)}),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(q + 1, __builtin_bit_cast(uint64_t, v2u{__float_as_uint(c), __float_as_uint(d)}),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Called by every thread of a workgroup once it has stored its partial results with the functions
+// above: counts the workgroup in at `counter`.  Returns (to every thread) whether it is the last of
+// `expected`; the last one then sees what all others stored, and has put the counter back to zero.
+//   (1) Every wavefront waits until its own stores are complete (written through); (2) past the
+//   barrier the whole workgroup's are, so they precede thread 0's arrival; (3) the last arrival's
+//   acquire drops what this XCD's caches may hold stale, before the barrier lets any thread load.
 __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t expected, uint32_t* flag) {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
   __builtin_amdgcn_s_waitcnt(kVmcntZero);
   __syncthreads();
   if (threadIdx.x == 0) {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    __builtin_amdgcn_s_waitcnt(kVmcntZero);
     const uint32_t n = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED,
                                               __HIP_MEMORY_SCOPE_AGENT);
     const bool last = n + 1 == expected;

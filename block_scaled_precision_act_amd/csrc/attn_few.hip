@@ -420,11 +420,10 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
         } else {
 #pragma unroll
           for (int e = 0; e < EPL; e += 4)
-            *reinterpret_cast<float4*>(part + r * D + od + e) =
-                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            store_shared4(part + r * D + od + e, o[e], o[e + 1], o[e + 2], o[e + 3]);
           if ((tid & 15) == 0) {
-            part[RB * D + r] = mm;
-            part[RB * D + RB + r] = ll;
+            store_shared(part + RB * D + r, mm);
+            store_shared(part + RB * D + RB + r, ll);
           }
         }
       }

@@ -304,11 +304,11 @@ __global__ __launch_bounds__(kThreads) void attn_many_kernel(const AttnProblem p
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int i = 0; i < 16; i += 4)
-      *reinterpret_cast<float4*>(mine + ((d * 4 + i / 4) * kThreads + tid) * 4) =
-          make_float4(acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]);
+      store_shared4(mine + ((d * 4 + i / 4) * kThreads + tid) * 4, acc[d][i], acc[d][i + 1],
+                    acc[d][i + 2], acc[d][i + 3]);
   if (hh == 0) {
-    mine[kRows * D + wave * 32 + c] = m;
-    mine[kRows * D + kRows + wave * 32 + c] = l;
+    store_shared(mine + kRows * D + wave * 32 + c, m);
+    store_shared(mine + kRows * D + kRows + wave * 32 + c, l);
   }
   if (!arrive_last(p.counters + unit, static_cast<uint32_t>(parts), &flag)) return;
   m = -kInf;

@@ -238,7 +238,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRope
     float v = 0.f;
 #pragma unroll 8
     for (int g = 0; g < RG; ++g) v += sums[g * D + threadIdx.x];
-    parts[threadIdx.x] = v;
+    store_shared(parts + threadIdx.x, v);
   }
   if (!arrive_last(p.counters + i, groups, &flag)) return;
   // The last workgroup: D / 4 lanes by kThreads * 4 / D runs of partials, then the runs' sums.
@@ -283,14 +283,14 @@ hipError_t launch_forward(const NormRopeProblem& p, hipStream_t stream) {
 template <int LR, int U>
 hipError_t launch_backward_u(const NormRopeBackProblem& p, hipStream_t stream) {
   constexpr uint64_t RG = kThreads / LR;
-  // Workgroups in proportion to the rows, no more than there are runs of RG units; one for a
+  // Workgroups in proportion to the rows, each owner with two units at least; one for a
   // weight gradient without rows, which it writes as zero.
   uint32_t groups[2];
   const uint64_t heads = p.heads[0] + p.heads[1];
   for (int i = 0; i < 2; ++i) {
     const uint64_t units = static_cast<uint64_t>(p.tokens) * ((p.heads[i] + U - 1) / U);
     const uint64_t share = heads ? (kNormBackGroups - 1) * p.heads[i] / heads : 0;
-    const uint64_t most = (units + RG - 1) / RG;
+    const uint64_t most = (units + 2 * RG - 1) / (2 * RG);
     groups[i] = static_cast<uint32_t>(most < share ? most : share);
     if (groups[i] == 0 && (units > 0 || p.dweight[i])) groups[i] = 1;
   }
