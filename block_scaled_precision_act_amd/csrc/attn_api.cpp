@@ -4,6 +4,7 @@
 #include "attn_internal.h"
 #include "mx_internal.h"
 
+#include <cfloat>
 #include <cmath>
 
 namespace {
@@ -267,7 +268,7 @@ int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
       a->q_heads % c.kv_heads != 0 || !fits31(a->total_q, a->q_heads) ||
       !fits31(a->max_q, a->q_heads) || !fits31(a->batch, c.kv_heads) || a->table_width < 0 ||
       a->window < 0 || a->window > kMax31 || (a->window > 0 && !a->causal) ||
-      !std::isfinite(a->scale))
+      !(std::fabs(a->scale) < 1e30))
     return MX_ERR_SHAPE;
   if (!a->q_starts && a->total_q != a->batch * a->max_q) return MX_ERR_SHAPE;
   // Tokens a table row covers, and the exactness of the page number as a high product.
@@ -304,7 +305,11 @@ int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
   p.total_q = static_cast<int32_t>(a->total_q);
   p.max_q = static_cast<int32_t>(a->max_q);
   p.group = static_cast<int32_t>(a->q_heads / c.kv_heads);
-  p.scale_log2 = static_cast<float>(a->scale * 1.4426950408889634);
+  // A scale of zero becomes the smallest normal number: every finite score still counts as zero, and
+  // the -infinity of a masked one stays what it is.
+  p.scale_log2 = static_cast<float>(std::fabs(a->scale) * 1.4426950408889634);
+  if (p.scale_log2 < FLT_MIN) p.scale_log2 = FLT_MIN;
+  p.flip = a->scale < 0 ? 0x80008000u : 0u;
   p.causal = a->causal != 0;
   p.window = static_cast<int32_t>(a->window);
   p.counters = static_cast<uint32_t*>(a->workspace);

@@ -29,6 +29,50 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
+template <int V>
+struct IntC { static constexpr int value = V; };
+
+// 8 E2M1 codes times the scale -> 8 bf16, exact.
+__device__ __forceinline__ uint4 decode8(uint32_t d, float s) {
+  return make_uint4(
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 1)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3)));
+}
+
+// Byte `a` (0..3, constant after unrolling) of d: two codes times the scale -> two bf16.
+__device__ __forceinline__ uint32_t decode2(uint32_t d, float s, int a) {
+  return __builtin_bit_cast(uint32_t, a == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0)
+                                      : a == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 1)
+                                      : a == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2)
+                                               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3));
+}
+
+// v_perm selectors: the low (high) halves of (second, first) operand, first in the low half.
+constexpr uint32_t kLowHalves = 0x05040100u, kHighHalves = 0x07060302u;
+
+// Reads an int32 that no kernel writes meanwhile (a scalar load where the index is uniform).
+typedef const __attribute__((address_space(4))) int32_t* ConstInts;
+
+__device__ __forceinline__ int32_t read_uniform(const int32_t* p, int64_t i) {
+  return reinterpret_cast<ConstInts>(reinterpret_cast<uintptr_t>(p))[i];
+}
+
+// The larger of the lane's value and that of the lane 32 away (every lane active).
+__device__ __forceinline__ float max_halves(float v) {
+  const v2u r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Workgroup barrier for data passed through LDS: waits for the wavefront's LDS accesses only, so
+// loads from memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Stores of partial results that other workgroups will read: device scope, so they are written
 // through this XCD's L2 to where every XCD sees them.  (Plain stores would need the L2 written back
 // before the handoff, and that L2 also holds whatever else the kernel writes: with the gradients of

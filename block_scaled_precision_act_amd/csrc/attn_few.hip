@@ -24,12 +24,6 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = 4, kWaveTokens = 32, kTile = kWaves * kWaveTokens;
 
-typedef const __attribute__((address_space(4))) int32_t* ConstInts;
-
-__device__ __forceinline__ int32_t read_uniform(const int32_t* p, int64_t i) {
-  return reinterpret_cast<ConstInts>(reinterpret_cast<uintptr_t>(p))[i];
-}
-
 // One sequence's rows and keys.
 struct Sequence {
   int32_t len, rows, q0, n;    // cached tokens; query rows (n queries x group); first query
@@ -154,8 +148,11 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
                             static_cast<int64_t>(h * p.group + hg) * p.q.head_stride + g * (D / 4);
 #pragma unroll
       for (int s = 0; s < KS; ++s)
-        qf[mt][s] = __builtin_bit_cast(
-            bf16x8, live ? *reinterpret_cast<const uint4*>(row + 8 * s) : make_uint4(0, 0, 0, 0));
+      {
+        uint4 w = live ? *reinterpret_cast<const uint4*>(row + 8 * s) : make_uint4(0, 0, 0, 0);
+        w.x ^= p.flip; w.y ^= p.flip; w.z ^= p.flip; w.w ^= p.flip;
+        qf[mt][s] = __builtin_bit_cast(bf16x8, w);
+      }
     }
     // Tokens below `full_hi` and from `full_lo` on are seen by every row.
     const int32_t full_hi = p.causal ? min(first + 1, sq.len) : sq.len;
@@ -243,12 +240,7 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
           const uint32_t byte = D == 256 ? (w.ks[t] >> (j < 4 ? 0 : 8)) & 0xFFu : w.ks[t];
           const float sc = __uint_as_float(byte << 23);
           const uint32_t d = w.k[t][j];
-          const uint4 o = make_uint4(
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 0)),
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 1)),
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 2)),
-              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 3)));
-          const bf16x8 kf = __builtin_bit_cast(bf16x8, o);
+          const bf16x8 kf = __builtin_bit_cast(bf16x8, decode8(d, sc));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
             s[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[mt][j], s[mt][t], 0, 0, 0);
@@ -311,19 +303,12 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
       auto value_pair = [&](int a) {           // head values 2 a and 2 a + 1 of the lane's EPL
         uint32_t pr[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t d = w.v[i][a >> 2];
-          const bf16x2 r = (a & 3) == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, vsc[i], 0)
-                           : (a & 3) == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, vsc[i], 1)
-                           : (a & 3) == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, vsc[i], 2)
-                                          : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, vsc[i], 3);
-          pr[i] = __builtin_bit_cast(uint32_t, r);
-        }
+        for (int i = 0; i < 8; ++i) pr[i] = decode2(w.v[i][a >> 2], vsc[i], a & 3);
         v4u lo, hi;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          lo[i] = __builtin_amdgcn_perm(pr[2 * i + 1], pr[2 * i], 0x05040100u);
-          hi[i] = __builtin_amdgcn_perm(pr[2 * i + 1], pr[2 * i], 0x07060302u);
+          lo[i] = __builtin_amdgcn_perm(pr[2 * i + 1], pr[2 * i], kLowHalves);
+          hi[i] = __builtin_amdgcn_perm(pr[2 * i + 1], pr[2 * i], kHighHalves);
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {

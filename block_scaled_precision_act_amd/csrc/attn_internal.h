@@ -77,7 +77,8 @@ struct AttnProblem {
   int32_t table_width;
   uint32_t page_div;         // ceil(2^32 / (page_size / 16)): n / (page_size / 16) as a high product
   int32_t batch, total_q, max_q, group;
-  float scale_log2;          // scale * log2(e)
+  float scale_log2;          // |scale| * log2(e), at least the smallest normal fp32
+  uint32_t flip;             // 0x80008000 where scale < 0: the queries' signs are turned instead
   bool causal;
   int32_t window;
   uint32_t* counters;        // one per (sequence, key/value head) (and row block), zero between calls
@@ -88,7 +89,7 @@ struct AttnProblem {
 // head are its (query, grouped head) pairs, max_q * group of them at most.
 struct AttnPlan {
   bool few;                  // few rows: the cache is what costs (attn_few.hip), else attn_many.hip
-  int row_tiles;             // few: 16-row tiles held at once (1, 2 or 4)
+  int row_tiles;             // of a workgroup: 16-row tiles (few), wavefronts of 32 rows (many)
   int groups;                // few: workgroups that the cached tokens are dealt to
   int row_blocks, splits;    // many: blocks of rows for each (sequence, head), parts of the keys
   int64_t counter_bytes, bytes;

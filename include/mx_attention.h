@@ -160,6 +160,7 @@ int mx_kv_append_fp4(const mx_kv_append_fp4_args* args, void* stream);
  *   lse (or NULL) = ln sum_t exp(s_t), fp32 [total_q, q_heads].
  * A query that sees no key gets zeros and lse -infinity.  What lies in the cache beyond a
  * sequence's length is never used, whatever its bytes.
+ * |scale| must be below 1e30.
  * seq_lens, q_starts and page_table entries are read on the device: lengths are clamped to what
  * the table covers, and an entry outside [0, pages) reads page 0 instead of memory that is not
  * the cache's.
