@@ -285,6 +285,9 @@ int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
     return st;
   const mx::AttnPlan plan = mx::plan_attn(a->batch, a->max_q, a->q_heads, c.kv_heads,
                                           static_cast<int>(c.head_dim));
+  // The deal of tiles of 128 tokens (plus a few slots for each sequence and head) counts in 31 bits.
+  if (plan.few && !fits31(a->batch * c.kv_heads, a->table_width * c.page_size / 128 + 8))
+    return MX_ERR_SHAPE;
   if (plan.bytes > 0 && (!a->workspace || a->workspace_bytes < plan.bytes ||
                          !aligned(a->workspace, 256)))
     return MX_ERR_WORKSPACE;

@@ -59,6 +59,19 @@ __device__ __forceinline__ int32_t read_uniform(const int32_t* p, int64_t i) {
   return reinterpret_cast<ConstInts>(reinterpret_cast<uintptr_t>(p))[i];
 }
 
+// The scale in a byte of `word`, for the scaled conversions: they read a scale's exponent field alone
+// (its sign and mantissa bits change nothing, checked for every byte and code), so rotating the word
+// right by 9 + 8 * byte is enough.
+__device__ __forceinline__ float scale_of_byte(uint32_t word, uint32_t turn) {
+  return __uint_as_float(__builtin_amdgcn_alignbit(word, word, turn));
+}
+
+// The largest of the values of lanes that differ in bit 4 (every lane active).
+__device__ __forceinline__ float max_rows(float v) {
+  const v2u r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // The larger of the lane's value and that of the lane 32 away (every lane active).
 __device__ __forceinline__ float max_halves(float v) {
   const v2u r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);

@@ -13,9 +13,10 @@
 // (value pairs) and regroups the halves by v_perm.  Nothing passes through LDS in the loop.
 // Codes are decoded exactly (v_cvt_scalef32_pk_bf16_fp4 applies the E8M0 scale).
 //
-// The cached tokens of all sequences and heads are laid end to end in tiles of 128 and dealt in
-// equal runs to a fixed number of workgroups, from the lengths on the device, so ragged batches are
-// balanced and one long sequence fills the chip.  A sequence and head that a run's end cuts leaves
+// The cached tokens of all sequences and heads are laid end to end in tiles of 128, with a few empty
+// slots before each sequence and head for what it costs beside its tokens, and dealt in equal runs to
+// a fixed number of workgroups, from the lengths on the device: ragged batches are balanced and one
+// long sequence fills the chip.  A sequence and head that a run's end cuts leaves
 // partial (m, sum, O) in the workspace; the last of its workgroups to arrive joins them, in order.
 #include "attn_common.h"
 
@@ -53,85 +54,159 @@ __device__ __forceinline__ Sequence sequence(const AttnProblem& p, int32_t b) {
   return s;
 }
 
-// What a wavefront loads for 32 tokens, undecoded.
+// What a lane holds of 32 tokens, undecoded.
 template <int D>
-struct Raw {
-  static constexpr int KW = D / 32, VW = D <= 128 ? 1 : 2, SW = D == 64 ? 2 : 4;
-  uint32_t k[2][KW];      // per 16 tokens: the lane's D / 4 codes of token lane % 16
-  uint32_t ks[2];         // their scale byte(s)
-  uint32_t v[8][VW];      // D / 16 codes of the lane's 8 tokens
-  uint32_t vs[2][SW];     // words that hold their scale bytes
+struct RawKeys {
+  uint32_t k[2][D / 32];  // per 16 tokens: D / 4 codes of token lane % 16
+  uint32_t s[2];          // their scale byte(s)
+};
+template <int D>
+struct RawValues {
+  uint32_t v[8][D <= 128 ? 1 : 2];   // D / 16 codes of the lane's 8 tokens
+  uint32_t s[2][D == 64 ? 2 : 4];    // words that hold their scale bytes
 };
 
+struct Places {           // where the two 16-token steps of 32 tokens lie: pages and first tokens
+  uint32_t id[2], off[2];
+};
+
+// Loads codes, which are read once: past the caches (4 x 131073 tokens: 106 us, 113 us without).
+template <class T>
+__device__ __forceinline__ T stream(const uint8_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+}
+
+// exp2(m - now), and 0 where nothing was seen yet (m = -infinity).
+__device__ __forceinline__ float weight_of(float m, float now) {
+  return m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
+}
+
+// What a sequence and head costs beside its tiles (queries, joins, latencies), counted in tiles.
+constexpr uint32_t kUnitSlots = 2;
+
+// What joining one part costs, counted in tiles: a sequence and head of n tiles cut into runs of s
+// takes about s + kJoinCost * n / s, least at s = sqrt(kJoinCost * n), so runs are no shorter.
+constexpr float kJoinCost = 0.2f;
+
+// The slots of a sequence: for each head, kUnitSlots and its tiles.
+__device__ __forceinline__ uint32_t slots(const Sequence& s, int heads) {
+  return s.tiles ? (static_cast<uint32_t>(s.tiles) + kUnitSlots) * heads : 0u;
+}
+
+// Inclusive prefix sum over the wavefront.
+__device__ __forceinline__ uint32_t prefix_sum(uint32_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v = max(v, static_cast<uint32_t>(__shfl_xor(v, d, 64)));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
 template <int D, int MT>
-__global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p) {
+__global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(const AttnProblem p) {
   constexpr int KS = D / 32;               // k steps of a score product
   constexpr int EPL = D / 16;              // head values a lane decodes of a token's value row
   constexpr int PAD = D + 4;
   __shared__ float obuf[kWaves][16][PAD];
   __shared__ float mbuf[kWaves][16], lbuf[kWaves][16];
-  __shared__ uint32_t scan[kThreads / 64 + 2];
+  __shared__ uint32_t scan[2 * kWaves + 2];
   __shared__ uint32_t flag;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int heads = static_cast<int>(p.cache.heads);
+  // Rotation that brings the byte of the lane's head values to a scale's exponent field.
+  const uint32_t turn_vs = 9 + 8 * (D == 64 ? c >> 3 : D == 128 ? c >> 2 : (c >> 1) & 3);
 
-  // This workgroup's run of tiles: a prefix sum of the sequences' tiles, each thread a run of
-  // sequences.
-  const int seg = (p.batch + kThreads - 1) / kThreads;
-  uint32_t mine = 0;
-  for (int i = 0; i < seg; ++i) {
-    const int b = tid * seg + i;
-    if (b < p.batch) mine += static_cast<uint32_t>(sequence(p, b).tiles * heads);
-  }
-  uint32_t incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint32_t o = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 63) scan[wave] = incl;
-  __syncthreads();
-  uint32_t before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += scan[w];
-    total += scan[w];
-  }
-  const uint32_t share = max(1u, (total + gridDim.x - 1) / gridDim.x);
-  const uint32_t start = blockIdx.x * share, end = min(start + share, total);
-  if (start >= total) return;
-  const uint32_t excl = before + incl - mine;
-  if (start >= excl && start < excl + mine) {
-    uint32_t at = excl;
-    int b = tid * seg;
-    for (;;) {
-      const uint32_t n = static_cast<uint32_t>(sequence(p, b).tiles * heads);
-      if (start < at + n) break;
-      at += n;
-      ++b;
+  // This workgroup's run of slots: a prefix sum over the sequences' slots finds the sequence that its
+  // run begins in (b) and that sequence's first slot (base).
+  uint32_t total, longest, base;           // all slots; the most of one sequence and head
+  int b;
+  auto share_of = [&]() {
+    const uint32_t even = (total + gridDim.x - 1) / gridDim.x;
+    const float least = __builtin_sqrtf(kJoinCost * static_cast<float>(longest));
+    return max(max(even, 1u), static_cast<uint32_t>(least));
+  };
+  if (p.batch <= 64) {                     // a lane each, every wavefront for itself
+    const Sequence s = sequence(p, min(lane, p.batch - 1));
+    const uint32_t mine = lane < p.batch ? slots(s, heads) : 0u;
+    const uint32_t incl = prefix_sum(mine);
+    total = __builtin_amdgcn_readlane(incl, 63);
+    longest = wave_max(static_cast<uint32_t>(s.tiles));
+    const uint32_t start = blockIdx.x * share_of();
+    if (start >= total) return;
+    b = __builtin_ctzll(__ballot(start < incl));
+    base = __builtin_amdgcn_readlane(incl - mine, b);
+  } else {                                 // a thread for each run of sequences
+    const int seg = (p.batch + kThreads - 1) / kThreads;
+    uint32_t mine = 0, most = 0;
+    for (int i = 0; i < seg; ++i) {
+      if (tid * seg + i >= p.batch) break;
+      const Sequence s = sequence(p, tid * seg + i);
+      mine += slots(s, heads);
+      most = max(most, static_cast<uint32_t>(s.tiles));
     }
-    scan[kWaves] = static_cast<uint32_t>(b);
-    scan[kWaves + 1] = at;
+    const uint32_t incl = prefix_sum(mine);
+    most = wave_max(most);
+    if (lane == 63) {
+      scan[wave] = incl;
+      scan[kWaves + wave] = most;
+    }
+    __syncthreads();
+    uint32_t excl = incl - mine;
+    total = longest = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) excl += scan[w];
+      total += scan[w];
+      longest = max(longest, scan[kWaves + w]);
+    }
+    total = __builtin_amdgcn_readfirstlane(total);
+    longest = __builtin_amdgcn_readfirstlane(longest);
+    const uint32_t start = blockIdx.x * share_of();
+    if (start >= total) return;
+    if (start >= excl && start < excl + mine) {
+      int i = tid * seg;
+      for (;;) {
+        const uint32_t n = slots(sequence(p, i), heads);
+        if (start < excl + n) break;
+        excl += n;
+        ++i;
+      }
+      scan[2 * kWaves] = static_cast<uint32_t>(i);
+      scan[2 * kWaves + 1] = excl;
+    }
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(static_cast<int>(scan[2 * kWaves]));
+    base = __builtin_amdgcn_readfirstlane(static_cast<int>(scan[2 * kWaves + 1]));
   }
-  __syncthreads();
-  int b = __builtin_amdgcn_readfirstlane(static_cast<int>(scan[kWaves]));
-  uint32_t base = __builtin_amdgcn_readfirstlane(static_cast<int>(scan[kWaves + 1]));
-  uint32_t at = start;
+  const uint32_t share = share_of();
+  uint32_t at = blockIdx.x * share;
+  const uint32_t end = min(at + share, total);
 
   while (at < end) {
     const Sequence sq = sequence(p, b);
-    const uint32_t seq_tiles = static_cast<uint32_t>(sq.tiles) * heads;
-    if (at - base >= seq_tiles) {            // also a sequence without rows
-      base += seq_tiles;
+    const uint32_t per = static_cast<uint32_t>(sq.tiles) + kUnitSlots, all = slots(sq, heads);
+    if (at - base >= all) {                  // also a sequence without rows
+      base += all;
       ++b;
       continue;
     }
-    const int h = static_cast<int>((at - base) / sq.tiles);
-    const uint32_t unit0 = base + static_cast<uint32_t>(h) * sq.tiles;
-    const int tile0 = static_cast<int>(at - unit0);
-    const int ntiles = min(sq.tiles - tile0, static_cast<int>(end - at));
+    const int h = static_cast<int>((at - base) / per);
+    const uint32_t unit0 = base + static_cast<uint32_t>(h) * per;
+    const uint32_t s0 = at - unit0, s1 = min(per, end - unit0);
+    const int tile0 = static_cast<int>(max(s0, kUnitSlots) - kUnitSlots);
+    const int ntiles = static_cast<int>(max(s1, kUnitSlots) - kUnitSlots) - tile0;
+    at = unit0 + s1;
+    if (ntiles == 0) continue;
 
     // Query rows, as B operands: lane (c, g) holds row c's values [g D/4, (g+1) D/4).
     bf16x8 qf[MT][KS];
@@ -147,8 +222,7 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
       const uint16_t* row = p.q.p + static_cast<int64_t>(sq.q0 + tok) * p.q.token_stride +
                             static_cast<int64_t>(h * p.group + hg) * p.q.head_stride + g * (D / 4);
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
-      {
+      for (int s = 0; s < KS; ++s) {
         uint4 w = live ? *reinterpret_cast<const uint4*>(row + 8 * s) : make_uint4(0, 0, 0, 0);
         w.x ^= p.flip; w.y ^= p.flip; w.z ^= p.flip; w.w ^= p.flip;
         qf[mt][s] = __builtin_bit_cast(bf16x8, w);
@@ -176,100 +250,110 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
     const uint8_t* const vsh = p.cache.vs + h * p.cache.scale_head;
     const uint32_t page16 = p.cache.page_size >> 4;
 
-    auto load = [&](Raw<D>& w, int32_t tok0) {
+    auto place = [&](int32_t tok0) {
+      Places at;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint32_t t16 = static_cast<uint32_t>(min((tok0 >> 4) + s, last16));
         const uint32_t page = p.page_div ? __umulhi(t16, p.page_div) : t16;
-        const uint32_t off = (t16 - page * page16) * 16u;
-        uint32_t id = static_cast<uint32_t>(read_uniform(p.table, trow + page));
-        id = id < p.cache.pages ? id : 0u;
-        const int64_t cb = id * p.cache.code_page + off * (D / 2);
-        const int64_t sb = id * p.cache.scale_page + off * (D / 32);
-        const uint8_t* const kp = kh + cb;
-        const uint8_t* const vp = vh + cb;
-        const uint8_t* const ksp = ksh + sb;
-        const uint8_t* const vsp = vsh + sb;
-        const uint32_t ko = c * (D / 2) + g * (D / 8);
+        const uint32_t id = static_cast<uint32_t>(read_uniform(p.table, trow + page));
+        at.id[s] = id < p.cache.pages ? id : 0u;
+        at.off[s] = (t16 - page * page16) * 16u;
+      }
+      return at;
+    };
+    auto load_keys = [&](RawKeys<D>& w, const Places& at) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint8_t* const kp = kh + (at.id[s] * p.cache.code_page + at.off[s] * (D / 2)) +
+                                  (c * (D / 2) + g * (D / 8));
+        const uint8_t* const sp = ksh + (at.id[s] * p.cache.scale_page + at.off[s] * (D / 32)) +
+                                  (c * (D / 32) + g * (D / 32) / 4);
         if constexpr (D == 64) {
-          const uint2 t = *reinterpret_cast<const uint2*>(kp + ko);
-          w.k[s][0] = t.x; w.k[s][1] = t.y;
-          w.ks[s] = ksp[c * 2 + (g >> 1)];
+          const v2u t = stream<v2u>(kp);
+          w.k[s][0] = t[0]; w.k[s][1] = t[1];
         } else {
 #pragma unroll
           for (int i = 0; i < D / 128; ++i) {
-            const uint4 t = *reinterpret_cast<const uint4*>(kp + ko + 16 * i);
-            w.k[s][4 * i] = t.x; w.k[s][4 * i + 1] = t.y;
-            w.k[s][4 * i + 2] = t.z; w.k[s][4 * i + 3] = t.w;
+            const v4u t = stream<v4u>(kp + 16 * i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w.k[s][4 * i + e] = t[e];
           }
-          if constexpr (D == 128) w.ks[s] = ksp[c * 4 + g];
-          else w.ks[s] = *reinterpret_cast<const uint16_t*>(ksp + c * 8 + g * 2);
         }
+        if constexpr (D == 256) w.s[s] = *reinterpret_cast<const uint16_t*>(sp);
+        else w.s[s] = *sp;
+      }
+    };
+    auto load_values = [&](RawValues<D>& w, const Places& at) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint8_t* const vp = vh + (at.id[s] * p.cache.code_page + at.off[s] * (D / 2)) +
+                                  (g * 4 * (D / 2) + c * (D / 32));
+        const uint8_t* const sp = vsh + (at.id[s] * p.cache.scale_page + at.off[s] * (D / 32)) +
+                                  g * 4 * (D / 32);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint8_t* a = vp + (g * 4 + i) * (D / 2) + c * (D / 32);
-          if constexpr (D == 64) w.v[4 * s + i][0] = *reinterpret_cast<const uint16_t*>(a);
-          if constexpr (D == 128) w.v[4 * s + i][0] = *reinterpret_cast<const uint32_t*>(a);
+          const uint8_t* a = vp + i * (D / 2);
+          if constexpr (D == 64) w.v[4 * s + i][0] = stream<uint16_t>(a);
+          if constexpr (D == 128) w.v[4 * s + i][0] = stream<uint32_t>(a);
           if constexpr (D == 256) {
-            const uint2 t = *reinterpret_cast<const uint2*>(a);
-            w.v[4 * s + i][0] = t.x; w.v[4 * s + i][1] = t.y;
+            const v2u t = stream<v2u>(a);
+            w.v[4 * s + i][0] = t[0]; w.v[4 * s + i][1] = t[1];
           }
         }
         if constexpr (D == 64) {
-          const uint2 t = *reinterpret_cast<const uint2*>(vsp + g * 8);
-          w.vs[s][0] = t.x; w.vs[s][1] = t.y;
+          const uint2 t = *reinterpret_cast<const uint2*>(sp);
+          w.s[s][0] = t.x; w.s[s][1] = t.y;
         } else if constexpr (D == 128) {
-          const uint4 t = *reinterpret_cast<const uint4*>(vsp + g * 16);
-          w.vs[s][0] = t.x; w.vs[s][1] = t.y; w.vs[s][2] = t.z; w.vs[s][3] = t.w;
+          const uint4 t = *reinterpret_cast<const uint4*>(sp);
+          w.s[s][0] = t.x; w.s[s][1] = t.y; w.s[s][2] = t.z; w.s[s][3] = t.w;
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            w.vs[s][i] = *reinterpret_cast<const uint32_t*>(vsp + (g * 4 + i) * 8 + (c >> 3) * 4);
+            w.s[s][i] = *reinterpret_cast<const uint32_t*>(sp + i * 8 + (c >> 3) * 4);
         }
       }
     };
 
-    auto compute = [&](const Raw<D>& w, int32_t tok0) {
+    // 32 tokens from tok0; what was loaded for them is replaced by the loads of `next` as soon as it
+    // is decoded.
+    auto step = [&](RawKeys<D>& rk, RawValues<D>& rv, int32_t tok0, const Places& next, bool more) {
       v4f s[MT][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) s[mt][t] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
         for (int j = 0; j < KS; ++j) {
-          const uint32_t byte = D == 256 ? (w.ks[t] >> (j < 4 ? 0 : 8)) & 0xFFu : w.ks[t];
-          const float sc = __uint_as_float(byte << 23);
-          const uint32_t d = w.k[t][j];
-          const bf16x8 kf = __builtin_bit_cast(bf16x8, decode8(d, sc));
+          const float sc = __uint_as_float((D == 256 && j >= 4 ? rk.s[t] >> 8 : rk.s[t]) << 23);
+          const bf16x8 kf = __builtin_bit_cast(bf16x8, decode8(rk.k[t][j], sc));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-            s[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[mt][j], s[mt][t], 0, 0, 0);
+            s[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[mt][j], j == 0 ? v4f(0.f) : s[mt][t],
+                                                               0, 0, 0);
         }
       }
-      const bool edge = tok0 + kWaveTokens > full_hi || tok0 < full_lo;
-      bf16x8 pf[MT];
+      if (more) load_keys(rk, next);
+      if (tok0 + kWaveTokens > full_hi || tok0 < full_lo) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = s[mt][i >> 2][i & 3] * p.scale_log2;
-        if (edge) {
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int32_t t = tok0 + (i >> 2) * 16 + g * 4 + (i & 3);
-            x[i] = t < hi_row[mt] && t >= lo_row[mt] ? x[i] : -kInf;
+            if (t >= hi_row[mt] || t < lo_row[mt]) s[mt][i >> 2][i & 3] = -kInf;
           }
-        }
-        float top = x[0];
+        __builtin_amdgcn_sched_barrier(0);        // keeps the masks a branch
+      }
+      bf16x8 pf[MT];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
+      for (int mt = 0; mt < MT; ++mt) {
+        float top = s[mt][0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, s[mt][i >> 2][i & 3]);
+        top = max_halves(max_rows(top)) * p.scale_log2;
         // The maximum that is subtracted moves only when some row's rose by more than 2^8: until
         // then weights stay below 2^8, and bf16 and fp32 hold them as well as those below one.
         if (__any(top > m[mt] + 8.f)) {
           const float now = fmaxf(m[mt], top);
-          const float f = m[mt] == -kInf ? 0.f : __builtin_amdgcn_exp2f(m[mt] - now);
+          const float f = weight_of(m[mt], now);
           m[mt] = now;
           l[mt] *= f;
 #pragma unroll
@@ -278,32 +362,34 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
             for (int i = 0; i < 4; ++i) acc[mt][e][i] *= f;
         }
         const float sub = m[mt] == -kInf ? 0.f : m[mt];
-        float w8[8];
+        float w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          w8[i] = __builtin_amdgcn_exp2f(x[i] - sub);
-          l[mt] += w8[i];
+          w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][i >> 2][i & 3], p.scale_log2, -sub));
+          l[mt] += w[i];
         }
-        pf[mt] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16(w8[0], w8[1]), pack_bf16(w8[2], w8[3]),
-                                                       pack_bf16(w8[4], w8[5]), pack_bf16(w8[6], w8[7])));
+        pf[mt] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]),
+                                                       pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])));
       }
-      // The values' scales; what lies past the keys is given scale 1: finite, and its weight is 0.
+      // The values' scales: the scaled conversions read a scale's exponent field alone, so the word is
+      // rotated until the lane's byte lies there.  What lies past the keys is given scale 1: finite,
+      // and its weight is 0.
       float vsc[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int sh = D == 64 ? 8 * (c >> 3) + 16 * (i & 1) : D == 128 ? 8 * (c >> 2) : 8 * ((c >> 1) & 3);
-        const uint32_t word = D == 64 ? w.vs[i >> 2][(i & 3) >> 1] : w.vs[i >> 2][i & 3];
-        vsc[i] = __uint_as_float(((word >> sh) & 0xFFu) << 23);
-      }
+      for (int i = 0; i < 8; ++i)
+        vsc[i] = scale_of_byte(D == 64 ? rv.s[i >> 2][(i & 3) >> 1] : rv.s[i >> 2][i & 3],
+                               D == 64 && (i & 1) ? turn_vs + 16 : turn_vs);
       if (tok0 + kWaveTokens > sq.hi) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (tok0 + (i >> 2) * 16 + g * 4 + (i & 3) >= sq.hi) vsc[i] = 1.f;
+        __builtin_amdgcn_sched_barrier(0);
       }
-      auto value_pair = [&](int a) {           // head values 2 a and 2 a + 1 of the lane's EPL
+#pragma unroll
+      for (int a = 0; a < EPL / 2; ++a) {        // head values 2 a and 2 a + 1 of the lane's EPL
         uint32_t pr[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) pr[i] = decode2(w.v[i][a >> 2], vsc[i], a & 3);
+        for (int i = 0; i < 8; ++i) pr[i] = decode2(rv.v[i][a >> 2], vsc[i], a & 3);
         v4u lo, hi;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -317,34 +403,30 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
           acc[mt][2 * a + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               __builtin_bit_cast(bf16x8, hi), pf[mt], acc[mt][2 * a + 1], 0, 0, 0);
         }
-      };
-#pragma unroll
-      for (int a = 0; a < EPL / 2; ++a) value_pair(a);
+      }
+      if (more) load_values(rv, next);
     };
 
     const int32_t tok_begin = sq.lo + tile0 * kTile + wave * kWaveTokens;
     const int32_t tok_end = min(sq.lo + (tile0 + ntiles) * kTile, sq.hi);
     if (tok_begin < tok_end) {
-      Raw<D> ra, rb;
-      load(ra, tok_begin);
-      for (int32_t t = tok_begin;;) {
-        int32_t nx = t + kTile;
-        if (nx < tok_end) load(rb, nx);
-        compute(ra, t);
-        if (nx >= tok_end) break;
-        t = nx;
-        nx = t + kTile;
-        if (nx < tok_end) load(ra, nx);
-        compute(rb, t);
-        if (nx >= tok_end) break;
-        t = nx;
+      RawKeys<D> rk;
+      RawValues<D> rv;
+      Places at = place(tok_begin);
+      load_keys(rk, at);
+      load_values(rv, at);
+      at = place(tok_begin + kTile);             // past the end: the last step's
+      for (int32_t t = tok_begin; t < tok_end; t += kTile) {
+        const Places next = place(t + 2 * kTile);
+        step(rk, rv, t, at, t + kTile < tok_end);
+        at = next;
       }
     }
 
     // Join the four wavefronts through LDS, 16 rows at a time; thread t then holds EPL values of
     // row t / 16.
     const bool whole = ntiles == sq.tiles;
-    const uint32_t wg0 = unit0 / share, wg1 = (unit0 + sq.tiles - 1) / share;
+    const uint32_t wg0 = (unit0 + kUnitSlots) / share, wg1 = (unit0 + per - 1) / share;
     constexpr int RB = MT * 16;
     constexpr int64_t kPart = static_cast<int64_t>(RB) * (D + 2);
     float* const part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (blockIdx.x == wg0)) * kPart;
@@ -379,7 +461,7 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
       }
       __syncthreads();
       const float mall = fmaxf(fmaxf(mbuf[0][c], mbuf[1][c]), fmaxf(mbuf[2][c], mbuf[3][c]));
-      const float f = m[mt] == -kInf ? 0.f : __builtin_amdgcn_exp2f(m[mt] - mall);
+      const float f = weight_of(m[mt], mall);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -394,7 +476,7 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
       for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, mbuf[w][orow]);
 #pragma unroll
       for (int w = 0; w < kWaves; ++w)
-        ll += lbuf[w][orow] * (mbuf[w][orow] == -kInf ? 0.f : __builtin_amdgcn_exp2f(mbuf[w][orow] - mm));
+        ll += lbuf[w][orow] * weight_of(mbuf[w][orow], mm);
 #pragma unroll
       for (int e = 0; e < EPL; ++e)
         o[e] = (obuf[0][orow][od + e] + obuf[1][orow][od + e]) +
@@ -414,40 +496,80 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(const AttnProblem p)
       }
       __syncthreads();
     }
-    if (!whole) {
-      const uint32_t count = wg1 - wg0 + 1;
-      if (arrive_last(p.counters + static_cast<int64_t>(b) * heads + h, count, &flag)) {
+    // The last workgroup to arrive joins the parts: its 16 lots of 16 threads take the tile's live
+    // rows, and the parts by turns where rows leave lots over; the lots of a row are then joined.
+    if (!whole && arrive_last(p.counters + (static_cast<int64_t>(b) * heads + h) * kCounterStride, wg1 - wg0 + 1, &flag)) {
+      const int lot = tid >> 4;
+      for (int mt = 0; mt < MT && mt * 16 < sq.rows; ++mt) {
+        const int live = min(16, sq.rows - mt * 16), turns = 16 / live;
+        const int turn = lot / live, r = mt * 16 + lot - turn * live;
+        float o[EPL], mm = -kInf, ll = 0.f;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int r = mt * 16 + orow;
-          if (r >= sq.rows) break;
-          float o[EPL], mm = -kInf, ll = 0.f;
+        for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+        if (turn < turns) {
+          constexpr int kBatch = D == 256 ? 4 : 8;
+          for (uint32_t w0 = wg0 + turn; w0 <= wg1; w0 += kBatch * turns) {
+            float pm[kBatch], pl[kBatch];
+            float4 v[kBatch][EPL / 4];
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-#pragma unroll 4
-          for (uint32_t w = wg0; w <= wg1; ++w) {
-            const float* src = p.parts + (2 * static_cast<int64_t>(w) + (w == wg0)) * kPart;
-            const float pm = src[RB * D + r], pl = src[RB * D + RB + r];
-            const float now = fmaxf(mm, pm);
-            const float fo = mm == -kInf ? 0.f : __builtin_amdgcn_exp2f(mm - now);
-            const float fn = pm == -kInf ? 0.f : __builtin_amdgcn_exp2f(pm - now);
+            for (int i = 0; i < kBatch; ++i) {     // past the last part: that part, with no weight
+              const uint32_t w = min(w0 + i * turns, wg1);
+              const float* src = p.parts + (2 * static_cast<int64_t>(w) + (w == wg0)) * kPart;
+              pm[i] = src[RB * D + r];
+              pl[i] = src[RB * D + RB + r];
+#pragma unroll
+              for (int e = 0; e < EPL / 4; ++e) v[i][e] = *reinterpret_cast<const float4*>(src + r * D + od + 4 * e);
+            }
+            float now = mm;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              if (w0 + i * turns > wg1) pm[i] = -kInf;
+              now = fmaxf(now, pm[i]);
+            }
+            const float fo = weight_of(mm, now);
             mm = now;
-            ll = ll * fo + pl * fn;
+            ll *= fo;
 #pragma unroll
-            for (int e = 0; e < EPL; e += 4) {
-              const float4 v = *reinterpret_cast<const float4*>(src + r * D + od + e);
-              o[e] = o[e] * fo + v.x * fn;
-              o[e + 1] = o[e + 1] * fo + v.y * fn;
-              o[e + 2] = o[e + 2] * fo + v.z * fn;
-              o[e + 3] = o[e + 3] * fo + v.w * fn;
+            for (int e = 0; e < EPL; ++e) o[e] *= fo;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              if (w0 + i * turns > wg1) break;
+              const float f = weight_of(pm[i], now);
+              ll += pl[i] * f;
+#pragma unroll
+              for (int e = 0; e < EPL / 4; ++e) {
+                o[4 * e] += v[i][e].x * f;
+                o[4 * e + 1] += v[i][e].y * f;
+                o[4 * e + 2] += v[i][e].z * f;
+                o[4 * e + 3] += v[i][e].w * f;
+              }
             }
           }
-          write_row(r, o, mm, ll);
         }
+        if (turns > 1) {
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) obuf[0][lot][od + e] = o[e];
+          if ((tid & 15) == 0) {
+            mbuf[0][lot] = mm;
+            lbuf[0][lot] = ll;
+          }
+          __syncthreads();
+          if (turn == 0) {
+            for (int i = 1; i < turns; ++i) {
+              const int other = lot + i * live;
+              const float pm = mbuf[0][other], now = fmaxf(mm, pm);
+              const float fo = weight_of(mm, now), fn = weight_of(pm, now);
+              mm = now;
+              ll = ll * fo + lbuf[0][other] * fn;
+#pragma unroll
+              for (int e = 0; e < EPL; ++e) o[e] = o[e] * fo + obuf[0][other][od + e] * fn;
+            }
+          }
+        }
+        if (turn == 0) write_row(r, o, mm, ll);
+        __syncthreads();
       }
-      __syncthreads();
     }
-    at += static_cast<uint32_t>(ntiles);
   }
 }
 

@@ -85,6 +85,9 @@ struct AttnProblem {
   float* parts;
 };
 
+// Counters lie a cache line apart: arrivals on neighbouring ones would pass one line around the XCDs.
+constexpr int kCounterStride = 32;
+
 // How a problem's rows are dealt out, by its sizes alone.  A sequence's rows for one key/value
 // head are its (query, grouped head) pairs, max_q * group of them at most.
 struct AttnPlan {
@@ -94,6 +97,10 @@ struct AttnPlan {
   int row_blocks, splits;    // many: blocks of rows for each (sequence, head), parts of the keys
   int64_t counter_bytes, bytes;
 };
+// Wavefronts of attn_few.hip that a SIMD holds (by their registers), and so workgroups a CU.
+constexpr int few_waves(int head_dim, int row_tiles) {
+  return head_dim * row_tiles <= 128 ? 3 : head_dim * row_tiles <= 256 ? 2 : 1;
+}
 AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim);
 
 hipError_t launch_attn_few(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream);

@@ -169,24 +169,25 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(co
   auto decode_keys = [&](const RawKeys<D>& w, uint4* dst) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const uint32_t byte = D == 256 ? (w.s >> (i < 4 ? 0 : 8)) & 0xFFu : w.s;
-      const float sc = __uint_as_float(byte << 23);
+      const float sc = __uint_as_float((D == 256 && i >= 4 ? w.s >> 8 : w.s) << 23);
       const int word = kq * (D / 32) + i;               // 8 codes: k step word / 2, half word % 2
       dst[((sub >> 1) * KS + (word >> 1)) * 64 + (word & 1) * 32 + (sub & 1) * 16 + k16] =
           decode8(w.k[i], sc);
     }
   };
   auto decode_values = [&](const RawValues<D>& w, int32_t t0, uint4* dst) {
+    const uint32_t turn = 9 + 8 * (D == 64 ? vc >> 4 : D == 128 ? vc >> 3 : (vc >> 2) & 3);
     float sc[8];
-    const bool tail = t0 + kTok > hi;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int sh = D == 64 ? 8 * (vc >> 4) + 16 * (i & 1) : D == 128 ? 8 * (vc >> 3) : 8 * ((vc >> 2) & 3);
-      const uint32_t word = D == 64 ? w.s[i >> 2][(i & 3) >> 1] : w.s[i >> 2][i & 3];
-      uint32_t e = (word >> sh) & 0xFFu;
-      // What lies past the keys is given scale 1: finite, and its weight is 0.
-      if (tail) e = t0 + sub * 16 + (i >> 2) * 8 + vh * 4 + (i & 3) >= hi ? 127u : e;
-      sc[i] = __uint_as_float(e << 23);
+    for (int i = 0; i < 8; ++i)
+      sc[i] = scale_of_byte(D == 64 ? w.s[i >> 2][(i & 3) >> 1] : w.s[i >> 2][i & 3],
+                            D == 64 && (i & 1) ? turn + 16 : turn);
+    // What lies past the keys is given scale 1: finite, and its weight is 0.
+    if (t0 + kTok > hi) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (t0 + sub * 16 + (i >> 2) * 8 + vh * 4 + (i & 3) >= hi) sc[i] = 1.f;
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int a = 0; a < EPI / 2; ++a) {
@@ -371,7 +372,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(co
     store_shared(mine + kRows * D + wave * 32 + c, m);
     store_shared(mine + kRows * D + kRows + wave * 32 + c, l);
   }
-  if (!arrive_last(p.counters + unit, static_cast<uint32_t>(parts), &flag)) return;
+  if (!arrive_last(p.counters + unit * kCounterStride, static_cast<uint32_t>(parts), &flag)) return;
   m = -kInf;
   l = 0.f;
 #pragma unroll
@@ -416,8 +417,8 @@ AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
   a.few = rows <= most;
   if (a.few) {
     a.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    a.groups = 512;
-    a.counter_bytes = (units * 4 + 255) / 256 * 256;
+    a.groups = 256 * few_waves(head_dim, a.row_tiles);
+    a.counter_bytes = (units * 4 * kCounterStride + 255) / 256 * 256;
     a.bytes = a.counter_bytes +
               2 * static_cast<int64_t>(a.groups) * 16 * a.row_tiles * (head_dim + 2) * 4;
     return a;
@@ -431,7 +432,7 @@ AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
   const int64_t fit = 512 / (blocks * units);
   a.splits = static_cast<int>(fit < 1 ? 1 : fit > 64 ? 64 : fit);
   if (a.splits > 1) {
-    a.counter_bytes = (blocks * units * 4 + 255) / 256 * 256;
+    a.counter_bytes = (blocks * units * 4 * kCounterStride + 255) / 256 * 256;
     a.bytes = a.counter_bytes +
               blocks * units * a.splits * block_rows * (head_dim + 2) * 4;
   }
