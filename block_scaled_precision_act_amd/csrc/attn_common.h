@@ -66,6 +66,15 @@ __device__ __forceinline__ float scale_of_byte(uint32_t word, uint32_t turn) {
   return __uint_as_float(__builtin_amdgcn_alignbit(word, word, turn));
 }
 
+// The value of lane `i` (0..3, constant after unrolling) of each group of four.
+__device__ __forceinline__ uint32_t quad_lane(uint32_t v, int i) {
+  const int x = static_cast<int>(v);
+  return static_cast<uint32_t>(i == 0   ? __builtin_amdgcn_mov_dpp(x, 0x00, 0xF, 0xF, false)
+                               : i == 1 ? __builtin_amdgcn_mov_dpp(x, 0x55, 0xF, 0xF, false)
+                               : i == 2 ? __builtin_amdgcn_mov_dpp(x, 0xAA, 0xF, 0xF, false)
+                                        : __builtin_amdgcn_mov_dpp(x, 0xFF, 0xF, 0xF, false));
+}
+
 // The largest of the values of lanes that differ in bit 4 (every lane active).
 __device__ __forceinline__ float max_rows(float v) {
   const v2u r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);

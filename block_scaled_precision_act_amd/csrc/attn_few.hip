@@ -32,20 +32,13 @@ struct Sequence {
   int32_t tiles;               // 0: no rows; at least 1 otherwise (a row that sees nothing is written)
 };
 
-__device__ __forceinline__ Sequence sequence(const AttnProblem& p, int32_t b) {
+// From its cached tokens and its queries.
+__device__ __forceinline__ Sequence sequence_of(const AttnProblem& p, int32_t len, int32_t q0,
+                                                int32_t n) {
   Sequence s;
-  const int64_t most = static_cast<int64_t>(p.table_width) * p.cache.page_size;
-  const int32_t len = read_uniform(p.lens, b);
-  s.len = len < 0 ? 0 : (len < most ? len : static_cast<int32_t>(most));
-  int32_t q0 = b * p.max_q, q1 = q0 + p.max_q;
-  if (p.starts) {
-    q0 = read_uniform(p.starts, b);
-    q1 = read_uniform(p.starts, b + 1);
-    q0 = min(max(q0, 0), p.total_q);
-    q1 = min(max(q1, q0), p.total_q);
-  }
+  s.len = len;
   s.q0 = q0;
-  s.n = min(q1 - q0, p.max_q);
+  s.n = n;
   s.rows = s.n * p.group;
   s.hi = s.len;
   const int32_t first = s.len - s.n;                     // the first query's position
@@ -54,16 +47,25 @@ __device__ __forceinline__ Sequence sequence(const AttnProblem& p, int32_t b) {
   return s;
 }
 
-// What a lane holds of 32 tokens, undecoded.
+// The first of the D / 16 neighbouring head values that lane c of 16 decodes.
+template <int D>
+__device__ __forceinline__ int value_of(int c) {
+  return D == 64 ? 8 * (c & 7) + 4 * (c >> 3) : c * (D / 16);
+}
+
+// What a lane holds of 32 tokens, undecoded.  Whole words: the widening of a loaded byte or half waits
+// for the load at once, where these wait until the next step needs them.
 template <int D>
 struct RawKeys {
   uint32_t k[2][D / 32];  // per 16 tokens: D / 4 codes of token lane % 16
-  uint32_t s[2];          // their scale byte(s)
+  uint32_t s[2];          // the word that holds their scale byte(s)
 };
 template <int D>
 struct RawValues {
-  uint32_t v[8][D <= 128 ? 1 : 2];   // D / 16 codes of the lane's 8 tokens
-  uint32_t s[2][D == 64 ? 2 : 4];    // words that hold their scale bytes
+  // D / 16 codes of the lane's 8 tokens.  D == 64: the first four words, 8 codes each of every second
+  // token, whose halves lanes c and c + 8 exchange (value_words).
+  uint32_t v[8][D <= 128 ? 1 : 2];
+  uint32_t s[2];                     // the word that holds token 4 (lane % 4) + g's scale byte
 };
 
 struct Places {           // where the two 16-token steps of 32 tokens lie: pages and first tokens
@@ -79,6 +81,18 @@ __device__ __forceinline__ T stream(const uint8_t* p) {
 // exp2(m - now), and 0 where nothing was seen yet (m = -infinity).
 __device__ __forceinline__ float weight_of(float m, float now) {
   return m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
+}
+
+__device__ __forceinline__ Sequence sequence(const AttnProblem& p, int32_t b) {
+  const int64_t most = static_cast<int64_t>(p.table_width) * p.cache.page_size;
+  const int32_t len = read_uniform(p.lens, b);
+  int32_t q0 = b * p.max_q, q1 = q0 + p.max_q;
+  if (p.starts) {
+    q0 = min(max(read_uniform(p.starts, b), 0), p.total_q);
+    q1 = min(max(read_uniform(p.starts, b + 1), q0), p.total_q);
+  }
+  return sequence_of(p, len < 0 ? 0 : (len < most ? len : static_cast<int32_t>(most)), q0,
+                     min(q1 - q0, p.max_q));
 }
 
 // What a sequence and head costs beside its tiles (queries, joins, latencies), counted in tiles.
@@ -123,24 +137,28 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int heads = static_cast<int>(p.cache.heads);
-  // Rotation that brings the byte of the lane's head values to a scale's exponent field.
-  const uint32_t turn_vs = 9 + 8 * (D == 64 ? c >> 3 : D == 128 ? c >> 2 : (c >> 1) & 3);
+  const int key_c = (c & 3) * 4 + (c >> 2);    // the token of 16 whose key the lane loads
+  // Rotations that bring the bytes of the lane's head values to a scale's exponent field.
+  const uint32_t turn_vs = 9 + 8 * (D == 64 ? 2 * (g & 1) + ((c & 7) >> 2) : D == 128 ? c >> 2 : (c >> 1) & 3);
+  const uint32_t turn_ks =
+      9 + 8 * (D == 64 ? 2 * (key_c & 1) + (g >> 1) : D == 128 ? g : 2 * (g & 1));
 
   // This workgroup's run of slots: a prefix sum over the sequences' slots finds the sequence that its
   // run begins in (b) and that sequence's first slot (base).
   uint32_t total, longest, base;           // all slots; the most of one sequence and head
   int b;
+  Sequence mine_of = {};                   // up to 64 sequences: the lane's
   auto share_of = [&]() {
     const uint32_t even = (total + gridDim.x - 1) / gridDim.x;
     const float least = __builtin_sqrtf(kJoinCost * static_cast<float>(longest));
     return max(max(even, 1u), static_cast<uint32_t>(least));
   };
   if (p.batch <= 64) {                     // a lane each, every wavefront for itself
-    const Sequence s = sequence(p, min(lane, p.batch - 1));
-    const uint32_t mine = lane < p.batch ? slots(s, heads) : 0u;
+    mine_of = sequence(p, min(lane, p.batch - 1));
+    const uint32_t mine = lane < p.batch ? slots(mine_of, heads) : 0u;
     const uint32_t incl = prefix_sum(mine);
     total = __builtin_amdgcn_readlane(incl, 63);
-    longest = wave_max(static_cast<uint32_t>(s.tiles));
+    longest = wave_max(static_cast<uint32_t>(mine_of.tiles));
     const uint32_t start = blockIdx.x * share_of();
     if (start >= total) return;
     b = __builtin_ctzll(__ballot(start < incl));
@@ -193,7 +211,10 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
   const uint32_t end = min(at + share, total);
 
   while (at < end) {
-    const Sequence sq = sequence(p, b);
+    const Sequence sq = p.batch > 64 ? sequence(p, b)
+                                     : sequence_of(p, __builtin_amdgcn_readlane(mine_of.len, b),
+                                                   __builtin_amdgcn_readlane(mine_of.q0, b),
+                                                   __builtin_amdgcn_readlane(mine_of.n, b));
     const uint32_t per = static_cast<uint32_t>(sq.tiles) + kUnitSlots, all = slots(sq, heads);
     if (at - base >= all) {                  // also a sequence without rows
       base += all;
@@ -266,9 +287,9 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint8_t* const kp = kh + (at.id[s] * p.cache.code_page + at.off[s] * (D / 2)) +
-                                  (c * (D / 2) + g * (D / 8));
+                                  (key_c * (D / 2) + g * (D / 8));
         const uint8_t* const sp = ksh + (at.id[s] * p.cache.scale_page + at.off[s] * (D / 32)) +
-                                  (c * (D / 32) + g * (D / 32) / 4);
+                                  (D == 64 ? (key_c >> 1) * 4 : D == 128 ? key_c * 4 : key_c * 8 + (g >> 1) * 4);
         if constexpr (D == 64) {
           const v2u t = stream<v2u>(kp);
           w.k[s][0] = t[0]; w.k[s][1] = t[1];
@@ -280,50 +301,45 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
             for (int e = 0; e < 4; ++e) w.k[s][4 * i + e] = t[e];
           }
         }
-        if constexpr (D == 256) w.s[s] = *reinterpret_cast<const uint16_t*>(sp);
-        else w.s[s] = *sp;
+        w.s[s] = *reinterpret_cast<const uint32_t*>(sp);
       }
     };
     auto load_values = [&](RawValues<D>& w, const Places& at) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint8_t* const vp = vh + (at.id[s] * p.cache.code_page + at.off[s] * (D / 2)) +
-                                  (g * 4 * (D / 2) + c * (D / 32));
+                                  (D == 64 ? ((c >> 3) * 4 + g) * 32 + (c & 7) * 4 : g * (D / 2) + c * (D / 32));
         const uint8_t* const sp = vsh + (at.id[s] * p.cache.scale_page + at.off[s] * (D / 32)) +
-                                  g * 4 * (D / 32);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t* a = vp + i * (D / 2);
-          if constexpr (D == 64) w.v[4 * s + i][0] = stream<uint16_t>(a);
-          if constexpr (D == 128) w.v[4 * s + i][0] = stream<uint32_t>(a);
-          if constexpr (D == 256) {
-            const v2u t = stream<v2u>(a);
-            w.v[4 * s + i][0] = t[0]; w.v[4 * s + i][1] = t[1];
-          }
-        }
+                                  (D == 64 ? ((c & 3) * 2 + (g >> 1)) * 4
+                                           : ((c & 3) * 4 + g) * (D / 32) + (D == 256 ? (c >> 3) * 4 : 0));
         if constexpr (D == 64) {
-          const uint2 t = *reinterpret_cast<const uint2*>(sp);
-          w.s[s][0] = t.x; w.s[s][1] = t.y;
-        } else if constexpr (D == 128) {
-          const uint4 t = *reinterpret_cast<const uint4*>(sp);
-          w.s[s][0] = t.x; w.s[s][1] = t.y; w.s[s][2] = t.z; w.s[s][3] = t.w;
+          w.v[2 * s][0] = stream<uint32_t>(vp);
+          w.v[2 * s + 1][0] = stream<uint32_t>(vp + 8 * 32);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w.s[s][i] = *reinterpret_cast<const uint32_t*>(sp + i * 8 + (c >> 3) * 4);
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t* a = vp + i * 4 * (D / 2);
+            if constexpr (D == 128) {
+              w.v[4 * s + i][0] = stream<uint32_t>(a);
+            } else {
+              const v2u t = stream<v2u>(a);
+              w.v[4 * s + i][0] = t[0]; w.v[4 * s + i][1] = t[1];
+            }
+          }
         }
+        w.s[s] = *reinterpret_cast<const uint32_t*>(sp);
       }
     };
 
     // 32 tokens from tok0; what was loaded for them is replaced by the loads of `next` as soon as it
     // is decoded.
-    auto step = [&](RawKeys<D>& rk, RawValues<D>& rv, int32_t tok0, const Places& next, bool more) {
+    auto step = [&](RawKeys<D>& rk, RawValues<D>& rv, int32_t tok0, const Places& next, auto more) {
       v4f s[MT][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
-          const float sc = __uint_as_float((D == 256 && j >= 4 ? rk.s[t] >> 8 : rk.s[t]) << 23);
+          const float sc = scale_of_byte(rk.s[t], D == 256 && j >= 4 ? turn_ks + 8 : turn_ks);
           const bf16x8 kf = __builtin_bit_cast(bf16x8, decode8(rk.k[t][j], sc));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -331,13 +347,13 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
                                                                0, 0, 0);
         }
       }
-      if (more) load_keys(rk, next);
+      if constexpr (decltype(more)::value) load_keys(rk, next);
       if (tok0 + kWaveTokens > full_hi || tok0 < full_lo) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int32_t t = tok0 + (i >> 2) * 16 + g * 4 + (i & 3);
+            const int32_t t = tok0 + (i >> 2) * 16 + (i & 3) * 4 + g;
             if (t >= hi_row[mt] || t < lo_row[mt]) s[mt][i >> 2][i & 3] = -kInf;
           }
         __builtin_amdgcn_sched_barrier(0);        // keeps the masks a branch
@@ -377,19 +393,30 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       float vsc[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        vsc[i] = scale_of_byte(D == 64 ? rv.s[i >> 2][(i & 3) >> 1] : rv.s[i >> 2][i & 3],
-                               D == 64 && (i & 1) ? turn_vs + 16 : turn_vs);
+        vsc[i] = scale_of_byte(quad_lane(rv.s[i >> 2], i & 3), turn_vs);
       if (tok0 + kWaveTokens > sq.hi) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (tok0 + (i >> 2) * 16 + g * 4 + (i & 3) >= sq.hi) vsc[i] = 1.f;
+          if (tok0 + (i >> 2) * 16 + (i & 3) * 4 + g >= sq.hi) vsc[i] = 1.f;
         __builtin_amdgcn_sched_barrier(0);
+      }
+      // D == 64: lane c loaded 8 codes of one token, lane c + 8 the same 8 of another; each keeps its
+      // half of both, the first token's in the low half of the word.
+      uint32_t vw[4];
+      if constexpr (D == 64) {
+        const uint32_t halves = c < 8 ? kLowHalves : 0x03020706u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vw[i] = __builtin_amdgcn_perm(
+              static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(rv.v[i][0]), 0x128, 0xF, 0xF, false)),
+              rv.v[i][0], halves);
       }
 #pragma unroll
       for (int a = 0; a < EPL / 2; ++a) {        // head values 2 a and 2 a + 1 of the lane's EPL
         uint32_t pr[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) pr[i] = decode2(rv.v[i][a >> 2], vsc[i], a & 3);
+        for (int i = 0; i < 8; ++i)
+          pr[i] = D == 64 ? decode2(vw[i >> 1], vsc[i], 2 * (i & 1) + a) : decode2(rv.v[i][a >> 2], vsc[i], a & 3);
         v4u lo, hi;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -404,7 +431,7 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
               __builtin_bit_cast(bf16x8, hi), pf[mt], acc[mt][2 * a + 1], 0, 0, 0);
         }
       }
-      if (more) load_values(rv, next);
+      if constexpr (decltype(more)::value) load_values(rv, next);
     };
 
     const int32_t tok_begin = sq.lo + tile0 * kTile + wave * kWaveTokens;
@@ -416,11 +443,15 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       load_keys(rk, at);
       load_values(rv, at);
       at = place(tok_begin + kTile);             // past the end: the last step's
-      for (int32_t t = tok_begin; t < tok_end; t += kTile) {
+      // The last step is apart: loads that depended on a condition would make every wait for keys one
+      // for the values behind them too.
+      int32_t t = tok_begin;
+      for (; t + kTile < tok_end; t += kTile) {
         const Places next = place(t + 2 * kTile);
-        step(rk, rv, t, at, t + kTile < tok_end);
+        step(rk, rv, t, at, IntC<1>{});
         at = next;
       }
+      step(rk, rv, t, at, IntC<0>{});
     }
 
     // Join the four wavefronts through LDS, 16 rows at a time; thread t then holds EPL values of
@@ -466,7 +497,7 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < EPL; e += 4)
-          *reinterpret_cast<float4*>(&obuf[wave][c][(g * 4 + i) * EPL + e]) =
+          *reinterpret_cast<float4*>(&obuf[wave][c][value_of<D>(g * 4 + i) + e]) =
               make_float4(acc[mt][e][i] * f, acc[mt][e + 1][i] * f, acc[mt][e + 2][i] * f,
                           acc[mt][e + 3][i] * f);
       __syncthreads();

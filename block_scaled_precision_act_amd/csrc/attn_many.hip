@@ -18,8 +18,10 @@ constexpr int kTok = 64;
 constexpr float kLn2 = 0.6931471805599453f;
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-// A decoding thread's undecoded share of 64 tokens: a quarter of a token's key codes and their scale
-// byte(s); or D / 32 value codes of 8 tokens and the words that hold their scale bytes.
+// A decoding thread's undecoded share of 64 tokens: a quarter of a token's key codes and the word that
+// holds their scale byte(s); or the words of 8 tokens that hold its D / 32 value codes, and those that
+// hold their scale bytes.  Whole words: the widening of a loaded byte or half waits for the load at
+// once, where these wait until the next tile needs them.
 template <int D>
 struct RawKeys {
   uint32_t k[D / 32], s;
@@ -106,6 +108,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(co
   const bool keys = NW == 4 || wave < 4, values = NW == 4 || wave >= 4;
   const int sub = wave & 3;
   const int k16 = lane & 15, kq = lane >> 4, vc = lane & 31, vh = lane >> 5;
+  const uint32_t turn_k = 9 + 8 * (D == 64 ? 2 * (k16 & 1) + (kq >> 1) : D == 128 ? kq : 2 * (kq & 1));
   const int32_t last16 = (hi - 1) >> 4;
   const int64_t trow = static_cast<int64_t>(b) * p.table_stride;
   const uint32_t page16 = p.cache.page_size >> 4;
@@ -124,31 +127,27 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(co
   auto load_keys = [&](RawKeys<D>& w, Place at) {
     const uint8_t* kp = kbase + (at.id * p.cache.code_page + at.off * (D / 2)) +
                         (k16 * (D / 2) + kq * (D / 8));
-    const uint8_t* sp = ksbase + (at.id * p.cache.scale_page + at.off * (D / 32)) + k16 * (D / 32);
+    const uint8_t* sp = ksbase + (at.id * p.cache.scale_page + at.off * (D / 32)) +
+                        (D == 64 ? (k16 >> 1) * 4 : D == 128 ? k16 * 4 : k16 * 8 + (kq >> 1) * 4);
     if constexpr (D == 64) {
       const uint2 t = *reinterpret_cast<const uint2*>(kp);
       w.k[0] = t.x; w.k[1] = t.y;
-      w.s = sp[kq >> 1];
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
         const uint4 t = *reinterpret_cast<const uint4*>(kp + 16 * i);
         w.k[4 * i] = t.x; w.k[4 * i + 1] = t.y; w.k[4 * i + 2] = t.z; w.k[4 * i + 3] = t.w;
       }
-      if constexpr (D == 128) w.s = sp[kq];
-      else w.s = *reinterpret_cast<const uint16_t*>(sp + 2 * kq);
     }
+    w.s = *reinterpret_cast<const uint32_t*>(sp);
   };
   auto load_values = [&](RawValues<D>& w, Place at) {
     const uint8_t* vp = vbase + (at.id * p.cache.code_page + at.off * (D / 2)) +
-                        (vh * 4 * (D / 2) + vc * (EPI / 2));
+                        (vh * 4 * (D / 2) + (vc * (EPI / 2) & ~3));
     const uint8_t* sp = vsbase + (at.id * p.cache.scale_page + at.off * (D / 32)) + vh * 4 * (D / 32);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint8_t* a = vp + ((i >> 2) * 8 + (i & 3)) * (D / 2);
-      if constexpr (D == 64) w.v[i] = *a;
-      if constexpr (D == 128) w.v[i] = *reinterpret_cast<const uint16_t*>(a);
-      if constexpr (D == 256) w.v[i] = *reinterpret_cast<const uint32_t*>(a);
+      w.v[i] = *reinterpret_cast<const uint32_t*>(vp + ((i >> 2) * 8 + (i & 3)) * (D / 2));
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -169,13 +168,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(co
   auto decode_keys = [&](const RawKeys<D>& w, uint4* dst) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const float sc = __uint_as_float((D == 256 && i >= 4 ? w.s >> 8 : w.s) << 23);
+      const float sc = scale_of_byte(w.s, D == 256 && i >= 4 ? turn_k + 8 : turn_k);
       const int word = kq * (D / 32) + i;               // 8 codes: k step word / 2, half word % 2
       dst[((sub >> 1) * KS + (word >> 1)) * 64 + (word & 1) * 32 + (sub & 1) * 16 + k16] =
           decode8(w.k[i], sc);
     }
   };
   auto decode_values = [&](const RawValues<D>& w, int32_t t0, uint4* dst) {
+    const uint32_t drop = D == 64 ? 8 * (vc & 3) : D == 128 ? 16 * (vc & 1) : 0;   // the lane's codes lowest
     const uint32_t turn = 9 + 8 * (D == 64 ? vc >> 4 : D == 128 ? vc >> 3 : (vc >> 2) & 3);
     float sc[8];
 #pragma unroll
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(co
     for (int a = 0; a < EPI / 2; ++a) {
       uint32_t pr[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pr[i] = decode2(w.v[i], sc[i], a);
+      for (int i = 0; i < 8; ++i) pr[i] = decode2(D == 256 ? w.v[i] : w.v[i] >> drop, sc[i], a);
       uint4 x, y;
       x.x = __builtin_amdgcn_perm(pr[1], pr[0], kLowHalves);
       x.y = __builtin_amdgcn_perm(pr[3], pr[2], kLowHalves);
