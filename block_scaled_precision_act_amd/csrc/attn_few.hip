@@ -614,10 +614,8 @@ hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream
 template <int D>
 hipError_t launch_d(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
   if (plan.row_tiles == 1) return launch<D, 1>(p, plan, stream);
-  if constexpr (D < 256) {
-    if (plan.row_tiles == 2) return launch<D, 2>(p, plan, stream);
-    return launch<D, 4>(p, plan, stream);
-  }
+  if (plan.row_tiles == 2) return launch<D, 2>(p, plan, stream);
+  if constexpr (D < 256) return launch<D, 4>(p, plan, stream);
   return hipErrorInvalidValue;
 }
 

@@ -81,7 +81,7 @@ struct AttnProblem {
   uint32_t flip;             // 0x80008000 where scale < 0: the queries' signs are turned instead
   bool causal;
   int32_t window;
-  uint32_t* counters;        // one per (sequence, key/value head) (and row block), zero between calls
+  uint32_t* counters;        // few rows: one per (sequence, key/value head), zero between calls
   float* parts;
 };
 

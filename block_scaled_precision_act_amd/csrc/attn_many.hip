@@ -32,19 +32,13 @@ struct Work {
   bool any;
 };
 
-__device__ __forceinline__ Work work_of(const AttnProblem& p, int block_rows, int row_blocks,
-                                        int splits) {
+__device__ __forceinline__ Work work_of(const AttnProblem& p, int block_rows, int splits, int h, int b,
+                                        int blk, int part) {
   Work w;
-  const uint32_t heads = p.cache.heads;
-  // Heads fastest: with 8 of them a head's keys stay on one XCD's L2.  Late rows (the longest under
-  // a causal mask) first.
-  uint32_t idx = blockIdx.x;
-  w.h = idx % heads;
-  idx /= heads;
-  w.b = idx % p.batch;
-  idx /= p.batch;
-  w.part = idx % splits;
-  w.blk = row_blocks - 1 - static_cast<int>(idx / splits);
+  w.h = h;
+  w.b = b;
+  w.blk = blk;
+  w.part = part;
   const int64_t most = static_cast<int64_t>(p.table_width) * p.cache.page_size;
   const int32_t raw_len = read_uniform(p.lens, w.b);
   w.len = raw_len < 0 ? 0 : (raw_len < most ? raw_len : static_cast<int32_t>(most));
@@ -72,6 +66,18 @@ __device__ __forceinline__ Work work_of(const AttnProblem& p, int block_rows, in
   w.full_hi = p.causal ? min(w.first + tok_lo + 1, w.len) : w.len;
   w.full_lo = p.window > 0 ? w.first + tok_hi + 1 - p.window : 0;
   return w;
+}
+
+// A workgroup's.  Heads fastest: with 8 of them a head's keys stay on one XCD's L2.  Late rows (the
+// longest under a causal mask) first.
+__device__ __forceinline__ Work my_work(const AttnProblem& p, int block_rows, int row_blocks, int splits) {
+  const uint32_t heads = p.cache.heads;
+  uint32_t idx = blockIdx.x;
+  const int h = idx % heads;
+  idx /= heads;
+  const int b = idx % p.batch;
+  idx /= p.batch;
+  return work_of(p, block_rows, splits, h, b, row_blocks - 1 - static_cast<int>(idx / splits), idx % splits);
 }
 
 // A lane's query row: lanes c and c + 32 of a wavefront share row r0 + 32 tile + c.
@@ -106,17 +112,13 @@ __device__ __forceinline__ void load_query(const AttnProblem& p, const Work& w, 
   }
 }
 
-// A decoding thread's undecoded share of 64 tokens: a quarter of a token's key codes and the word that
-// holds their scale byte(s); or the words of 8 tokens that hold its D / 32 value codes, and those that
-// hold their scale bytes.  Whole words: the widening of a loaded byte or half waits for the load at
-// once, where these wait until the next tile needs them.
-template <int D>
-struct RawKeys {
-  uint32_t k[D / 32], s;
-};
-template <int D>
-struct RawValues {
-  uint32_t v[8], s[2][D == 64 ? 2 : 4];
+// A decoding thread's undecoded share of 64 tokens.  Of keys: a quarter of a token's codes (x[0 ..
+// D / 32)) and the word that holds their scale byte(s) (x[15]).  Of values: the words of 8 tokens that
+// hold its D / 32 codes (x[0 .. 8)), and those that hold their scale bytes (from x[8]: of the first
+// four tokens, from x[12]: of the others).  Whole words: the widening of a loaded byte or half waits
+// for the load at once, where these wait until the next tile needs them.
+struct Raw {
+  uint32_t x[16];
 };
 
 struct Place {                // where a 16-token step lies: its page and the first token's offset
@@ -159,64 +161,64 @@ struct Decoder {
     const uint32_t id = static_cast<uint32_t>(read_uniform(p.table, trow + page));
     return Place{id < p.cache.pages ? id : 0u, (t16 - page * page16) * 16u};
   }
-  __device__ __forceinline__ void load_keys(RawKeys<D>& w, Place at) const {
+  __device__ __forceinline__ void load_keys(Raw& w, Place at) const {
     const uint8_t* kp = kbase + (at.id * p.cache.code_page + at.off * (D / 2)) +
                         (k16 * (D / 2) + kq * (D / 8));
     const uint8_t* sp = ksbase + (at.id * p.cache.scale_page + at.off * (D / 32)) +
                         (D == 64 ? (k16 >> 1) * 4 : D == 128 ? k16 * 4 : k16 * 8 + (kq >> 1) * 4);
     if constexpr (D == 64) {
       const uint2 t = *reinterpret_cast<const uint2*>(kp);
-      w.k[0] = t.x; w.k[1] = t.y;
+      w.x[0] = t.x; w.x[1] = t.y;
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
         const uint4 t = *reinterpret_cast<const uint4*>(kp + 16 * i);
-        w.k[4 * i] = t.x; w.k[4 * i + 1] = t.y; w.k[4 * i + 2] = t.z; w.k[4 * i + 3] = t.w;
+        w.x[4 * i] = t.x; w.x[4 * i + 1] = t.y; w.x[4 * i + 2] = t.z; w.x[4 * i + 3] = t.w;
       }
     }
-    w.s = *reinterpret_cast<const uint32_t*>(sp);
+    w.x[15] = *reinterpret_cast<const uint32_t*>(sp);
   }
-  __device__ __forceinline__ void load_values(RawValues<D>& w, Place at) const {
+  __device__ __forceinline__ void load_values(Raw& w, Place at) const {
     const uint8_t* vp = vbase + (at.id * p.cache.code_page + at.off * (D / 2)) +
                         (vh * 4 * (D / 2) + (vc * (EPI / 2) & ~3));
     const uint8_t* sp = vsbase + (at.id * p.cache.scale_page + at.off * (D / 32)) + vh * 4 * (D / 32);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      w.v[i] = *reinterpret_cast<const uint32_t*>(vp + ((i >> 2) * 8 + (i & 3)) * (D / 2));
+      w.x[i] = *reinterpret_cast<const uint32_t*>(vp + ((i >> 2) * 8 + (i & 3)) * (D / 2));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint8_t* a = sp + i * 8 * (D / 32);
       if constexpr (D == 64) {
         const uint2 x = *reinterpret_cast<const uint2*>(a);
-        w.s[i][0] = x.x; w.s[i][1] = x.y;
+        w.x[8 + 4 * i] = x.x; w.x[9 + 4 * i] = x.y;
       } else if constexpr (D == 128) {
         const uint4 x = *reinterpret_cast<const uint4*>(a);
-        w.s[i][0] = x.x; w.s[i][1] = x.y; w.s[i][2] = x.z; w.s[i][3] = x.w;
+        w.x[8 + 4 * i] = x.x; w.x[9 + 4 * i] = x.y; w.x[10 + 4 * i] = x.z; w.x[11 + 4 * i] = x.w;
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          w.s[i][e] = *reinterpret_cast<const uint32_t*>(a + e * 8 + (vc >> 4) * 4);
+          w.x[8 + 4 * i + e] = *reinterpret_cast<const uint32_t*>(a + e * 8 + (vc >> 4) * 4);
       }
     }
   }
   // Into [32-token half][k step][lane].
-  __device__ __forceinline__ void decode_keys(const RawKeys<D>& w, uint4* dst) const {
+  __device__ __forceinline__ void decode_keys(const Raw& w, uint4* dst) const {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const float sc = scale_of_byte(w.s, D == 256 && i >= 4 ? turn_k + 8 : turn_k);
+      const float sc = scale_of_byte(w.x[15], D == 256 && i >= 4 ? turn_k + 8 : turn_k);
       const int word = kq * (D / 32) + i;               // 8 codes: k step word / 2, half word % 2
       dst[((sub >> 1) * KS + (word >> 1)) * 64 + (word & 1) * 32 + (sub & 1) * 16 + k16] =
-          decode8(w.k[i], sc);
+          decode8(w.x[i], sc);
     }
   }
   // Of the tile from t0, into [16-token step][head value % DT][lane].
-  __device__ __forceinline__ void decode_values(const RawValues<D>& w, int32_t t0, uint4* dst) const {
+  __device__ __forceinline__ void decode_values(const Raw& w, int32_t t0, uint4* dst) const {
     const uint32_t drop = D == 64 ? 8 * (vc & 3) : D == 128 ? 16 * (vc & 1) : 0;   // the lane's codes lowest
     const uint32_t turn = 9 + 8 * (D == 64 ? vc >> 4 : D == 128 ? vc >> 3 : (vc >> 2) & 3);
     float sc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      sc[i] = scale_of_byte(D == 64 ? w.s[i >> 2][(i & 3) >> 1] : w.s[i >> 2][i & 3],
+      sc[i] = scale_of_byte(w.x[8 + (D == 64 ? 4 * (i >> 2) + ((i & 3) >> 1) : i)],
                             D == 64 && (i & 1) ? turn + 16 : turn);
     // What lies past the keys is given scale 1: finite, and its weight is 0.
     if (t0 + kTok > hi) {
@@ -229,7 +231,7 @@ struct Decoder {
     for (int a = 0; a < EPI / 2; ++a) {
       uint32_t pr[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pr[i] = decode2(D == 256 ? w.v[i] : w.v[i] >> drop, sc[i], a);
+      for (int i = 0; i < 8; ++i) pr[i] = decode2(D == 256 ? w.x[i] : w.x[i] >> drop, sc[i], a);
       uint4 x, y;
       x.x = __builtin_amdgcn_perm(pr[1], pr[0], kLowHalves);
       x.y = __builtin_amdgcn_perm(pr[3], pr[2], kLowHalves);
@@ -277,75 +279,124 @@ __device__ __forceinline__ bf16x8 weights(const v16f& s, int at, float scale, fl
                                                pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])));
 }
 
-// The lane's sums are head values DT (i % 4 + 8 (i / 4) + 4 h) + d0 + d, d < N, h its half: the row
-// is written, or (several parts) left in the workspace for the last part to join.
-// Partial layout: values as the lanes hold them, 4 to a lane, lanes in a row; then m, then l.
-template <int DT, int N>
-__device__ __forceinline__ void write_row(const AttnProblem& p, const Work& w, const Row& r,
-                                          const v16f (&acc)[N], float m, float l, int d0, bool lse) {
-  const int hh = (threadIdx.x & 63) >> 5, head = w.h * p.group + r.hg;
-  const int64_t qrow = w.q0 + r.tok;
+// Writes N of the lane's sums of its row's head values DT (i % 4 + 8 (i / 4) + 4 h) + d0 + d, d < N,
+// for i in [4 q0, 4 q1), h the lane's half.
+template <int DT, int N, int Q0, int Q1>
+__device__ __forceinline__ void write_values(const AttnProblem& p, const Work& w, const Row& r,
+                                             const v4f (&acc)[N][Q1 - Q0], float l, int d0) {
+  const int hh = (threadIdx.x & 63) >> 5;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* dst = p.out.p + qrow * p.out.token_stride + head * p.out.head_stride + d0;
+  uint16_t* dst = p.out.p + static_cast<int64_t>(w.q0 + r.tok) * p.out.token_stride +
+                  static_cast<int64_t>(w.h * p.group + r.hg) * p.out.head_stride + d0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 4 * Q0; i < 4 * Q1; ++i) {
     uint32_t x[N / 2];
 #pragma unroll
-    for (int d = 0; d < N / 2; ++d) x[d] = pack_bf16(acc[2 * d][i] * inv, acc[2 * d + 1][i] * inv);
+    for (int d = 0; d < N / 2; ++d)
+      x[d] = pack_bf16(acc[2 * d][i / 4 - Q0][i % 4] * inv, acc[2 * d + 1][i / 4 - Q0][i % 4] * inv);
     uint16_t* at = dst + DT * ((i & 3) + 8 * (i >> 2) + 4 * hh);
     if constexpr (N == 2) *reinterpret_cast<uint32_t*>(at) = x[0];
     else *reinterpret_cast<uint2*>(at) = make_uint2(x[0], x[1]);
   }
-  if (lse && p.lse && hh == 0)
-    p.lse[qrow * (static_cast<int64_t>(p.group) * p.cache.heads) + head] =
+}
+
+__device__ __forceinline__ void write_lse(const AttnProblem& p, const Work& w, const Row& r, float m, float l) {
+  if (p.lse && (threadIdx.x & 32) == 0)
+    p.lse[static_cast<int64_t>(w.q0 + r.tok) * p.group * p.cache.heads + w.h * p.group + r.hg] =
         l == 0.f ? -kInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-template <int THREADS, int N>
-__device__ __forceinline__ void store_part(float* part, const v16f (&acc)[N], float m, float l, int stat) {
-#pragma unroll
-  for (int d = 0; d < N; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-      store_shared4(part + ((d * 4 + i / 4) * THREADS + threadIdx.x) * 4, acc[d][i], acc[d][i + 1],
-                    acc[d][i + 2], acc[d][i + 3]);
-  if ((threadIdx.x & 32) == 0) {
-    store_shared(part + N * 16 * THREADS + stat, m);
-    store_shared(part + N * 16 * THREADS + THREADS / 2 + stat, l);
-  }
-}
+// Floats of one part's partial result: a thread's N sums of 16, as 4 N units of 4, unit by unit, a
+// thread after the other; then m, then l, of each row (a row is two threads').
+constexpr int64_t part_floats(int threads, int n) { return static_cast<int64_t>(threads) * (16 * n + 1); }
 
-// Joins `parts` partials, in order.  A part that saw nothing has m = -infinity and weight 0.
-template <int THREADS, int N>
-__device__ __forceinline__ void join_parts(const float* first, int64_t stride, int parts, int stat,
-                                           v16f (&acc)[N], float& m, float& l) {
-  m = -kInf;
-  l = 0.f;
-#pragma unroll
-  for (int d = 0; d < N; ++d) acc[d] = v16f(0.f);
-  for (int q = 0; q < parts; ++q) {
-    const float* src = first + q * stride;
-    const float pm = src[N * 16 * THREADS + stat], pl = src[N * 16 * THREADS + THREADS / 2 + stat];
-    const float now = fmaxf(m, pm);
-    const float fo = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
-    const float fn = pm == -kInf ? 0.f : __builtin_amdgcn_exp2f(pm - now);
-    m = now;
-    l = l * fo + pl * fn;
+// The rows are written (one part), or left for the join.
+template <int DT, int THREADS, int N>
+__device__ __forceinline__ void finish(const AttnProblem& p, const Work& w, const Row& r, int splits,
+                                       const v16f (&acc)[N], float m, float l, int d0) {
+  if (w.parts == 1) {
+    if (!r.live) return;
+    v4f x[N][4];
 #pragma unroll
     for (int d = 0; d < N; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src + ((d * 4 + i / 4) * THREADS + threadIdx.x) * 4);
-        acc[d][i] = acc[d][i] * fo + x.x * fn;
-        acc[d][i + 1] = acc[d][i + 1] * fo + x.y * fn;
-        acc[d][i + 2] = acc[d][i + 2] * fo + x.z * fn;
-        acc[d][i + 3] = acc[d][i + 3] * fo + x.w * fn;
-      }
+      for (int i = 0; i < 16; ++i) x[d][i / 4][i % 4] = acc[d][i];
+    write_values<DT, N, 0, 4>(p, w, r, x, l, d0);
+    if (d0 == 0) write_lse(p, w, r, m, l);
+    return;
+  }
+  const int64_t unit = (static_cast<int64_t>(w.blk) * p.batch + w.b) * p.cache.heads + w.h;
+  float* const part = p.parts + (unit * splits + w.part) * part_floats(THREADS, N);
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(part + ((d * 4 + i) * THREADS + threadIdx.x) * 4) =
+          make_float4(acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]);
+  if ((threadIdx.x & 32) == 0) {
+    const int row = threadIdx.x / 64 * 32 + (threadIdx.x & 31);
+    part[N * 16 * THREADS + row] = m;
+    part[N * 16 * THREADS + THREADS / 2 + row] = l;
   }
 }
 
-// Floats of one partial: N sums of 16 a thread, m and l for each 2 threads.
-constexpr int64_t part_floats(int threads, int n) { return static_cast<int64_t>(threads) * (16 * n + 1); }
+// Joins a block's parts, in their order, whole rows at a time; a workgroup takes one of a thread's
+// four lots of 4 for two of its N sums.  A launch of its own: the parts of one block would be joined
+// by one workgroup otherwise (128 rows of 60000 keys in 64 parts: 110 us, 63 us so).
+// HALVES: 2 where two wavefronts share rows (attn_wide_kernel).
+template <int DT, int THREADS, int N, int HALVES>
+__global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p, int splits) {
+  constexpr int kSlices = 4 * N / 2, kTiles = THREADS / 64 / HALVES;
+  const uint32_t heads = p.cache.heads;
+  const uint32_t slice = blockIdx.x % kSlices, unit = blockIdx.x / kSlices;
+  const Work w = work_of(p, 32 * kTiles, splits, unit % heads, unit / heads % p.batch,
+                         unit / heads / p.batch, 0);
+  if (!w.any || w.parts == 1) return;
+  const int wave = threadIdx.x / 64, row = wave * 32 + (threadIdx.x & 31);
+  const int q = slice % 4, d = slice / 4 * 2;
+  constexpr int64_t kPart = part_floats(THREADS, N);
+  const float* src = p.parts + static_cast<int64_t>(unit) * splits * kPart;
+  float m = -kInf, l = 0.f;
+  v4f acc[2][1] = {{v4f(0.f)}, {v4f(0.f)}};
+  constexpr int kBatch = 8;
+  for (int at = 0; at < w.parts; at += kBatch) {
+    float pm[kBatch], pl[kBatch];
+    v4f x[kBatch][2];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {               // past the last part: that part, with no weight
+      const float* s = src + min(at + i, w.parts - 1) * kPart;
+      pm[i] = at + i < w.parts ? s[N * 16 * THREADS + row] : -kInf;
+      pl[i] = s[N * 16 * THREADS + THREADS / 2 + row];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        x[i][e] = *reinterpret_cast<const v4f*>(s + (((d + e) * 4 + q) * THREADS + threadIdx.x) * 4);
+    }
+    float now = m;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) now = fmaxf(now, pm[i]);
+    const float fo = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
+    m = now;
+    l *= fo;
+    acc[0][0] *= fo;
+    acc[1][0] *= fo;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (at + i >= w.parts) break;
+      const float f = pm[i] == -kInf ? 0.f : __builtin_amdgcn_exp2f(pm[i] - now);
+      l += pl[i] * f;
+      acc[0][0] += x[i][0] * f;
+      acc[1][0] += x[i][1] * f;
+    }
+  }
+  const Row r = row_of(p, w, wave % kTiles);
+  if (!r.live) return;
+  const int d0 = wave / kTiles * N + d;
+  if (q == 0) write_values<DT, 2, 0, 1>(p, w, r, acc, l, d0);
+  if (q == 1) write_values<DT, 2, 1, 2>(p, w, r, acc, l, d0);
+  if (q == 2) write_values<DT, 2, 2, 3>(p, w, r, acc, l, d0);
+  if (q == 3) write_values<DT, 2, 3, 4>(p, w, r, acc, l, d0);
+  if (q == 0 && d0 == 0) write_lse(p, w, r, m, l);
+}
 
 // NW wavefronts of 32 query rows each.  Of 8, the first four decode keys and the others values (one
 // of each to a SIMD); of 4, all decode both.
@@ -355,10 +406,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
   constexpr int KS = D / 16, DT = D / 32, kThreads = 64 * NW;
   __shared__ uint4 kl[2][2 * KS * 64];
   __shared__ uint4 vl[2][4 * DT * 64];
-  __shared__ uint32_t flag;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Work w = work_of(p, 32 * NW, row_blocks, splits);
+  const Work w = my_work(p, 32 * NW, row_blocks, splits);
   if (!w.any) return;
   const Row row = row_of(p, w, wave);
   bf16x8 qf[KS];
@@ -370,9 +420,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
   float m = -kInf, l = 0.f;
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = v16f(0.f);
-  RawKeys<D> rk;
-  RawValues<D> rv;
-  Place next_k, next_v;
+  // A wavefront that decodes one of the two holds one share.
+  Raw rk, rv_own;
+  Raw& rv = NW == 4 ? rv_own : rk;
+  Place next_k, next_v_own;
+  Place& next_v = NW == 4 ? next_v_own : next_k;
 
   // Tile i: its scores `s` are there; while its weights and products are made, the next tile's scores
   // are (into `sn`), the keys after those and the next tile's values are decoded, and the ones after
@@ -462,16 +514,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
   }
   l += __shfl_xor(l, 32, 64);
 
-  if (w.parts > 1) {
-    const int64_t unit = (static_cast<int64_t>(w.blk) * p.batch + w.b) * p.cache.heads + w.h;
-    constexpr int64_t kPart = part_floats(kThreads, DT);
-    float* const parts = p.parts + unit * splits * kPart;
-    const int stat = wave * 32 + (lane & 31);
-    store_part<kThreads>(parts + w.part * kPart, acc, m, l, stat);
-    if (!arrive_last(p.counters + unit * kCounterStride, static_cast<uint32_t>(w.parts), &flag)) return;
-    join_parts<kThreads>(parts, kPart, w.parts, stat, acc, m, l);
-  }
-  if (row.live) write_row<DT>(p, w, row, acc, m, l, 0, true);
+  finish<DT, kThreads>(p, w, row, splits, acc, m, l, 0);
 }
 
 // Heads of 256: eight wavefronts, the first four (half 0) and the last four (half 1) on the same four
@@ -488,11 +531,10 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem p, 
   __shared__ uint4 vl[4 * DT * 64];
   __shared__ uint4 pl[4][4 * 64];           // [row tile][16-token step][lane]
   __shared__ float tops[2][4][2][32];       // [tile parity][row tile][half][row]
-  __shared__ uint32_t flag;
   const int lane = threadIdx.x & 63, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rt = wave & 3, half = wave >> 2;
-  const Work w = work_of(p, 128, row_blocks, splits);
+  const Work w = my_work(p, 128, row_blocks, splits);
   if (!w.any) return;
   const Row row = row_of(p, w, rt);
   bf16x8 qf[KS];
@@ -503,8 +545,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem p, 
   float m = -kInf, l = 0.f;
 #pragma unroll
   for (int d = 0; d < N; ++d) acc[d] = v16f(0.f);
-  RawKeys<D> rk;
-  RawValues<D> rv;
+  Raw raw;
   Place next;
 
   // Scores of tile i, masked, and their maxima for the other half.
@@ -538,9 +579,9 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem p, 
     for (int u = 0; u < 2; ++u)
       pl[rt][(half * 2 + u) * 64 + lane] = __builtin_bit_cast(uint4, weights(s, 8 * u, p.scale_log2, sub, l));
     if (half == 1) {
-      dec.decode_values(rv, t0, vl);
+      dec.decode_values(raw, t0, vl);
       if constexpr (!LAST) {
-        dec.load_values(rv, next);
+        dec.load_values(raw, next);
         next = dec.place(t0 + 2 * kTok);
       }
     }
@@ -556,8 +597,8 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem p, 
     }
     if constexpr (!LAST) {
       if (half == 0) {
-        dec.decode_keys(rk, kl);
-        dec.load_keys(rk, next);
+        dec.decode_keys(raw, kl);
+        dec.load_keys(raw, next);
         next = dec.place(t0 + 4 * kTok);
       }
       lds_barrier();
@@ -567,19 +608,19 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem p, 
   if (w.tiles > 0) {
     v16f sa, sb;
     if (half == 0) {
-      dec.load_keys(rk, dec.place(w.t_begin));
-      dec.decode_keys(rk, kl);
-      dec.load_keys(rk, dec.place(w.t_begin + kTok));
+      dec.load_keys(raw, dec.place(w.t_begin));
+      dec.decode_keys(raw, kl);
+      dec.load_keys(raw, dec.place(w.t_begin + kTok));
     } else {
-      dec.load_values(rv, dec.place(w.t_begin));
+      dec.load_values(raw, dec.place(w.t_begin));
       next = dec.place(w.t_begin + kTok);
     }
     lds_barrier();
     score(sa, 0);
     lds_barrier();                           // K(0) is read before K(1) overwrites it
     if (half == 0) {
-      dec.decode_keys(rk, kl);
-      dec.load_keys(rk, dec.place(w.t_begin + 2 * kTok));
+      dec.decode_keys(raw, kl);
+      dec.load_keys(raw, dec.place(w.t_begin + 2 * kTok));
       next = dec.place(w.t_begin + 3 * kTok);
     }
     lds_barrier();
@@ -602,29 +643,26 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem p, 
   lds_barrier();
   l += tops[0][rt][half ^ 1][c];
 
-  if (w.parts > 1) {
-    const int64_t unit = (static_cast<int64_t>(w.blk) * p.batch + w.b) * p.cache.heads + w.h;
-    constexpr int64_t kPart = part_floats(kThreads, N);
-    float* const parts = p.parts + unit * splits * kPart;
-    const int stat = wave * 32 + c;
-    store_part<kThreads>(parts + w.part * kPart, acc, m, l, stat);
-    if (!arrive_last(p.counters + unit * kCounterStride, static_cast<uint32_t>(w.parts), &flag)) return;
-    join_parts<kThreads>(parts, kPart, w.parts, stat, acc, m, l);
-  }
-  if (row.live) write_row<DT>(p, w, row, acc, m, l, half * N, half == 0);
-}
-
-hipError_t grid_of(const AttnProblem& p, const AttnPlan& plan, dim3* grid) {
-  const int64_t n = static_cast<int64_t>(plan.row_blocks) * plan.splits * p.batch * p.cache.heads;
-  if (n > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  *grid = dim3(static_cast<unsigned>(n));
-  return hipSuccess;
+  finish<DT, kThreads>(p, w, row, splits, acc, m, l, half * N);
 }
 
 template <int D, int NW>
-void launch(const AttnProblem& p, const AttnPlan& plan, dim3 grid, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_many_kernel<D, NW>), grid, dim3(64 * NW), 0, stream, p, plan.row_blocks,
+hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
+  constexpr int DT = D / 32, kThreads = D == 256 ? 512 : 64 * NW, N = D == 256 ? DT / 2 : DT;
+  const int64_t units = static_cast<int64_t>(plan.row_blocks) * p.batch * p.cache.heads;
+  if (units * plan.splits > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(units * plan.splits));
+  if constexpr (D == 256)
+    hipLaunchKernelGGL(attn_wide_kernel, grid, dim3(kThreads), 0, stream, p, plan.row_blocks, plan.splits);
+  else
+    hipLaunchKernelGGL((attn_many_kernel<D, NW>), grid, dim3(kThreads), 0, stream, p, plan.row_blocks,
+                       plan.splits);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || plan.splits == 1) return e;
+  hipLaunchKernelGGL((attn_join_kernel<DT, kThreads, N, D == 256 ? 2 : 1>),
+                     dim3(static_cast<unsigned>(units * (2 * N))), dim3(kThreads), 0, stream, p,
                      plan.splits);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -632,7 +670,7 @@ void launch(const AttnProblem& p, const AttnPlan& plan, dim3 grid, hipStream_t s
 AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim) {
   AttnPlan a = {};
   const int64_t rows = max_q * (q_heads / kv_heads), units = batch * kv_heads;
-  const int64_t most = head_dim == 256 ? 16 : 64;
+  const int64_t most = head_dim == 256 ? 32 : 64;
   a.few = rows <= most;
   if (a.few) {
     a.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
@@ -648,30 +686,22 @@ AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
   const int64_t block_rows = 32 * a.row_tiles;
   const int64_t blocks = (rows + block_rows - 1) / block_rows;
   a.row_blocks = static_cast<int>(blocks);
-  const int64_t fit = 512 / (blocks * units);
+  // Parts until a workgroup for every CU (two of four wavefronts) has its share of the keys.
+  const int64_t fit = (head_dim == 256 || a.row_tiles == 8 ? 256 : 512) / (blocks * units);
   a.splits = static_cast<int>(fit < 1 ? 1 : fit > 64 ? 64 : fit);
   if (a.splits > 1) {
-    a.counter_bytes = (blocks * units * 4 * kCounterStride + 255) / 256 * 256;
-    a.bytes = a.counter_bytes +
-              blocks * units * a.splits * 4 *
-                  (head_dim == 256 ? part_floats(512, 4) : part_floats(64 * a.row_tiles, head_dim / 32));
+    a.bytes = blocks * units * a.splits * 4 *
+              (head_dim == 256 ? part_floats(512, 4) : part_floats(64 * a.row_tiles, head_dim / 32));
   }
   return a;
 }
 
 hipError_t launch_attn_many(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
-  dim3 grid;
-  const hipError_t e = grid_of(p, plan, &grid);
-  if (e != hipSuccess) return e;
   const bool eight = plan.row_tiles == 8;
-  if (p.cache.head_dim == 64) {
-    eight ? launch<64, 8>(p, plan, grid, stream) : launch<64, 4>(p, plan, grid, stream);
-  } else if (p.cache.head_dim == 128) {
-    eight ? launch<128, 8>(p, plan, grid, stream) : launch<128, 4>(p, plan, grid, stream);
-  } else {
-    hipLaunchKernelGGL(attn_wide_kernel, grid, dim3(512), 0, stream, p, plan.row_blocks, plan.splits);
-  }
-  return hipGetLastError();
+  if (p.cache.head_dim == 64) return eight ? launch<64, 8>(p, plan, stream) : launch<64, 4>(p, plan, stream);
+  if (p.cache.head_dim == 128)
+    return eight ? launch<128, 8>(p, plan, stream) : launch<128, 4>(p, plan, stream);
+  return launch<256, 4>(p, plan, stream);
 }
 
 }  // namespace mx
