@@ -253,7 +253,8 @@ def mx_kv_append_fp4(cache, k, v, slots, positions=None, cos=None, sin=None, k_o
 
 
 def mx_attn_fp4_workspace_size(batch, max_q, q_heads, kv_heads, head_dim) -> int:
-    """Bytes of workspace mx_attn_fp4 needs for these sizes (whatever the lengths)."""
+    """Bytes of workspace mx_attn_fp4 needs for these sizes and all smaller batch and max_q, whatever
+    the lengths."""
     return int(load().mx_attn_fp4_workspace_size(batch, max_q, q_heads, kv_heads, head_dim))
 
 

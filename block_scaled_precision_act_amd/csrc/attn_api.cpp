@@ -256,7 +256,8 @@ int64_t mx_attn_fp4_workspace_size(int64_t batch, int64_t max_q, int64_t q_heads
       !head_dim_ok(head_dim) || batch > 65535 || kv_heads > 65535 || !fits31(max_q, q_heads) ||
       !fits31(batch, kv_heads))
     return 0;
-  return mx::plan_attn(batch, max_q, q_heads, kv_heads, static_cast<int>(head_dim)).bytes;
+  return mx::kCounterBytes +
+         mx::most_part_bytes(max_q, q_heads / kv_heads, static_cast<int>(head_dim));
 }
 
 int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
@@ -286,10 +287,11 @@ int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
   const mx::AttnPlan plan = mx::plan_attn(a->batch, a->max_q, a->q_heads, c.kv_heads,
                                           static_cast<int>(c.head_dim));
   // The deal of tiles of 128 tokens (plus a few slots for each sequence and head) counts in 31 bits.
-  if (plan.few && !fits31(a->batch * c.kv_heads, a->table_width * c.page_size / 128 + 8))
+  const int64_t units = a->batch * c.kv_heads;
+  if (plan.few && (units > mx::kMaxUnits || !fits31(units, a->table_width * c.page_size / 128 + 8)))
     return MX_ERR_SHAPE;
-  if (plan.bytes > 0 && (!a->workspace || a->workspace_bytes < plan.bytes ||
-                         !aligned(a->workspace, 256)))
+  if (plan.part_bytes > 0 && (!a->workspace || a->workspace_bytes < mx::kCounterBytes + plan.part_bytes ||
+                              !aligned(a->workspace, 256)))
     return MX_ERR_WORKSPACE;
   if ((st = device_status()) != MX_OK) return st;
   mx::AttnProblem p;
@@ -316,7 +318,8 @@ int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
   p.causal = a->causal != 0;
   p.window = static_cast<int32_t>(a->window);
   p.counters = static_cast<uint32_t*>(a->workspace);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + plan.counter_bytes);
+  p.counter_stride = mx::counter_stride(units);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + mx::kCounterBytes);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return status_of(plan.few ? mx::launch_attn_few(p, plan, s) : mx::launch_attn_many(p, plan, s));
 }

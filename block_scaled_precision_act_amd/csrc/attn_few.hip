@@ -529,7 +529,7 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
     }
     // The last workgroup to arrive joins the parts: its 16 lots of 16 threads take the tile's live
     // rows, and the parts by turns where rows leave lots over; the lots of a row are then joined.
-    if (!whole && arrive_last(p.counters + (static_cast<int64_t>(b) * heads + h) * kCounterStride, wg1 - wg0 + 1, &flag)) {
+    if (!whole && arrive_last(p.counters + (static_cast<int64_t>(b) * heads + h) * p.counter_stride, wg1 - wg0 + 1, &flag)) {
       const int lot = tid >> 4;
       for (int mt = 0; mt < MT && mt * 16 < sq.rows; ++mt) {
         const int live = min(16, sq.rows - mt * 16), turns = 16 / live;

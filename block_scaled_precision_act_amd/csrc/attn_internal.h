@@ -81,12 +81,22 @@ struct AttnProblem {
   uint32_t flip;             // 0x80008000 where scale < 0: the queries' signs are turned instead
   bool causal;
   int32_t window;
-  uint32_t* counters;        // few rows: one per (sequence, key/value head), zero between calls
+  uint32_t* counters;
+  uint32_t counter_stride;
   float* parts;
 };
 
-// Counters lie a cache line apart: arrivals on neighbouring ones would pass one line around the XCDs.
-constexpr int kCounterStride = 32;
+// A workspace begins with the arrival counters of few rows, one per (sequence, key/value head), zero
+// between calls; partial results follow at a fixed place, whatever the sizes, so calls of any sizes
+// can share a workspace.  Counters lie a cache line apart while that fits (arrivals on neighbouring
+// ones would pass one line around the XCDs).
+constexpr int64_t kCounterBytes = int64_t{8} << 20;
+constexpr int64_t kMaxUnits = kCounterBytes / 4;
+constexpr uint32_t counter_stride(int64_t units) {
+  uint32_t stride = 32;
+  while (stride > 1 && units * stride > kMaxUnits) stride /= 2;
+  return stride;
+}
 
 // How a problem's rows are dealt out, by its sizes alone.  A sequence's rows for one key/value
 // head are its (query, grouped head) pairs, max_q * group of them at most.
@@ -95,13 +105,15 @@ struct AttnPlan {
   int row_tiles;             // of a workgroup: 16-row tiles (few), wavefronts of 32 rows (many)
   int groups;                // few: workgroups that the cached tokens are dealt to
   int row_blocks, splits;    // many: blocks of rows for each (sequence, head), parts of the keys
-  int64_t counter_bytes, bytes;
+  int64_t part_bytes;        // of partial results
 };
 // Wavefronts of attn_few.hip that a SIMD holds (by their registers), and so workgroups a CU.
 constexpr int few_waves(int head_dim, int row_tiles) {
   return head_dim * row_tiles <= 128 ? 3 : head_dim * row_tiles <= 256 ? 2 : 1;
 }
 AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim);
+// Partial results of any plan with at most max_q queries a sequence.
+int64_t most_part_bytes(int64_t max_q, int64_t group, int head_dim);
 
 hipError_t launch_attn_few(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream);
 hipError_t launch_attn_many(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream);

@@ -16,6 +16,8 @@
 // their weights pass through LDS.
 #include "attn_common.h"
 
+#include <algorithm>
+
 namespace mx {
 namespace {
 
@@ -667,33 +669,54 @@ hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream
 
 }  // namespace
 
+namespace {
+
+// Rows that go with the few: more than twice the sequences' rows of one 16-row tile hold for heads of
+// 64 and 128 (4 tiles; 64 rows of 8000 keys: 71 us, 83 us with the many), 2 tiles for heads of 256
+// (32 rows of 8000 keys: 45 us against 96 us).
+constexpr int few_tiles(int head_dim) { return head_dim == 256 ? 2 : 4; }
+
+constexpr int64_t few_part_bytes(int head_dim, int row_tiles) {
+  return int64_t{2} * 256 * few_waves(head_dim, row_tiles) * 16 * row_tiles * (head_dim + 2) * 4;
+}
+
+// Threads of the workgroups that the parts of a problem of many rows keep at most: a workgroup for
+// every CU (two of four wavefronts).
+constexpr int64_t kPartThreads = 256 * 512;
+
+}  // namespace
+
 AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim) {
   AttnPlan a = {};
   const int64_t rows = max_q * (q_heads / kv_heads), units = batch * kv_heads;
-  const int64_t most = head_dim == 256 ? 32 : 64;
-  a.few = rows <= most;
+  a.few = rows <= 16 * few_tiles(head_dim);
   if (a.few) {
     a.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     a.groups = 256 * few_waves(head_dim, a.row_tiles);
-    a.counter_bytes = (units * 4 * kCounterStride + 255) / 256 * 256;
-    a.bytes = a.counter_bytes +
-              2 * static_cast<int64_t>(a.groups) * 16 * a.row_tiles * (head_dim + 2) * 4;
+    a.part_bytes = few_part_bytes(head_dim, a.row_tiles);
     return a;
   }
   // Eight wavefronts of 32 rows share the decoding where there are rows for them; with heads of 256,
   // eight share 128 rows.
   a.row_tiles = head_dim == 256 || rows <= 128 ? 4 : 8;
-  const int64_t block_rows = 32 * a.row_tiles;
+  const int64_t block_rows = 32 * a.row_tiles, threads = head_dim == 256 ? 512 : 64 * a.row_tiles;
   const int64_t blocks = (rows + block_rows - 1) / block_rows;
   a.row_blocks = static_cast<int>(blocks);
-  // Parts until a workgroup for every CU (two of four wavefronts) has its share of the keys.
-  const int64_t fit = (head_dim == 256 || a.row_tiles == 8 ? 256 : 512) / (blocks * units);
+  const int64_t fit = kPartThreads / threads / (blocks * units);
   a.splits = static_cast<int>(fit < 1 ? 1 : fit > 64 ? 64 : fit);
-  if (a.splits > 1) {
-    a.bytes = blocks * units * a.splits * 4 *
-              (head_dim == 256 ? part_floats(512, 4) : part_floats(64 * a.row_tiles, head_dim / 32));
-  }
+  if (a.splits > 1)
+    a.part_bytes = blocks * units * a.splits * 4 * part_floats(threads, head_dim == 64 ? 2 : 4);
   return a;
+}
+
+int64_t most_part_bytes(int64_t max_q, int64_t group, int head_dim) {
+  const int64_t rows = max_q * group;
+  int64_t most = 0;
+  for (int t = 1; t <= few_tiles(head_dim); t *= 2)
+    if (t == 1 || rows > 8 * t) most = std::max(most, few_part_bytes(head_dim, t));
+  if (rows > 16 * few_tiles(head_dim))
+    most = std::max(most, kPartThreads * 4 * (16 * (head_dim == 64 ? 2 : 4) + 1));
+  return most;
 }
 
 hipError_t launch_attn_many(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {

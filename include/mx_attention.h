@@ -164,10 +164,14 @@ int mx_kv_append_fp4(const mx_kv_append_fp4_args* args, void* stream);
  * seq_lens, q_starts and page_table entries are read on the device: lengths are clamped to what
  * the table covers, and an entry outside [0, pages) reads page 0 instead of memory that is not
  * the cache's.
- * workspace: mx_attn_fp4_workspace_size bytes (it depends on the sizes alone, not on lengths),
- * 256-byte aligned, zero before its first use and left reusable by every call; calls that may
- * overlap need workspaces of their own.  q and out rows must be 16-byte aligned (bases 16-byte
- * aligned, strides multiples of 8 elements).
+ * workspace: mx_attn_fp4_workspace_size bytes, 256-byte aligned, zero before its first use and left
+ * reusable by every call; the size depends on the sizes alone, not on lengths, and suffices for every
+ * smaller max_q and batch too.  One workspace serves calls of any sizes it is large enough for;
+ * calls that may overlap need workspaces of their own.  q and out rows must be 16-byte aligned
+ * (bases 16-byte aligned, strides multiples of 8 elements).
+ * At most 64 rows (queries of a sequence times q_heads / kv_heads; 32 with heads of 256) take a path
+ * bound by reading the cache, for at most 2^21 sequences times kv_heads; more rows one bound by the
+ * matrix instructions.
  * Rounding: products of bf16 queries and exactly decoded keys are summed in fp32; weights
  * exp(s - m) are rounded to bf16 for their product with the exactly decoded values, summed in
  * fp32; the softmax's maximum and sum stay in fp32.

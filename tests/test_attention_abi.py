@@ -182,7 +182,7 @@ def test_append(lib, change, status):
     (dict(page_table=0), mx.MX_ERR_NULL), (dict(seq_lens=0), mx.MX_ERR_NULL), (dict(q=0), mx.MX_ERR_NULL),
     (dict(out=0), mx.MX_ERR_NULL), (dict(q=A + 8), mx.MX_ERR_ALIGN), (dict(out_token_stride=516), mx.MX_ERR_ALIGN),
     (dict(out_head_stride=120), mx.MX_ERR_STRIDE), (dict(workspace=0), mx.MX_ERR_WORKSPACE),
-    (dict(workspace_bytes=1000), mx.MX_ERR_WORKSPACE), (dict(workspace=A + 16), mx.MX_ERR_WORKSPACE),
+    (dict(workspace_bytes=1 << 23), mx.MX_ERR_WORKSPACE), (dict(workspace=A + 16), mx.MX_ERR_WORKSPACE),
     (dict(batch=0, total_q=0, q=0), mx.MX_OK), (dict(total_q=0, q_starts=A, q=0), mx.MX_OK),
     ({}, "device"), (dict(q_token_stride=0), "device"), (dict(q_starts=A, total_q=1), "device")])
 def test_attn(lib, change, status):
@@ -207,10 +207,29 @@ def test_attn_page_number_arithmetic_bound(lib):
 
 def test_attn_workspace_size(lib):
     size = mx.mx_attn_fp4_workspace_size
-    assert size(1, 1, 32, 8, 128) > 0 and size(1, 1, 32, 8, 128) == size(1, 1, 40, 8, 128)
-    assert size(4, 8192, 32, 8, 128) == 0                 # enough blocks of rows: no parts to join
+    assert size(1, 1, 32, 8, 128) > 0
+    for hq, hk, d in ((32, 8, 128), (6, 6, 64), (16, 1, 256), (128, 1, 128)):
+        got = [size(b, n, hq, hk, d) for b in (1, 64) for n in (1, 2, 3, 5, 9, 17, 40, 300, 5000)]
+        assert got == sorted(got[:9]) * 2                 # grows with max_q, whatever the batch
     for bad in ((0, 1, 32, 8, 128), (1, 0, 32, 8, 128), (1, 1, 30, 8, 128), (1, 1, 32, 8, 80), (70000, 1, 32, 8, 128)):
         assert size(*bad) == 0
+
+
+def test_attn_takes_the_queried_workspace_for_every_smaller_call(lib):
+    # sizes pass the workspace check (they reach the device check) with what the largest one asks for
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is visible: fake addresses must not reach it")
+    keep = []
+    cache = _cache_address(keep)
+    for top in (1, 7, 64, 3000):
+        need = mx.mx_attn_fp4_workspace_size(8, top, 4, 2, 128)
+        for batch in (1, 3, 8):
+            for n in {1, 2, 5, 8, 9, 16, 17, 31, 32, 33, 64, 65, 128, 500, 3000}:
+                if n > top:
+                    continue
+                args = {**ATTN, "cache": cache, "batch": batch, "max_q": n, "total_q": batch * n,
+                        "workspace_bytes": need}
+                assert lib.mx_attn_fp4(_pack("mx_attn_fp4_args", args), None) == mx.MX_ERR_DEVICE, (top, batch, n)
 
 
 def test_host_tensors_are_refused_before_any_library_call():

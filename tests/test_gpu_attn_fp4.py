@@ -236,6 +236,20 @@ def test_workspace_is_left_reusable_and_bits_repeat(mx, nq, lens):
     attention_close(out, l, oracle(other, q2, uniform(nq, 2), 128 ** -0.5))
 
 
+def test_one_workspace_for_calls_of_all_sizes(mx):
+    # few rows, many rows in parts, other batches and head sizes in turn
+    rng = np.random.default_rng(14)
+    ws = torch.zeros(max(mx.mx_attn_fp4_workspace_size(8, 200, 8, 2, d) for d in (64, 128, 256)),
+                     dtype=torch.uint8, device="cuda")
+    for D, lens, nq in ((128, [900, 2000], 100), (128, [1500] * 8, 1), (256, [1100], 40), (64, [2600, 5, 700], 3),
+                        (256, [3000, 1], 2), (128, [2500], 1), (64, [900], 200), (128, [1500, 800] * 4, 2)):
+        paged = Paged(rng, lens, 2, D, 16)
+        q = queries(rng, nq * len(lens), 8, D)
+        note(f"attn shared workspace D={D} nq={nq} batch={len(lens)}")
+        out, lse = run(mx, paged, q, ws=ws)
+        attention_close(out, lse, oracle(paged, q, uniform(nq, len(lens)), D ** -0.5), f"{D} {nq}")
+
+
 def test_streams_and_graph_replay(mx):
     rng = np.random.default_rng(12)
     paged = Paged(rng, [1000, 700], 2, 128, 16)
@@ -296,7 +310,7 @@ def test_binding_refusals(mx):
     refused(mx.MX_ERR_STRIDE, page_table=table.t().contiguous().t() if table.shape[1] > 1 and table.shape[0] > 1
             else torch.zeros(1, 8, dtype=torch.int32, device="cuda")[:, ::2])
     refused(mx.MX_ERR_WORKSPACE, workspace=None)
-    refused(mx.MX_ERR_WORKSPACE, workspace=ws[:-256])
+    refused(mx.MX_ERR_WORKSPACE, workspace=ws[:1 << 23])
     refused(mx.MX_ERR_SHAPE, window=5, causal=False)
     refused(mx.MX_ERR_SHAPE, window=-1)
     refused(mx.MX_ERR_SHAPE, max_q=2)                               # 2 rows in q expected
