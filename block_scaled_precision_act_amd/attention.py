@@ -55,27 +55,28 @@ def _need(fn: str, t, what: str, dtype, dev: int):
         raise TypeError(f"{fn}: {what} must be {dtype}, got {t.dtype}")
 
 
-def _heads(fn: str, t, what: str, dev: int, tokens=None, heads=None, dim=None):
+def _heads(fn: str, t, what: str, dev: int, shape=None):
     """Pointer, token and head stride of bf16 heads [tokens, heads, dim] with contiguous values."""
-    _need(fn, t, what, _bf16, dev)
-    sh = t.shape
-    if len(sh) != 3 or (tokens is not None and (sh[0] != tokens or sh[1] != heads or sh[2] != dim)):
-        want = "[tokens, heads, head_dim]" if tokens is None else f"[{tokens}, {heads}, {dim}]"
-        raise MxError(fn, MX_ERR_SHAPE, f"{what} has shape {tuple(sh)}, expected {want}")
-    a, b, c = t.stride()
-    if c != 1 and sh[2] > 1:
-        raise MxError(fn, MX_ERR_STRIDE, f"{what}'s head values are not contiguous ({t.stride()})")
-    return t.data_ptr(), a if sh[0] > 1 else 0, b if sh[1] > 1 else 0
+    if isinstance(t, _Tensor) and t.dtype is _bf16 and t.get_device() == dev >= 0:
+        sh, st = t.shape, t.stride()
+        if len(sh) == 3 and (shape is None or sh == shape) and (st[2] == 1 or sh[2] <= 1):
+            return t.data_ptr(), st[0] if sh[0] > 1 else 0, st[1] if sh[1] > 1 else 0
+    _need(fn, t, what, _bf16, dev)                # what is wrong with it
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        want = "[tokens, heads, head_dim]" if shape is None else list(shape)
+        raise MxError(fn, MX_ERR_SHAPE, f"{what} has shape {tuple(t.shape)}, expected {want}")
+    raise MxError(fn, MX_ERR_STRIDE, f"{what}'s head values are not contiguous ({t.stride()})")
 
 
-def _flat(fn: str, t, what: str, dtype, dev: int, *shape):
+def _flat(fn: str, t, what: str, dtype, dev: int, shape):
     """Pointer of a contiguous tensor of exactly `shape`."""
-    _need(fn, t, what, dtype, dev)
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 and \
+            t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _need(fn, t, what, dtype, dev)                # what is wrong with it
     if t.shape != shape:
         raise MxError(fn, MX_ERR_SHAPE, f"{what} has shape {tuple(t.shape)}, expected {list(shape)}")
-    if not t.is_contiguous():
-        raise MxError(fn, MX_ERR_STRIDE, f"{what} is not contiguous ({t.stride()})")
-    return t.data_ptr()
+    raise MxError(fn, MX_ERR_STRIDE, f"{what} is not contiguous ({t.stride()})")
 
 
 def _rotation(fn: str, positions, cos, sin, tokens: int, dev: int):
@@ -84,12 +85,13 @@ def _rotation(fn: str, positions, cos, sin, tokens: int, dev: int):
         if cos is not None or sin is not None:
             raise TypeError(f"{fn}: cos and sin need positions")
         return 0, 0, 0, 0, 0
-    pp = _flat(fn, positions, "positions", _i32, dev, tokens)
-    _need(fn, cos, "cos", _f32, dev)
+    if not isinstance(cos, _Tensor):
+        raise TypeError(f"{fn}: cos must be a torch tensor, got {type(cos).__name__}")
     sh = cos.shape
     if len(sh) != 2:
         raise MxError(fn, MX_ERR_SHAPE, f"cos has shape {tuple(sh)}, expected [positions, rot / 2]")
-    return (pp, _flat(fn, cos, "cos", _f32, dev, *sh), _flat(fn, sin, "sin", _f32, dev, *sh),
+    return (_flat(fn, positions, "positions", _i32, dev, (tokens,)),
+            _flat(fn, cos, "cos", _f32, dev, sh), _flat(fn, sin, "sin", _f32, dev, sh),
             sh[0], 2 * sh[1])
 
 
@@ -169,16 +171,16 @@ def mx_qk_norm_rope(q, k, positions, cos, sin, q_out, k_out, q_weight=None, k_we
     fn, dev = "mx_qk_norm_rope", _current_device()
     qp, qt, qh = _heads(fn, q, "q", dev)
     T, Hq, D = q.shape
-    qop, qot, qoh = _heads(fn, q_out, "q_out", dev, T, Hq, D)
+    qop, qot, qoh = _heads(fn, q_out, "q_out", dev, q.shape)
     kp = kt = kh = kop = kot = koh = Hk = 0
     if k is not None:
         kp, kt, kh = _heads(fn, k, "k", dev)
         Hk = k.shape[1]
         if k.shape[0] != T or k.shape[2] != D:
             raise MxError(fn, MX_ERR_SHAPE, f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
-        kop, kot, koh = _heads(fn, k_out, "k_out", dev, T, Hk, D)
-    qw = 0 if q_weight is None else _flat(fn, q_weight, "q_weight", _bf16, dev, D)
-    kw = 0 if k_weight is None else _flat(fn, k_weight, "k_weight", _bf16, dev, D)
+        kop, kot, koh = _heads(fn, k_out, "k_out", dev, k.shape)
+    qw = 0 if q_weight is None else _flat(fn, q_weight, "q_weight", _bf16, dev, (D,))
+    kw = 0 if k_weight is None else _flat(fn, k_weight, "k_weight", _bf16, dev, (D,))
     pp, cp, sp, rows, rot = _rotation(fn, positions, cos, sin, T, dev)
     st = load().mx_qk_norm_rope(
         _NORM_ROPE.pack(qp, kp, qop, kop, qw, kw, pp, cp, sp, qt, qh, kt, kh, qot, qoh, kot, koh,
@@ -201,20 +203,20 @@ def mx_qk_norm_rope_backward(dq_out, dk_out, q, k, positions, cos, sin, dq, dk, 
     fn, dev = "mx_qk_norm_rope_backward", _current_device()
     qp, qt, qh = _heads(fn, q, "q", dev)
     T, Hq, D = q.shape
-    gqp, gqt, gqh = _heads(fn, dq_out, "dq_out", dev, T, Hq, D)
-    dqp, dqt, dqh = _heads(fn, dq, "dq", dev, T, Hq, D)
+    gqp, gqt, gqh = _heads(fn, dq_out, "dq_out", dev, q.shape)
+    dqp, dqt, dqh = _heads(fn, dq, "dq", dev, q.shape)
     kp = kt = kh = gkp = gkt = gkh = dkp = dkt = dkh = Hk = 0
     if k is not None:
         kp, kt, kh = _heads(fn, k, "k", dev)
         Hk = k.shape[1]
         if k.shape[0] != T or k.shape[2] != D:
             raise MxError(fn, MX_ERR_SHAPE, f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
-        gkp, gkt, gkh = _heads(fn, dk_out, "dk_out", dev, T, Hk, D)
-        dkp, dkt, dkh = _heads(fn, dk, "dk", dev, T, Hk, D)
-    qw = 0 if q_weight is None else _flat(fn, q_weight, "q_weight", _bf16, dev, D)
-    kw = 0 if k_weight is None else _flat(fn, k_weight, "k_weight", _bf16, dev, D)
-    dqw = 0 if dq_weight is None else _flat(fn, dq_weight, "dq_weight", _f32, dev, D)
-    dkw = 0 if dk_weight is None else _flat(fn, dk_weight, "dk_weight", _f32, dev, D)
+        gkp, gkt, gkh = _heads(fn, dk_out, "dk_out", dev, k.shape)
+        dkp, dkt, dkh = _heads(fn, dk, "dk", dev, k.shape)
+    qw = 0 if q_weight is None else _flat(fn, q_weight, "q_weight", _bf16, dev, (D,))
+    kw = 0 if k_weight is None else _flat(fn, k_weight, "k_weight", _bf16, dev, (D,))
+    dqw = 0 if dq_weight is None else _flat(fn, dq_weight, "dq_weight", _f32, dev, (D,))
+    dkw = 0 if dk_weight is None else _flat(fn, dk_weight, "dk_weight", _f32, dev, (D,))
     pp, cp, sp, rows, rot = _rotation(fn, positions, cos, sin, T, dev)
     wp, wb = _workspace(fn, workspace, dev)
     st = load().mx_qk_norm_rope_backward(
@@ -240,11 +242,11 @@ def mx_kv_append_fp4(cache, k, v, slots, positions=None, cos=None, sin=None, k_o
     if H != cache.kv_heads or D != cache.head_dim:
         raise MxError(fn, MX_ERR_SHAPE, f"k has shape {tuple(k.shape)}, the cache "
                                         f"{cache.kv_heads} heads of {cache.head_dim}")
-    vp, vt, vh = _heads(fn, v, "v", dev, T, H, D)
-    sp_ = _flat(fn, slots, "slots", _i64, dev, T)
+    vp, vt, vh = _heads(fn, v, "v", dev, k.shape)
+    sp_ = _flat(fn, slots, "slots", _i64, dev, (T,))
     pp, cp, sp, rows, rot = _rotation(fn, positions, cos, sin, T, dev)
-    ko = 0 if k_out is None else _flat(fn, k_out, "k_out", _bf16, dev, T, H, D)
-    vo = 0 if v_out is None else _flat(fn, v_out, "v_out", _bf16, dev, T, H, D)
+    ko = 0 if k_out is None else _flat(fn, k_out, "k_out", _bf16, dev, k.shape)
+    vo = 0 if v_out is None else _flat(fn, v_out, "v_out", _bf16, dev, k.shape)
     st = load().mx_kv_append_fp4(
         _APPEND.pack(cache._addr, kp, vp, sp_, pp, cp, sp, ko, vo, kt, kh, vt, vh, T, rows, rot,
                      interleaved), _stream(stream, dev))
@@ -274,7 +276,7 @@ def mx_attn_fp4(cache, q, page_table, seq_lens, out, workspace, q_starts=None, m
     N, H, D = q.shape
     if D != cache.head_dim:
         raise MxError(fn, MX_ERR_SHAPE, f"q has head_dim {D}, the cache {cache.head_dim}")
-    op, ot, oh = _heads(fn, out, "out", dev, N, H, D)
+    op, ot, oh = _heads(fn, out, "out", dev, q.shape)
     _need(fn, page_table, "page_table", _i32, dev)
     if page_table.dim() != 2:
         raise MxError(fn, MX_ERR_SHAPE, f"page_table has shape {tuple(page_table.shape)}, expected "
@@ -283,15 +285,15 @@ def mx_attn_fp4(cache, q, page_table, seq_lens, out, workspace, q_starts=None, m
     if width > 1 and page_table.stride(1) != 1:
         raise MxError(fn, MX_ERR_STRIDE, f"page_table's rows are not contiguous "
                                          f"({page_table.stride()})")
-    lens = _flat(fn, seq_lens, "seq_lens", _i32, dev, B)
+    lens = _flat(fn, seq_lens, "seq_lens", _i32, dev, (B,))
     starts = 0
     if q_starts is not None:
-        starts = _flat(fn, q_starts, "q_starts", _i32, dev, B + 1)
+        starts = _flat(fn, q_starts, "q_starts", _i32, dev, (B + 1,))
         if max_q is None:
             raise TypeError(f"{fn}: q_starts needs max_q")
     elif max_q is None:
         max_q = N // B if B else 0
-    lp = 0 if lse is None else _flat(fn, lse, "lse", _f32, dev, N, H)
+    lp = 0 if lse is None else _flat(fn, lse, "lse", _f32, dev, (N, H))
     wp, wb = _workspace(fn, workspace, dev)
     st = load().mx_attn_fp4(
         _ATTN.pack(cache._addr, qp, op, lp, page_table.data_ptr(), lens, starts, wp, wb, qt, qh,

@@ -58,6 +58,18 @@ __device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
   x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
 }
 
+// Past the caches: the values as stored are most of what is written (16384 x 8 heads of 128: 34 us, 39
+// us without).
+__device__ __forceinline__ void store_stream(uint16_t* p, uint4 v) {
+  __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p));
+}
+
+// Values are read once (keys by two lanes, where they are rotated): 2 us less.
+__device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
+  const v4u t = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
+  return make_uint4(t[0], t[1], t[2], t[3]);
+}
+
 // (a, b) -> a c + b s with both products and the sum rounded (no fused multiply-add).
 __device__ __forceinline__ float turned(float a, float c, float b, float s) {
 #pragma clang fp contract(off)
@@ -66,33 +78,66 @@ __device__ __forceinline__ float turned(float a, float c, float b, float s) {
   return ac + bs;
 }
 
-template <int LR>
-__global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvAppendProblem p) {
+// A row's owners handle U heads of one token, all loaded before the first is used; the token's slot and
+// table entries are loaded once.
+template <int LR, int U>
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvAppendProblem p, uint32_t units) {
   constexpr int D = 8 * LR, RG = kThreads / LR;
   const int j = threadIdx.x % LR;
-  const uint32_t total = p.tokens * p.cache.heads;
-  const uint32_t row = blockIdx.x * RG + threadIdx.x / LR;
-  if (row >= total) return;               // whole rows leave together
-  const uint32_t t = row / p.cache.heads, h = row - t * p.cache.heads;
+  const uint32_t unit = blockIdx.x * RG + threadIdx.x / LR;
+  if (unit >= p.tokens * units) return;   // whole rows leave together
+  const uint32_t t = unit / units, h0 = (unit - t * units) * U, heads = p.cache.heads;
+  const uint16_t* const kt = p.k.p + t * p.k.token_stride + h0 * p.k.head_stride;
+  const uint16_t* const vt = p.v.p + t * p.v.token_stride + h0 * p.v.head_stride;
+  const int rot = p.rot.positions ? p.rot.rot : 0, half = rot >> 1;
+  const bool turns = 8 * j < rot, halves = turns && !p.rot.interleaved;
+  // rot % 16 == 0: the lane's 8 values lie on one side of rot / 2.
+  const bool upper = 8 * j >= half;
+  const int partner = upper ? 8 * j - half : 8 * j + half;
+  uint4 kw[U], vw[U], ow[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t at = h0 + u < heads ? u : 0;
+    const uint16_t* row = kt + at * p.k.head_stride;
+    kw[u] = *reinterpret_cast<const uint4*>(row + 8 * j);
+    ow[u] = halves ? *reinterpret_cast<const uint4*>(row + partner) : make_uint4(0, 0, 0, 0);
+    vw[u] = load_stream(vt + at * p.v.head_stride + 8 * j);
+  }
   const int64_t slot = p.slots[t];
-  if (slot < 0 || slot >= static_cast<int64_t>(p.cache.pages) * p.cache.page_size) return;
-  const uint16_t* krow = p.k.p + t * p.k.token_stride + h * p.k.head_stride;
-  const uint16_t* vrow = p.v.p + t * p.v.token_stride + h * p.v.head_stride;
-  float k[8], v[8];
-  widen(*reinterpret_cast<const uint4*>(krow + 8 * j), k);
-  widen(*reinterpret_cast<const uint4*>(vrow + 8 * j), v);
-  bool bad = false;
-  if (p.rot.positions) {
+  bool lost = false;                      // the position is outside the table
+  float cc[8], ss[8];
+  if (rot) {
     const uint32_t pos = static_cast<uint32_t>(p.rot.positions[t]);
-    bad = pos >= p.rot.rows;
-    const int rot = p.rot.rot, half = rot >> 1;
-    if (!bad && 8 * j < rot) {
-      const float* cs = p.rot.cos + static_cast<int64_t>(pos) * half;
-      const float* sn = p.rot.sin + static_cast<int64_t>(pos) * half;
+    lost = pos >= p.rot.rows;
+    if (turns && !lost) {
+      const int64_t at = static_cast<int64_t>(pos) * half + (p.rot.interleaved ? 4 * j : upper ? 8 * j - half : 8 * j);
+      const float4 c0 = *reinterpret_cast<const float4*>(p.rot.cos + at);
+      const float4 s0 = *reinterpret_cast<const float4*>(p.rot.sin + at);
+      float4 c1 = c0, s1 = s0;
+      if (halves) {
+        c1 = *reinterpret_cast<const float4*>(p.rot.cos + at + 4);
+        s1 = *reinterpret_cast<const float4*>(p.rot.sin + at + 4);
+      }
+      cc[0] = c0.x; cc[1] = c0.y; cc[2] = c0.z; cc[3] = c0.w;
+      cc[4] = c1.x; cc[5] = c1.y; cc[6] = c1.z; cc[7] = c1.w;
+      ss[0] = s0.x; ss[1] = s0.y; ss[2] = s0.z; ss[3] = s0.w;
+      ss[4] = s1.x; ss[5] = s1.y; ss[6] = s1.z; ss[7] = s1.w;
+    }
+  }
+  if (slot < 0 || slot >= static_cast<int64_t>(p.cache.pages) * p.cache.page_size) return;
+  const uint32_t page = static_cast<uint32_t>(slot) / p.cache.page_size;
+  const uint32_t off = static_cast<uint32_t>(slot) - page * p.cache.page_size;
+  const int64_t code0 = page * p.cache.code_page + off * (D / 2) + 4 * j;
+  const int64_t scale0 = page * p.cache.scale_page + off * (D / 32) + j / 4;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t h = h0 + u;
+    if (h >= heads) break;
+    float k[8], v[8];
+    widen(kw[u], k);
+    widen(vw[u], v);
+    if (turns && !lost) {
       if (p.rot.interleaved) {
-        const float4 c = *reinterpret_cast<const float4*>(cs + 4 * j);
-        const float4 s = *reinterpret_cast<const float4*>(sn + 4 * j);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float a = k[2 * i], b = k[2 * i + 1];
@@ -100,57 +145,55 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvAppendProbl
           k[2 * i + 1] = turned(b, cc[i], a, ss[i]);
         }
       } else {
-        // rot % 16 == 0: the lane's 8 values lie on one side of rot / 2.
-        const bool upper = 8 * j >= half;
-        const int at = upper ? 8 * j - half : 8 * j;
         float o[8];
-        widen(*reinterpret_cast<const uint4*>(krow + (upper ? 8 * j - half : 8 * j + half)), o);
-        const float4 c0 = *reinterpret_cast<const float4*>(cs + at);
-        const float4 c1 = *reinterpret_cast<const float4*>(cs + at + 4);
-        const float4 s0 = *reinterpret_cast<const float4*>(sn + at);
-        const float4 s1 = *reinterpret_cast<const float4*>(sn + at + 4);
-        const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        widen(ow[u], o);
 #pragma unroll
         for (int e = 0; e < 8; ++e) k[e] = turned(k[e], cc[e], o[e], upper ? ss[e] : -ss[e]);
       }
     }
+    // A value that no finite code stands for anywhere in the token's key or value (of this head) makes
+    // the whole row NaN, through the key's scales.
+    const uint32_t ktop = block_top(k), vtop = block_top(v);
+    const uint64_t votes = __ballot(lost || ktop > kLargest || vtop > kLargest);
+    constexpr uint64_t kMine = (uint64_t{1} << LR) - 1;
+    const bool bad = ((votes >> (threadIdx.x % 64 / LR * LR)) & kMine) != 0;
+    Quantized qk = quantize(k, ktop), qv = quantize(v, vtop);
+    if (bad) {
+      qk = {0u, 255u};
+      qv = {0u, 127u};
+    }
+    const int64_t code = code0 + h * p.cache.code_head, scale = scale0 + h * p.cache.scale_head;
+    *reinterpret_cast<uint32_t*>(p.cache.k + code) = qk.codes;
+    *reinterpret_cast<uint32_t*>(p.cache.v + code) = qv.codes;
+    if (j % 4 == 0) {
+      p.cache.ks[scale] = static_cast<uint8_t>(qk.byte);
+      p.cache.vs[scale] = static_cast<uint8_t>(qv.byte);
+    }
+    const int64_t out = (static_cast<int64_t>(t) * heads + h) * D + 8 * j;
+    const uint4 nan = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+    if (p.k_out) store_stream(p.k_out + out, bad ? nan : stored_values(qk));
+    if (p.v_out) store_stream(p.v_out + out, bad ? nan : stored_values(qv));
   }
-  // A value that no finite code stands for anywhere in the token's key or value (of this head)
-  // makes the whole row NaN, through the key's scales.
-  const uint32_t ktop = block_top(k), vtop = block_top(v);
-  const uint64_t votes = __ballot(bad || ktop > kLargest || vtop > kLargest);
-  const uint64_t mine = LR == 64 ? ~uint64_t{0} : ((uint64_t{1} << LR) - 1);
-  bad = ((votes >> (threadIdx.x % 64 / LR * LR)) & mine) != 0;
-  Quantized qk = quantize(k, ktop), qv = quantize(v, vtop);
-  uint4 ko = stored_values(qk), vo = stored_values(qv);
-  if (bad) {
-    qk = {0u, 255u};
-    qv = {0u, 127u};
-    ko = vo = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-  }
-  const uint32_t page = static_cast<uint32_t>(slot) / p.cache.page_size;
-  const uint32_t off = static_cast<uint32_t>(slot) - page * p.cache.page_size;
-  const int64_t code = page * p.cache.code_page + h * p.cache.code_head + off * (D / 2) + 4 * j;
-  const int64_t scale = page * p.cache.scale_page + h * p.cache.scale_head + off * (D / 32) + j / 4;
-  *reinterpret_cast<uint32_t*>(p.cache.k + code) = qk.codes;
-  *reinterpret_cast<uint32_t*>(p.cache.v + code) = qv.codes;
-  if (j % 4 == 0) {
-    p.cache.ks[scale] = static_cast<uint8_t>(qk.byte);
-    p.cache.vs[scale] = static_cast<uint8_t>(qv.byte);
-  }
-  const int64_t out = static_cast<int64_t>(row) * D + 8 * j;
-  if (p.k_out) *reinterpret_cast<uint4*>(p.k_out + out) = ko;
-  if (p.v_out) *reinterpret_cast<uint4*>(p.v_out + out) = vo;
 }
+
+template <int LR, int U>
+hipError_t launch_u(const KvAppendProblem& p, hipStream_t stream) {
+  constexpr int RG = kThreads / LR;
+  const uint32_t units = (p.cache.heads + U - 1) / U;
+  const uint64_t all = static_cast<uint64_t>(p.tokens) * units;
+  hipLaunchKernelGGL((kv_append_kernel<LR, U>), dim3(static_cast<unsigned>((all + RG - 1) / RG)),
+                     dim3(kThreads), 0, stream, p, units);
+  return hipGetLastError();
+}
+
+// From this many rows on a row's owners take two heads at once; below, the rows alone do not fill the
+// chip.
+constexpr uint64_t kManyRows = 32768;
 
 template <int LR>
 hipError_t launch(const KvAppendProblem& p, hipStream_t stream) {
-  constexpr int RG = kThreads / LR;
-  const uint64_t rows = static_cast<uint64_t>(p.tokens) * p.cache.heads;
-  hipLaunchKernelGGL((kv_append_kernel<LR>), dim3(static_cast<unsigned>((rows + RG - 1) / RG)),
-                     dim3(kThreads), 0, stream, p);
-  return hipGetLastError();
+  return static_cast<uint64_t>(p.tokens) * p.cache.heads >= kManyRows ? launch_u<LR, 2>(p, stream)
+                                                                     : launch_u<LR, 1>(p, stream);
 }
 
 }  // namespace
