@@ -18,9 +18,11 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// From this many rows on a row's owners take four heads at once (more loads in flight); below, the
-// rows alone do not fill the chip.
-constexpr uint64_t kManyRows = 32768;
+// From this many values on a row's owners take four heads at once (more loads in flight); below, one,
+// as the rows then do not fill the chip.  Four and one: forward, 3.1 M values 5.1 and 4.8 us, 6.1 M 6.2
+// and 7.9 us; backward (its workgroups are 511 at most), 0.8 M 9.4 and 9.1 us, 1.5 M 10.1 and 12.8 us
+// (heads of 128; 64 and 256 cross over within the same steps).
+constexpr uint64_t kManyForward = uint64_t{1} << 22, kManyBackward = uint64_t{1} << 20;
 
 // Sum over the LR lanes that own a row, by DPP: quads, then mirrors of 8 and 16 lanes (whose quads
 // and halves already hold equal sums), then the two rows of 16.  All lanes are active.
@@ -81,7 +83,7 @@ __device__ __forceinline__ void load8(const uint16_t* row, const LaneChunks& lc,
 }
 
 // Rows are loaded and stored past the caches, each being read or written once: 16384 x 40 heads of 128
-// take 61 us so (68 us through the caches), their gradients 99 us (107 us).
+// take 60 us so (68 us through the caches), their gradients 100 us (107 us): 5.6 and 5.0 TB/s.
 __device__ __forceinline__ void load_stream(const uint16_t* row, const LaneChunks& lc, uint2* lo, uint2* hi) {
   const v2u a = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(row + lc.c0));
   const v2u b = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(row + lc.c1));
@@ -254,10 +256,17 @@ __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRope
   const float* parts_i = p.parts + static_cast<int64_t>(i ? groups_q : 0) * D;
   const int d4 = threadIdx.x % L4, run = threadIdx.x / L4;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (uint32_t g = run; g < groups; g += RUNS) {
-    const float4 a = *reinterpret_cast<const float4*>(parts_i + static_cast<int64_t>(g) * D + 4 * d4);
-    v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+  // Loads in flight; their latency is what the join costs (48000 rows of 256: 29.5 us, 32.2 with 8).
+  constexpr int kBatch = 16;
+  for (uint32_t g0 = run; g0 < groups; g0 += kBatch * RUNS) {
+    float4 a[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      a[b] = *reinterpret_cast<const float4*>(
+          parts_i + static_cast<int64_t>(min(g0 + b * RUNS, groups - 1)) * D + 4 * d4);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (g0 + b * RUNS < groups) v.x += a[b].x, v.y += a[b].y, v.z += a[b].z, v.w += a[b].w;
   }
   *reinterpret_cast<float4*>(&sums[run * D + 4 * d4]) = v;
   __syncthreads();
@@ -285,7 +294,7 @@ hipError_t launch_forward_u(const NormRopeProblem& p, hipStream_t stream) {
 template <int LR>
 hipError_t launch_forward(const NormRopeProblem& p, hipStream_t stream) {
   const uint64_t rows = static_cast<uint64_t>(p.tokens) * (p.heads[0] + p.heads[1]);
-  return rows >= kManyRows ? launch_forward_u<LR, 4>(p, stream) : launch_forward_u<LR, 1>(p, stream);
+  return rows * (8 * LR) >= kManyForward ? launch_forward_u<LR, 4>(p, stream) : launch_forward_u<LR, 1>(p, stream);
 }
 
 template <int LR, int U>
@@ -316,7 +325,7 @@ hipError_t launch_backward_u(const NormRopeBackProblem& p, hipStream_t stream) {
 template <int LR>
 hipError_t launch_backward(const NormRopeBackProblem& p, hipStream_t stream) {
   const uint64_t rows = static_cast<uint64_t>(p.tokens) * (p.heads[0] + p.heads[1]);
-  return rows >= kManyRows ? launch_backward_u<LR, 4>(p, stream) : launch_backward_u<LR, 1>(p, stream);
+  return rows * (8 * LR) >= kManyBackward ? launch_backward_u<LR, 4>(p, stream) : launch_backward_u<LR, 1>(p, stream);
 }
 
 }  // namespace

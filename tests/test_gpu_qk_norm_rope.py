@@ -57,6 +57,21 @@ def test_forward(mx, D, rot, inter, norm, T, hq, hk):
     assert torch.equal(y[:, :hq], qo) and torch.equal(y[:, hq:], x[:, hq:])
 
 
+@pytest.mark.parametrize("D,rot,T", [(64, 32, 9401), (128, 128, 4703), (256, 192, 2351)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_forward_of_many_rows(mx, D, rot, T, inter):
+    """From 2^22 values on, four heads of a token at once: 5 and 2 heads leave three and two short."""
+    rng, x, w, pos, cos, sin, dev = _setup(D + T, T, 5, 2, D, rot, True)
+    q, k = x[:, :5], x[:, 5:7]
+    qo, ko = (torch.full((T, h, D), float("nan"), dtype=torch.bfloat16, device="cuda") for h in (5, 2))
+    note(f"norm_rope of many rows D={D} rot={rot} inter={inter} T={T}")
+    mx.mx_qk_norm_rope(q, k, *dev, qo, ko, *w, eps=1e-5, interleaved=inter)
+    torch.cuda.synchronize()
+    for got, a, b, name in ((qo, q, w[0], "q"), (ko, k, w[1], "k")):
+        want, size = A.norm_rope(f64(a), _np(b), pos, cos, sin, 1e-5, inter)
+        _close(got, want, size, name)
+
+
 def test_rows_of_zeros_huge_and_tiny_values(mx):
     D, T = 128, 4
     x = torch.zeros((T, 2, D), dtype=torch.bfloat16, device="cuda")
