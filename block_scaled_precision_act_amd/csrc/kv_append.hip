@@ -7,7 +7,9 @@
 // Bound by HBM.  D / 8 lanes own a token and head, 16 bytes of key and of value each, so four
 // neighbouring lanes own a 32-block and its largest magnitude needs two quad permutes.  A rotated
 // pair's other member, half a rotation away, is read again (it is another lane's 16 bytes of the
-// same row, in the L1 by then).
+// same row, in the L1 by then).  16384 x 8 heads of 128, with the values as stored: 32 us for 161 MB,
+// 5.0 TB/s, what a large copy reaches; one token for each of 41 sequences, 12 heads: 3.3 us, two
+// thirds of it the launch.
 #include "attn_common.h"
 
 namespace mx {
@@ -58,13 +60,13 @@ __device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
   x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
 }
 
-// Past the caches: the values as stored are most of what is written (16384 x 8 heads of 128: 34 us, 39
+// Past the caches: the values as stored are most of what is written (16384 x 8 heads of 128: 32 us, 39
 // us without).
 __device__ __forceinline__ void store_stream(uint16_t* p, uint4 v) {
   __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p));
 }
 
-// Values are read once (keys by two lanes, where they are rotated): 2 us less.
+// Values are read once (keys by two lanes, where they are rotated): 34 us without, there.
 __device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
   const v4u t = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
   return make_uint4(t[0], t[1], t[2], t[3]);
@@ -186,14 +188,16 @@ hipError_t launch_u(const KvAppendProblem& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// From this many rows on a row's owners take two heads at once; below, the rows alone do not fill the
-// chip.
-constexpr uint64_t kManyRows = 32768;
+// From this many values on a row's owners take two heads at once; below, one, as the rows then do not
+// fill the chip.  Two and one: 3.1 M values 7.6 and 7.5 us, 6.1 M 11.9 and 13.2 (heads of 128; 64 and
+// 256 alike).
+constexpr uint64_t kManyValues = uint64_t{1} << 22;
 
 template <int LR>
 hipError_t launch(const KvAppendProblem& p, hipStream_t stream) {
-  return static_cast<uint64_t>(p.tokens) * p.cache.heads >= kManyRows ? launch_u<LR, 2>(p, stream)
-                                                                     : launch_u<LR, 1>(p, stream);
+  return static_cast<uint64_t>(p.tokens) * p.cache.heads * (8 * LR) >= kManyValues
+             ? launch_u<LR, 2>(p, stream)
+             : launch_u<LR, 1>(p, stream);
 }
 
 }  // namespace

@@ -59,6 +59,13 @@ def test_bytes(mx, D, rot, inter, T, h, page):
     assert (f64(ko)[~live] == 9).all() and (f64(vo)[~live] == 9).all()
 
 
+@pytest.mark.parametrize("D,rot,T", [(64, 64, 22003), (128, 64, 11003), (256, 256, 5503)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_bytes_of_many_rows(mx, D, rot, inter, T):
+    """From 2^22 values on, two heads of a token at once: three heads leave one short."""
+    test_bytes(mx, D, rot, inter, T, 3, 32)
+
+
 def test_codes_of_values_between_codes(mx):
     # every E2M1 code, midpoint and their bf16 neighbours, at several scales, both signs
     base = np.array([0, .25, .5, .75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 0.1])
