@@ -199,7 +199,8 @@ def mx_qk_norm_rope_backward(dq_out, dk_out, q, k, positions, cos, sin, dq, dk, 
                              eps=1e-6, interleaved=False, stream=None):
     """Gradients of mx_qk_norm_rope: dq, dk (bf16, may be dq_out, dk_out) from those of its outputs,
     and dq_weight, dk_weight (fp32 [head_dim], written; None: not wanted).  workspace: a tensor of
-    mx_qk_norm_rope_backward_workspace_size bytes, zero before its first use, reusable."""
+    mx_qk_norm_rope_backward_workspace_size bytes, zero before its first use, reusable (by this call, not
+    by mx_attn_fp4)."""
     fn, dev = "mx_qk_norm_rope_backward", _current_device()
     qp, qt, qh = _heads(fn, q, "q", dev)
     T, Hq, D = q.shape

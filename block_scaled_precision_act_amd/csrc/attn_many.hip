@@ -454,7 +454,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
     for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
     top = max_halves(top) * p.scale_log2;
     // The maximum that is subtracted moves only when some row's rose by more than 2^8 (weights below
-    // that are held as exactly as those below one).
+    // that are held as exactly as those below one).  Moved at every rise: 551 us for 521 (8192 tokens).
     if (__any(top > m + 8.f)) {
       const float now = fmaxf(m, top);
       const float f = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);

@@ -87,7 +87,8 @@ int mx_qk_norm_rope(const mx_qk_norm_rope_args* args, void* stream);
  * one fixed order: the same call gives the same bits.
  * workspace: mx_qk_norm_rope_backward_workspace_size bytes, 256-byte aligned, zero before its
  * first use and left reusable by every call; needed only where a weight gradient is written.
- * Calls that may overlap need workspaces of their own.
+ * Calls that may overlap need workspaces of their own.  Not to be shared with mx_attn_fp4: this call
+ * leaves partial results where that one expects zeros.
  */
 typedef struct mx_qk_norm_rope_backward_args {
   const void* dq_out;                             /* bf16 [tokens, q_heads, head_dim]         */
