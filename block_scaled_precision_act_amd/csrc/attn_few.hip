@@ -22,8 +22,8 @@
 // Measured, 8 heads of 128: 4 sequences of up to 131073 tokens, 4 rows each: 93 us for 555 MB, 5.95
 // TB/s (a large copy reaches 5.1); 41 sequences of 1 to 8192 tokens, 7 rows: 41 us, 4.5 TB/s, the ramp
 // and the join being 6 of them; 1000 tokens: 8 us, nearly all latency.  Heads of 64 have half the bytes
-// a token for the same instructions a step and are bound by these: 32 sequences, 12 heads, 4 rows, a
-// window of 4096: 30 us, 3.0 TB/s.
+// a token for the same instructions and nearly the same loads a step: 32 sequences, 12 heads, 4 rows, a
+// window of 4096: 28 us, 3.2 TB/s (22 without the loads; without decoding or exponentials no less).
 #include "attn_common.h"
 
 namespace mx {
@@ -64,14 +64,14 @@ __device__ __forceinline__ int value_of(int c) {
 template <int D>
 struct RawKeys {
   uint32_t k[2][D / 32];  // per 16 tokens: D / 4 codes of token lane % 16
-  uint32_t s[2];          // the word that holds their scale byte(s)
+  uint32_t s;             // the word that holds their scale byte(s), of step g % 2
 };
 template <int D>
 struct RawValues {
   // D / 16 codes of the lane's 8 tokens.  D == 64: the first four words, 8 codes each of every second
   // token, whose halves lanes c and c + 8 exchange (value_words).
   uint32_t v[8][D <= 128 ? 1 : 2];
-  uint32_t s[2];                     // the word that holds token 4 (lane % 4) + g's scale byte
+  uint32_t s;         // the word that holds token 4 (lane % 4) + g's scale byte, of step lane / 4 % 2
 };
 
 struct Places {           // where the two 16-token steps of 32 tokens lie: pages and first tokens
@@ -289,13 +289,19 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       }
       return at;
     };
+    // Both steps' scales come in one load, half of the lanes each, and are handed over in registers (4 x
+    // 131073 tokens of 8 heads of 64: 64 us, 72 with a load for each step).  The codes are not: 16 bytes
+    // a lane of all that lies together, exchanged among lanes, 67 us.
+    auto scales_of = [&](const Places& at, int second) {
+      const int64_t a = at.id[0] * p.cache.scale_page + at.off[0] * (D / 32);
+      const int64_t b = at.id[1] * p.cache.scale_page + at.off[1] * (D / 32);
+      return second ? b : a;
+    };
     auto load_keys = [&](RawKeys<D>& w, const Places& at) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint8_t* const kp = kh + (at.id[s] * p.cache.code_page + at.off[s] * (D / 2)) +
                                   (key_c * (D / 2) + g * (D / 8));
-        const uint8_t* const sp = ksh + (at.id[s] * p.cache.scale_page + at.off[s] * (D / 32)) +
-                                  (D == 64 ? (key_c >> 1) * 4 : D == 128 ? key_c * 4 : key_c * 8 + (g >> 1) * 4);
         if constexpr (D == 64) {
           const v2u t = stream<v2u>(kp);
           w.k[s][0] = t[0]; w.k[s][1] = t[1];
@@ -307,17 +313,16 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
             for (int e = 0; e < 4; ++e) w.k[s][4 * i + e] = t[e];
           }
         }
-        w.s[s] = *reinterpret_cast<const uint32_t*>(sp);
       }
+      w.s = *reinterpret_cast<const uint32_t*>(
+          ksh + scales_of(at, g & 1) +
+          (D == 64 ? (key_c >> 1) * 4 : D == 128 ? key_c * 4 : key_c * 8 + (g >> 1) * 4));
     };
     auto load_values = [&](RawValues<D>& w, const Places& at) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint8_t* const vp = vh + (at.id[s] * p.cache.code_page + at.off[s] * (D / 2)) +
                                   (D == 64 ? ((c >> 3) * 4 + g) * 32 + (c & 7) * 4 : g * (D / 2) + c * (D / 32));
-        const uint8_t* const sp = vsh + (at.id[s] * p.cache.scale_page + at.off[s] * (D / 32)) +
-                                  (D == 64 ? ((c & 3) * 2 + (g >> 1)) * 4
-                                           : ((c & 3) * 4 + g) * (D / 32) + (D == 256 ? (c >> 3) * 4 : 0));
         if constexpr (D == 64) {
           w.v[2 * s][0] = stream<uint32_t>(vp);
           w.v[2 * s + 1][0] = stream<uint32_t>(vp + 8 * 32);
@@ -333,19 +338,22 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
             }
           }
         }
-        w.s[s] = *reinterpret_cast<const uint32_t*>(sp);
       }
+      w.s = *reinterpret_cast<const uint32_t*>(
+          vsh + scales_of(at, c & 4) +
+          (D == 64 ? ((c & 3) * 2 + (g >> 1)) * 4 : ((c & 3) * 4 + g) * (D / 32) + (D == 256 ? (c >> 3) * 4 : 0)));
     };
 
     // 32 tokens from tok0; what was loaded for them is replaced by the loads of `next` as soon as it
     // is decoded.
     auto step = [&](RawKeys<D>& rk, RawValues<D>& rv, int32_t tok0, const Places& next, auto more) {
       v4f s[MT][2];
+      const v2u ks = __builtin_amdgcn_permlane16_swap(rk.s, rk.s, false, false);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
-          const float sc = scale_of_byte(rk.s[t], D == 256 && j >= 4 ? turn_ks + 8 : turn_ks);
+          const float sc = scale_of_byte(ks[t], D == 256 && j >= 4 ? turn_ks + 8 : turn_ks);
           const bf16x8 kf = __builtin_bit_cast(bf16x8, decode8(rk.k[t][j], sc));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -396,10 +404,14 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       // The values' scales: the scaled conversions read a scale's exponent field alone, so the word is
       // rotated until the lane's byte lies there.  What lies past the keys is given scale 1: finite,
       // and its weight is 0.
+      const int vs = static_cast<int>(rv.s);
+      const uint32_t vss[2] = {
+          static_cast<uint32_t>(__builtin_amdgcn_update_dpp(vs, vs, 0x114, 0xF, 0xA, false)),   // from quads 0, 2
+          static_cast<uint32_t>(__builtin_amdgcn_update_dpp(vs, vs, 0x104, 0xF, 0x5, false))};  // from quads 1, 3
       float vsc[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        vsc[i] = scale_of_byte(quad_lane(rv.s[i >> 2], i & 3), turn_vs);
+        vsc[i] = scale_of_byte(quad_lane(vss[i >> 2], i & 3), turn_vs);
       if (tok0 + kWaveTokens > sq.hi) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
