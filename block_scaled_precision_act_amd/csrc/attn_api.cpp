@@ -284,12 +284,19 @@ int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
                          output_status(a->out, a->out_token_stride, a->out_head_stride, a->total_q,
                                        a->q_heads, c.head_dim, 8)})) != MX_OK)
     return st;
-  const mx::AttnPlan plan = mx::plan_attn(a->batch, a->max_q, a->q_heads, c.kv_heads,
-                                          static_cast<int>(c.head_dim));
+  mx::AttnPlan plan = mx::plan_attn(a->batch, a->max_q, a->q_heads, c.kv_heads,
+                                    static_cast<int>(c.head_dim));
   // The deal of tiles of 128 tokens (plus a few slots for each sequence and head) counts in 31 bits.
   const int64_t units = a->batch * c.kv_heads;
   if (plan.few && (units > mx::kMaxUnits || !fits31(units, a->table_width * c.page_size / 128 + 8)))
     return MX_ERR_SHAPE;
+  // So does that of tiles of 64 tokens; past it there is none.  Nor is there one where the table's tokens
+  // are too few for it to gain what looking costs (the longest part's tiles; looking takes about 5 us, a
+  // tile 2).
+  const int64_t tiles = a->table_width * c.page_size / 64;
+  if (!plan.few && plan.groups > 0 &&
+      (tiles / plan.splits <= mx::kLeastDealTiles || !fits31(units * plan.row_blocks, tiles + 8)))
+    plan.groups = 0;
   if (plan.part_bytes > 0 && (!a->workspace || a->workspace_bytes < mx::kCounterBytes + plan.part_bytes ||
                               !aligned(a->workspace, 256)))
     return MX_ERR_WORKSPACE;

@@ -103,14 +103,17 @@ constexpr uint32_t counter_stride(int64_t units) {
 struct AttnPlan {
   bool few;                  // few rows: the cache is what costs (attn_few.hip), else attn_many.hip
   int row_tiles;             // of a workgroup: 16-row tiles (few), wavefronts of 32 rows (many)
-  int groups;                // few: workgroups that the cached tokens are dealt to
-  int row_blocks, splits;    // many: blocks of rows for each (sequence, head), parts of the keys
+  int groups;                // workgroups that the cached tokens are dealt to (many: 0: no deal)
+  int row_blocks, splits;    // many: blocks of rows of each (sequence, head), parts of their keys at most
   int64_t part_bytes;        // of partial results
 };
 // Wavefronts of attn_few.hip that a SIMD holds (by their registers), and so workgroups a CU.
 constexpr int few_waves(int head_dim, int row_tiles) {
   return head_dim * row_tiles <= 128 ? 3 : head_dim * row_tiles <= 256 ? 2 : 1;
 }
+// A deal among many rows (attn_many.hip) is looked at where a part of a unit may have more tiles of 64
+// tokens.
+constexpr int64_t kLeastDealTiles = 32;
 AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim);
 // Partial results of any plan with at most max_q queries a sequence.
 int64_t most_part_bytes(int64_t max_q, int64_t group, int head_dim);

@@ -17,12 +17,12 @@
 //
 // Measured: a prompt of 8192 tokens, 32 heads of 128 on 8: 520 us, 1050 TFLOP/s (a large library
 // product: 1172), the matrix instructions busy 43% of the cycles; 512 and 386 queries of 16 heads of
-// 256 on 2 against 32768 and 27891 tokens: 545 us, 820 TFLOP/s.  Power does not bound them (2.35 GHz
+// 256 on 2 against 32768 and 27891 tokens: 495 us, 905 TFLOP/s.  Power does not bound them (2.35 GHz
 // sustained): for every matrix instruction a wavefront reads 1 KB from LDS, which takes about as long,
-// and decoding and softmax take as many cycles again; with the decoding left out the two take 410 and
-// 360 us, without those reads the first takes 355.  More rows a wavefront would need fewer reads: 64
-// (four wavefronts, every register of the CU) leave one wavefront a SIMD and nothing to cover its waits
-// with, 595 us.
+// and decoding and softmax take as many cycles again; with the decoding left out the first takes 410 us
+// and the second two thirds, without those reads the first takes 355.  More rows a wavefront would need
+// fewer reads: 64 (four wavefronts, every register of the CU) leave one wavefront a SIMD and nothing to
+// cover its waits with, 595 us.
 #include "attn_common.h"
 
 #include <algorithm>
@@ -34,22 +34,22 @@ constexpr int kTok = 64;
 constexpr float kLn2 = 0.6931471805599453f;
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-// What a workgroup works on: a block of rows of a sequence and head, and a part of its keys.
+// What a workgroup works on at a time: a block of rows of a sequence and head (a unit), and a run of
+// the 64-token tiles that some of its rows see.
 struct Work {
-  int32_t b, h, blk, part, parts;
+  int32_t b, h, blk;
   int32_t len, q0, rows, r0, first;       // first: the position of the sequence's first query
-  int32_t hi, t_begin, tiles;             // keys end; this part's first token and tiles of 64
+  int32_t hi, t_begin, tiles;             // keys end; the run's first token and tiles of 64
   int32_t full_hi, full_lo;               // tokens below and from which every row sees
-  bool any;
+  bool any;                               // the block has rows
 };
 
-__device__ __forceinline__ Work work_of(const AttnProblem& p, int block_rows, int splits, int h, int b,
-                                        int blk, int part) {
+// A whole unit.
+__device__ __forceinline__ Work unit_of(const AttnProblem& p, int block_rows, int h, int b, int blk) {
   Work w;
   w.h = h;
   w.b = b;
   w.blk = blk;
-  w.part = part;
   const int64_t most = static_cast<int64_t>(p.table_width) * p.cache.page_size;
   const int32_t raw_len = read_uniform(p.lens, w.b);
   w.len = raw_len < 0 ? 0 : (raw_len < most ? raw_len : static_cast<int32_t>(most));
@@ -63,33 +63,208 @@ __device__ __forceinline__ Work work_of(const AttnProblem& p, int block_rows, in
   w.rows = n * p.group;
   w.r0 = w.blk * block_rows;
   w.any = w.r0 < w.rows;
+  w.tiles = 0;
   if (!w.any) return w;
   w.first = w.len - n;
   const int32_t tok_lo = w.r0 / p.group, tok_hi = (min(w.r0 + block_rows, w.rows) - 1) / p.group;
   w.hi = p.causal ? min(max(w.first + tok_hi + 1, 0), w.len) : w.len;
-  const int32_t lo = p.window > 0 ? max(w.first + tok_lo + 1 - p.window, 0) & ~(kTok - 1) : 0;
-  const int32_t all = max(0, (w.hi - lo + kTok - 1) / kTok);
-  w.parts = max(1, min(splits, all / 4));
-  w.any = w.part < w.parts;
-  const int32_t tile0 = static_cast<int32_t>(static_cast<int64_t>(all) * w.part / w.parts);
-  w.tiles = static_cast<int32_t>(static_cast<int64_t>(all) * (w.part + 1) / w.parts) - tile0;
-  w.t_begin = lo + tile0 * kTok;
+  w.t_begin = p.window > 0 ? max(w.first + tok_lo + 1 - p.window, 0) & ~(kTok - 1) : 0;
+  w.tiles = max(0, (w.hi - w.t_begin + kTok - 1) / kTok);
   w.full_hi = p.causal ? min(w.first + tok_lo + 1, w.len) : w.len;
   w.full_lo = p.window > 0 ? w.first + tok_hi + 1 - p.window : 0;
   return w;
 }
 
-// A workgroup's.  Heads fastest: with 8 of them a head's keys stay on one XCD's L2.  Late rows (the
-// longest under a causal mask) first.
-__device__ __forceinline__ Work my_work(const AttnProblem& p, int block_rows, int row_blocks, int splits) {
-  const uint32_t heads = p.cache.heads;
-  uint32_t idx = blockIdx.x;
-  const int h = idx % heads;
-  idx /= heads;
-  const int b = idx % p.batch;
-  idx /= p.batch;
-  return work_of(p, block_rows, splits, h, b, row_blocks - 1 - static_cast<int>(idx / splits), idx % splits);
+// How units come to workgroups.
+//
+// As they are: a workgroup each, heads fastest (with 8 of them a head's keys stay on one XCD's L2), late
+// rows, the longest under a causal mask, first.  Where they are fewer than the chip holds, each is cut
+// into up to `splits` parts of its tiles, of 4 at least.
+//
+// Or dealt: sequences differ in length, and the longest unit's part lasts while other workgroups idle.
+// All units' tiles, in the order (head, sequence, block), with kUnitSlots before each unit's for what it
+// costs besides, are cut into equal runs, one a workgroup.  A run that would begin within kSnap tiles of
+// a unit's ends begins there.  What a workgroup has of a unit that others share is a part: a workgroup
+// has two at most (the end of a unit, the beginning of another).
+//
+// The lengths decide, on the device: a deal costs kDealCost tiles (more beginnings and parts), units as
+// they are last as long as the longest one's part, or as the average in rounds.  One sequence is not
+// dealt, nor are kDealUnits or more units a workgroup, which fill the chip evenly enough.  Dealt and not:
+// 4 sequences of 5000 to 32768 tokens, up to 500 queries, 32 heads of 128 on 4: 515 and 915 us; 4 of 1000
+// to 9000, up to 300, 16 of 256 on 2: 137 and 304 us; the two above with heads of 256: 495 and 545.
+// Looking at it costs about 5 us (4 x 300 queries of 200 to 300 tokens: 20 us, 25 when looked at), so the
+// host spares it where the table is short.
+//
+// Parts are joined by attn_join_kernel.
+constexpr int64_t kDealUnits = 4;
+constexpr uint32_t kUnitSlots = 2, kSnap = 2, kLeastShare = 4, kDealCost = 8;
+constexpr int kLeastPart = 4;
+constexpr int kMostEntries = 2048;         // (sequence, block) pairs of a deal
+constexpr int kMostGroups = 512;
+
+__device__ __forceinline__ int parts_of(int tiles, int splits) { return max(1, min(splits, tiles / kLeastPart)); }
+
+// Where a run begins, and the unit it begins in: its first slot and the one after its last, its number
+// (head, sequence, block).  Left in the workspace for the join; the first run's holds the number of runs
+// instead (0: no deal).
+struct RunStart {
+  uint32_t unit_first, unit_end, at, unit;
+};
+constexpr int64_t kStartFloats = kMostGroups * sizeof(RunStart) / 4;
+
+struct Deal {
+  const uint32_t* first;     // of each (sequence, block): its first slot in a head's, in LDS
+  uint32_t entries, heads, groups;
+
+  __device__ __forceinline__ uint32_t slot_of(uint32_t e) const {
+    return __builtin_amdgcn_readfirstlane(first[e]);
+  }
+  __device__ __forceinline__ uint32_t per_head() const { return slot_of(entries); }
+  // The entry that slot x of a head lies in: of the 64 runs of entries that the lanes stand for, then of
+  // the run's entries.
+  __device__ __forceinline__ uint32_t entry(uint32_t x) const {
+    const uint32_t lane = threadIdx.x & 63, run = (entries + 63) / 64;
+    const uint32_t next = (lane + 1) * run;
+    const uint32_t e0 = run * __builtin_popcountll(__ballot(next < entries && first[min(next, entries)] <= x));
+    const uint32_t e1 = e0 + lane + 1;
+    return e0 + __builtin_popcountll(__ballot(lane + 1 < run && e1 < entries && first[min(e1, entries)] <= x));
+  }
+  __device__ __forceinline__ RunStart start(uint32_t g) const {
+    const uint32_t per = per_head(), total = per * heads;
+    const uint32_t whole = total / groups;
+    const uint32_t x = g * whole + g * (total - whole * groups) / groups;      // g total / groups
+    if (x >= total) return RunStart{total, total, total, 0};
+    const uint32_t head = x / per, base = head * per, e = entry(x - base);
+    const uint32_t s = base + slot_of(e), end = base + slot_of(e + 1);
+    return RunStart{s, end, x <= s + kUnitSlots + kSnap ? s : x + kSnap >= end ? end : x, head * entries + e};
+  }
+};
+
+// Called by all THREADS of a workgroup; `first` has room for kMostEntries + 3.  The slots of all heads
+// number less than 2^31.
+template <int THREADS>
+__device__ __forceinline__ Deal deal(const AttnProblem& p, int block_rows, int row_blocks, int splits,
+                                     int groups, uint32_t* first) {
+  Deal d;
+  d.first = first;
+  d.entries = p.batch * row_blocks;
+  d.heads = p.cache.heads;
+  for (uint32_t e = threadIdx.x; e < d.entries; e += THREADS) {
+    const uint32_t b = e / row_blocks;
+    const Work w = unit_of(p, block_rows, 0, b, e - b * row_blocks);
+    first[e + 1] = w.any ? static_cast<uint32_t>(w.tiles) + kUnitSlots : 0u;
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const uint32_t run = (d.entries + 63) / 64;
+    const uint32_t e0 = min(threadIdx.x * run, d.entries), e1 = min(e0 + run, d.entries);
+    uint32_t sum = 0, longest = 0, count = 0;
+    for (uint32_t e = e0; e < e1; ++e) {
+      const uint32_t n = first[e + 1];
+      sum += n;
+      longest = max(longest, n);
+      count += n != 0;
+    }
+    uint32_t upto = sum;
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) {
+      const uint32_t v = __shfl_up(upto, i, 64);
+      if (static_cast<int>(threadIdx.x) >= i) upto += v;
+      longest = max(longest, static_cast<uint32_t>(__shfl_xor(longest, i, 64)));
+      count += __shfl_xor(count, i, 64);
+    }
+    uint32_t at = upto - sum;
+    for (uint32_t e = e0; e < e1; ++e) first[e + 1] = at += first[e + 1];
+    if (threadIdx.x == 0) {
+      first[0] = 0;
+      first[d.entries + 1] = longest;
+      first[d.entries + 2] = count;
+    }
+  }
+  __syncthreads();
+  const uint32_t total = d.per_head() * d.heads, units = max(1u, d.slot_of(d.entries + 2) * d.heads);
+  const uint32_t longest = d.slot_of(d.entries + 1);
+  const uint32_t span = max(longest / parts_of(static_cast<int>(longest), splits),
+                            (units + groups - 1) / groups * (splits == 1 ? total / units : 0));
+  d.groups = span <= total / groups + kDealCost
+                 ? 0
+                 : max(1u, min(static_cast<uint32_t>(groups), total / kLeastShare));
+  return d;
 }
+
+// The kernel's argument, read again: what a workgroup derives from it for one unit is not kept in
+// registers for the next (that cost spills in the loop over tokens).
+__device__ __forceinline__ AttnProblem argument() {
+  auto at = reinterpret_cast<uintptr_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(at));
+  AttnProblem p;
+  __builtin_memcpy(&p, reinterpret_cast<const __attribute__((address_space(4))) AttnProblem*>(at), sizeof(p));
+  return p;
+}
+
+// A workgroup's units or parts, one after the other.  `groups`: runs of a deal (DEALT).
+template <int THREADS, bool DEALT>
+struct Walk {
+  uint32_t g, x, end;
+  bool dealt;
+
+  __device__ __forceinline__ Walk(const AttnProblem& p, int block_rows, int row_blocks, int splits, int groups,
+                                  uint32_t* first) {
+    x = 0;
+    end = 1;
+    dealt = false;
+    if constexpr (DEALT) {
+      const Deal d = deal<THREADS>(p, block_rows, row_blocks, splits, groups, first);
+      RunStart* const starts = reinterpret_cast<RunStart*>(p.parts);
+      if (blockIdx.x == 0 && threadIdx.x == 0) starts[0] = RunStart{0, 0, 0, d.groups};
+      if (d.groups == 0) {
+        end = blockIdx.x < d.entries * d.heads * splits;
+        return;
+      }
+      dealt = true;
+      // Neighbouring runs (of one head's tokens) to one XCD.
+      const uint32_t each = (d.groups + 7) / 8;
+      g = blockIdx.x % 8 * each + blockIdx.x / 8;
+      x = end = 0;
+      if (blockIdx.x / 8 < each && g < d.groups) {
+        const RunStart s = d.start(g);
+        if (g > 0 && threadIdx.x == 0) starts[g] = s;
+        x = s.at;
+        end = d.start(g + 1).at;
+      }
+    }
+  }
+  // The next one and where its part goes (-1: it is whole); false: none is left.
+  __device__ __forceinline__ bool next(const AttnProblem& p, int block_rows, int row_blocks, int splits,
+                                       const uint32_t* first, Work* w, int* slot) {
+    *slot = -1;
+    if (x >= end) return false;
+    if (!DEALT || !dealt) {
+      x = end;
+      const uint32_t heads = p.cache.heads, h = blockIdx.x % heads, r = blockIdx.x / heads, b = r % p.batch;
+      const int part = r / p.batch % splits, blk = row_blocks - 1 - static_cast<int>(r / p.batch / splits);
+      *w = unit_of(p, block_rows, h, b, blk);
+      const int parts = parts_of(w->tiles, splits);
+      if (!w->any || part >= parts) return false;
+      if (parts == 1) return true;
+      *slot = ((blk * p.batch + b) * heads + h) * splits + part;
+      const int32_t tile0 = static_cast<int32_t>(static_cast<int64_t>(w->tiles) * part / parts);
+      w->tiles = static_cast<int32_t>(static_cast<int64_t>(w->tiles) * (part + 1) / parts) - tile0;
+      w->t_begin += tile0 * kTok;
+      return true;
+    }
+    const Deal d = {first, static_cast<uint32_t>(p.batch * row_blocks), 0, 0};
+    const uint32_t per = d.per_head(), head = x / per, base = head * per, e = d.entry(x - base);
+    *w = unit_of(p, block_rows, head, e / row_blocks, e % row_blocks);
+    const uint32_t s = base + d.slot_of(e), stop = base + d.slot_of(e + 1), upto = min(end, stop);
+    const uint32_t tile0 = x > s ? x - s - kUnitSlots : 0;
+    if (x > s || upto < stop) *slot = 2 * g + (x == s);
+    w->tiles = upto - s - kUnitSlots - tile0;
+    w->t_begin += tile0 * kTok;
+    x = upto;
+    return true;
+  }
+};
 
 // A lane's query row: lanes c and c + 32 of a wavefront share row r0 + 32 tile + c.
 struct Row {
@@ -321,11 +496,11 @@ __device__ __forceinline__ void write_lse(const AttnProblem& p, const Work& w, c
 // thread after the other; then m, then l, of each row (a row is two threads').
 constexpr int64_t part_floats(int threads, int n) { return static_cast<int64_t>(threads) * (16 * n + 1); }
 
-// The rows are written (one part), or left for the join.
+// The rows are written, or a part of them left for the join.
 template <int DT, int THREADS, int N>
-__device__ __forceinline__ void finish(const AttnProblem& p, const Work& w, const Row& r, int splits,
+__device__ __forceinline__ void finish(const AttnProblem& p, const Work& w, const Row& r, int slot,
                                        const v16f (&acc)[N], float m, float l, int d0) {
-  if (w.parts == 1) {
+  if (slot < 0) {
     if (!r.live) return;
     v4f x[N][4];
 #pragma unroll
@@ -336,8 +511,7 @@ __device__ __forceinline__ void finish(const AttnProblem& p, const Work& w, cons
     if (d0 == 0) write_lse(p, w, r, m, l);
     return;
   }
-  const int64_t unit = (static_cast<int64_t>(w.blk) * p.batch + w.b) * p.cache.heads + w.h;
-  float* const part = p.parts + (unit * splits + w.part) * part_floats(THREADS, N);
+  float* const part = p.parts + kStartFloats + slot * part_floats(THREADS, N);
 #pragma unroll
   for (int d = 0; d < N; ++d)
 #pragma unroll
@@ -351,36 +525,85 @@ __device__ __forceinline__ void finish(const AttnProblem& p, const Work& w, cons
   }
 }
 
-// Joins a block's parts, in their order, whole rows at a time; a workgroup takes one of a thread's
-// four lots of 4 for two of its N sums.  A launch of its own: the parts of one block would be joined
+// Joins a unit's parts, in their order, whole rows at a time; a workgroup takes one of a thread's
+// four lots of 4 for two of its N sums.  A launch of its own: the parts of one unit would be joined
 // by one workgroup otherwise (128 rows of 60000 keys in 64 parts: 110 us, 63 us so).
 // HALVES: 2 where two wavefronts share rows (attn_wide_kernel).
 template <int DT, int THREADS, int N, int HALVES>
-__global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p, int splits) {
+__global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p, int row_blocks, int splits,
+                                                            int groups) {
   constexpr int kSlices = 4 * N / 2, kTiles = THREADS / 64 / HALVES;
-  const uint32_t heads = p.cache.heads;
-  const uint32_t slice = blockIdx.x % kSlices, unit = blockIdx.x / kSlices;
-  const Work w = work_of(p, 32 * kTiles, splits, unit % heads, unit / heads % p.batch,
-                         unit / heads / p.batch, 0);
-  if (!w.any || w.parts == 1) return;
+  const RunStart* const starts = reinterpret_cast<const RunStart*>(p.parts);
+  const uint32_t slice = blockIdx.x % kSlices, lane = threadIdx.x & 63, runs = groups ? starts[0].unit : 0;
+  uint32_t left = blockIdx.x / kSlices;
+  // Part k lies at slot base + step k, the first at base + lead.
+  int parts = 0, base, lead, step;
+  Work w;
+  if (runs == 0) {                           // the units as they are
+    const uint32_t heads = p.cache.heads;
+    if (splits == 1 || left >= heads * p.batch * row_blocks) return;
+    w = unit_of(p, 32 * kTiles, left % heads, left / heads % p.batch, left / heads / p.batch);
+    parts = parts_of(w.tiles, splits);
+    if (!w.any || parts == 1) return;
+    base = left * splits;
+    lead = 0;
+    step = 1;
+  } else {
+    // Those that runs begin inside of, the i-th by the workgroups i of each slice: the part of the
+    // workgroup before the first of these runs, and theirs.
+    constexpr int kChunks = kMostGroups / 64;
+    RunStart all[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) all[i] = starts[i * 64 + lane];
+    uint32_t g0 = 0, before = ~0u, unit = ~0u;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const uint32_t g = i * 64 + lane;
+      const bool in = g > 0 && g < runs && all[i].at > all[i].unit_first && all[i].at < all[i].unit_end;
+      const uint32_t its = in ? all[i].unit : ~0u;
+      uint32_t prev = __shfl_up(its, 1, 64);
+      if (lane == 0) prev = before;
+      before = __builtin_amdgcn_readlane(its, 63);
+      if (parts == 0) {
+        uint64_t firsts = __ballot(in && prev != its);
+        const uint32_t n = __builtin_popcountll(firsts);
+        if (left < n) {
+          for (; left > 0; --left) firsts &= firsts - 1;
+          g0 = i * 64 + __builtin_ctzll(firsts);
+          unit = __builtin_amdgcn_readlane(its, g0 & 63);
+          parts = 1;
+        } else {
+          left -= n;
+        }
+      }
+      if (parts > 0) parts += __builtin_popcountll(__ballot(its == unit));
+    }
+    if (parts == 0) return;
+    const uint32_t entries = p.batch * row_blocks, h = unit / entries, e = unit - h * entries;
+    w = unit_of(p, 32 * kTiles, h, e / row_blocks, e % row_blocks);
+    base = 2 * (g0 - 1);
+    lead = 1;
+    step = 2;
+  }
   const int wave = threadIdx.x / 64, row = wave * 32 + (threadIdx.x & 31);
   const int q = slice % 4, d = slice / 4 * 2;
   constexpr int64_t kPart = part_floats(THREADS, N);
-  const float* src = p.parts + static_cast<int64_t>(unit) * splits * kPart;
+  const float* src = p.parts + kStartFloats + base * kPart;
   float m = -kInf, l = 0.f;
   v4f acc[2][1] = {{v4f(0.f)}, {v4f(0.f)}};
   constexpr int kBatch = 8;
-  for (int at = 0; at < w.parts; at += kBatch) {
+  for (int at = 0; at < parts; at += kBatch) {
     float pm[kBatch], pl[kBatch];
     v4f x[kBatch][2];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {               // past the last part: that part, with no weight
-      const float* s = src + min(at + i, w.parts - 1) * kPart;
-      pm[i] = at + i < w.parts ? s[N * 16 * THREADS + row] : -kInf;
-      pl[i] = s[N * 16 * THREADS + THREADS / 2 + row];
+      const int part = min(at + i, parts - 1);
+      const float* from = src + (part == 0 ? lead : step * part) * kPart;
+      pm[i] = at + i < parts ? from[N * 16 * THREADS + row] : -kInf;
+      pl[i] = from[N * 16 * THREADS + THREADS / 2 + row];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        x[i][e] = *reinterpret_cast<const v4f*>(s + (((d + e) * 4 + q) * THREADS + threadIdx.x) * 4);
+      for (int c = 0; c < 2; ++c)
+        x[i][c] = *reinterpret_cast<const v4f*>(from + (((d + c) * 4 + q) * THREADS + threadIdx.x) * 4);
     }
     float now = m;
 #pragma unroll
@@ -392,7 +615,7 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p,
     acc[1][0] *= fo;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (at + i >= w.parts) break;
+      if (at + i >= parts) break;
       const float f = pm[i] == -kInf ? 0.f : __builtin_amdgcn_exp2f(pm[i] - now);
       l += pl[i] * f;
       acc[0][0] += x[i][0] * f;
@@ -411,121 +634,129 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p,
 
 // NW wavefronts of 32 query rows each.  Of 8, the first four decode keys and the others values (one
 // of each to a SIMD); of 4, all decode both.
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem p, int row_blocks,
-                                                               int splits) {
+template <int D, int NW, bool DEALT>
+__global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem args, int row_blocks,
+                                                               int splits, int groups) {
   constexpr int KS = D / 16, DT = D / 32, kThreads = 64 * NW;
   __shared__ uint4 kl[2][2 * KS * 64];
   __shared__ uint4 vl[2][4 * DT * 64];
+  __shared__ uint32_t first[DEALT ? kMostEntries + 3 : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Work w = my_work(p, 32 * NW, row_blocks, splits);
-  if (!w.any) return;
-  const Row row = row_of(p, w, wave);
-  bf16x8 qf[KS];
-  load_query(p, w, row, qf);
   const bool keys = NW == 4 || wave < 4, values = NW == 4 || wave >= 4;
-  const Decoder<D> dec(p, w, wave & 3);
+  Walk<kThreads, DEALT> walk(args, 32 * NW, row_blocks, splits, groups, first);
+  for (;;) {
+    const AttnProblem p = DEALT ? argument() : args;
+    Work w;
+    int slot;
+    if (!walk.next(p, 32 * NW, row_blocks, splits, first, &w, &slot)) return;
+    const Row row = row_of(p, w, wave);
+    bf16x8 qf[KS];
+    load_query(p, w, row, qf);
+    const Decoder<D> dec(p, w, wave & 3);
 
-  v16f acc[DT];
-  float m = -kInf, l = 0.f;
+    v16f acc[DT];
+    float m = -kInf, l = 0.f;
 #pragma unroll
-  for (int d = 0; d < DT; ++d) acc[d] = v16f(0.f);
-  // A wavefront that decodes one of the two holds one share.
-  Raw rk, rv_own;
-  Raw& rv = NW == 4 ? rv_own : rk;
-  Place next_k, next_v_own;
-  Place& next_v = NW == 4 ? next_v_own : next_k;
+    for (int d = 0; d < DT; ++d) acc[d] = v16f(0.f);
+    // A wavefront that decodes one of the two holds one share.
+    Raw rk, rv_own;
+    Raw& rv = NW == 4 ? rv_own : rk;
+    Place next_k, next_v_own;
+    Place& next_v = NW == 4 ? next_v_own : next_k;
 
-  // Tile i: its scores `s` are there; while its weights and products are made, the next tile's scores
-  // are (into `sn`), the keys after those and the next tile's values are decoded, and the ones after
-  // them loaded.  One barrier a tile: K(i + 2) goes where K(i) was, V(i + 1) where V(i - 1) was, both
-  // read by every wavefront before the last barrier.
-  auto step = [&](v16f (&s)[2], v16f (&sn)[2], auto odd, auto final, int32_t i) {
-    constexpr int B = decltype(odd)::value;
-    constexpr bool LAST = decltype(final)::value;
-    const int32_t t0 = w.t_begin + i * kTok;
-    if (t0 + kTok > w.full_hi || t0 < w.full_lo) {
-      mask(s[0], row, t0);
-      mask(s[1], row, t0 + 32);
-    }
-    float top = s[0][0];
+    // Tile i: its scores `s` are there; while its weights and products are made, the next tile's scores
+    // are (into `sn`), the keys after those and the next tile's values are decoded, and the ones after
+    // them loaded.  One barrier a tile: K(i + 2) goes where K(i) was, V(i + 1) where V(i - 1) was, both
+    // read by every wavefront before the last barrier.
+    auto step = [&](v16f (&s)[2], v16f (&sn)[2], auto odd, auto final, int32_t i) {
+      constexpr int B = decltype(odd)::value;
+      constexpr bool LAST = decltype(final)::value;
+      const int32_t t0 = w.t_begin + i * kTok;
+      if (t0 + kTok > w.full_hi || t0 < w.full_lo) {
+        mask(s[0], row, t0);
+        mask(s[1], row, t0 + 32);
+      }
+      float top = s[0][0];
 #pragma unroll
-    for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
-    top = max_halves(top) * p.scale_log2;
-    // The maximum that is subtracted moves only when some row's rose by more than 2^8 (weights below
-    // that are held as exactly as those below one).  Moved at every rise: 551 us for 521 (8192 tokens).
-    if (__any(top > m + 8.f)) {
-      const float now = fmaxf(m, top);
-      const float f = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
-      m = now;
-      l *= f;
+      for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
+      top = max_halves(top) * p.scale_log2;
+      // The maximum that is subtracted moves only when some row's rose by more than 2^8 (weights below
+      // that are held as exactly as those below one).  Moved at every rise: 551 us for 521 (8192 tokens).
+      if (__any(top > m + 8.f)) {
+        const float now = fmaxf(m, top);
+        const float f = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
+        m = now;
+        l *= f;
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[d][e] *= f;
-    }
-    const float sub = m == -kInf ? 0.f : m;
+          for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+      }
+      const float sub = m == -kInf ? 0.f : m;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {            // 16 tokens each
-      const bf16x8 pf = weights(s[q >> 1], 8 * (q & 1), p.scale_log2, sub, l);
+      for (int q = 0; q < 4; ++q) {            // 16 tokens each
+        const bf16x8 pf = weights(s[q >> 1], 8 * (q & 1), p.scale_log2, sub, l);
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8, vl[B][(q * DT + d) * 64 + lane]), pf, acc[d], 0, 0, 0);
-      if constexpr (!LAST)
-        scores(sn[q >> 1], kl[B ^ 1] + (q >> 1) * KS * 64, qf, (q & 1) * (KS / 2), ((q & 1) + 1) * (KS / 2));
-    }
-    if constexpr (!LAST) {
+        for (int d = 0; d < DT; ++d)
+          acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8, vl[B][(q * DT + d) * 64 + lane]), pf, acc[d], 0, 0, 0);
+        if constexpr (!LAST)
+          scores(sn[q >> 1], kl[B ^ 1] + (q >> 1) * KS * 64, qf, (q & 1) * (KS / 2), ((q & 1) + 1) * (KS / 2));
+      }
+      if constexpr (!LAST) {
+        if (keys) {
+          dec.decode_keys(rk, kl[B]);
+          dec.load_keys(rk, next_k);
+          next_k = dec.place(t0 + 4 * kTok);
+        }
+        if (values) {
+          dec.decode_values(rv, t0 + kTok, vl[B ^ 1]);
+          dec.load_values(rv, next_v);
+          next_v = dec.place(t0 + 3 * kTok);
+        }
+        lds_barrier();
+      }
+    };
+
+    if (w.tiles > 0) {
+      v16f sa[2], sb[2];
       if (keys) {
-        dec.decode_keys(rk, kl[B]);
-        dec.load_keys(rk, next_k);
-        next_k = dec.place(t0 + 4 * kTok);
+        dec.load_keys(rk, dec.place(w.t_begin));
+        dec.decode_keys(rk, kl[0]);
+        dec.load_keys(rk, dec.place(w.t_begin + kTok));
+        dec.decode_keys(rk, kl[1]);
+        dec.load_keys(rk, dec.place(w.t_begin + 2 * kTok));
+        next_k = dec.place(w.t_begin + 3 * kTok);
       }
       if (values) {
-        dec.decode_values(rv, t0 + kTok, vl[B ^ 1]);
-        dec.load_values(rv, next_v);
-        next_v = dec.place(t0 + 3 * kTok);
+        dec.load_values(rv, dec.place(w.t_begin));
+        dec.decode_values(rv, w.t_begin, vl[0]);
+        dec.load_values(rv, dec.place(w.t_begin + kTok));
+        next_v = dec.place(w.t_begin + 2 * kTok);
       }
       lds_barrier();
+      scores(sa[0], kl[0], qf, 0, KS);
+      scores(sa[1], kl[0] + KS * 64, qf, 0, KS);
+      lds_barrier();                           // K(0) is read before K(2) overwrites it
+      int32_t i = 0;
+      for (; i + 2 < w.tiles; i += 2) {
+        step(sa, sb, IntC<0>{}, IntC<0>{}, i);
+        step(sb, sa, IntC<1>{}, IntC<0>{}, i + 1);
+      }
+      if (i + 1 < w.tiles) {
+        step(sa, sb, IntC<0>{}, IntC<0>{}, i);
+        step(sb, sa, IntC<1>{}, IntC<1>{}, i + 1);
+      } else {
+        step(sa, sb, IntC<0>{}, IntC<1>{}, i);
+      }
     }
-  };
+    l += __shfl_xor(l, 32, 64);
 
-  if (w.tiles > 0) {
-    v16f sa[2], sb[2];
-    if (keys) {
-      dec.load_keys(rk, dec.place(w.t_begin));
-      dec.decode_keys(rk, kl[0]);
-      dec.load_keys(rk, dec.place(w.t_begin + kTok));
-      dec.decode_keys(rk, kl[1]);
-      dec.load_keys(rk, dec.place(w.t_begin + 2 * kTok));
-      next_k = dec.place(w.t_begin + 3 * kTok);
-    }
-    if (values) {
-      dec.load_values(rv, dec.place(w.t_begin));
-      dec.decode_values(rv, w.t_begin, vl[0]);
-      dec.load_values(rv, dec.place(w.t_begin + kTok));
-      next_v = dec.place(w.t_begin + 2 * kTok);
-    }
-    lds_barrier();
-    scores(sa[0], kl[0], qf, 0, KS);
-    scores(sa[1], kl[0] + KS * 64, qf, 0, KS);
-    lds_barrier();                           // K(0) is read before K(2) overwrites it
-    int32_t i = 0;
-    for (; i + 2 < w.tiles; i += 2) {
-      step(sa, sb, IntC<0>{}, IntC<0>{}, i);
-      step(sb, sa, IntC<1>{}, IntC<0>{}, i + 1);
-    }
-    if (i + 1 < w.tiles) {
-      step(sa, sb, IntC<0>{}, IntC<0>{}, i);
-      step(sb, sa, IntC<1>{}, IntC<1>{}, i + 1);
-    } else {
-      step(sa, sb, IntC<0>{}, IntC<1>{}, i);
-    }
+    finish<DT, kThreads>(p, w, row, slot, acc, m, l, 0);
+    if constexpr (!DEALT) return;
+    lds_barrier();                           // before the next one's keys and values
   }
-  l += __shfl_xor(l, 32, 64);
-
-  finish<DT, kThreads>(p, w, row, splits, acc, m, l, 0);
 }
 
 // Heads of 256: eight wavefronts, the first four (half 0) and the last four (half 1) on the same four
@@ -536,143 +767,161 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
 //   second  the products of tile i's weights and values; half 0 decodes the keys of tile i + 2
 // so that each of the matrix runs has the other side's decoding beside it, and one buffer of keys,
 // values and weights is enough.
-__global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem p, int row_blocks, int splits) {
+template <bool DEALT>
+__global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem args, int row_blocks, int splits,
+                                                           int groups) {
   constexpr int D = 256, KS = D / 16, DT = D / 32, N = DT / 2, kThreads = 512;
   __shared__ uint4 kl[2 * KS * 64];
   __shared__ uint4 vl[4 * DT * 64];
   __shared__ uint4 pl[4][4 * 64];           // [row tile][16-token step][lane]
   __shared__ float tops[2][4][2][32];       // [tile parity][row tile][half][row]
+  __shared__ uint32_t first[DEALT ? kMostEntries + 3 : 1];
   const int lane = threadIdx.x & 63, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rt = wave & 3, half = wave >> 2;
-  const Work w = my_work(p, 128, row_blocks, splits);
-  if (!w.any) return;
-  const Row row = row_of(p, w, rt);
-  bf16x8 qf[KS];
-  load_query(p, w, row, qf);
-  const Decoder<D> dec(p, w, rt);
+  Walk<kThreads, DEALT> walk(args, 128, row_blocks, splits, groups, first);
+  for (;;) {
+    const AttnProblem p = DEALT ? argument() : args;
+    Work w;
+    int slot;
+    if (!walk.next(p, 128, row_blocks, splits, first, &w, &slot)) return;
+    const Row row = row_of(p, w, rt);
+    bf16x8 qf[KS];
+    load_query(p, w, row, qf);
+    const Decoder<D> dec(p, w, rt);
 
-  v16f acc[N];
-  float m = -kInf, l = 0.f;
+    v16f acc[N];
+    float m = -kInf, l = 0.f;
 #pragma unroll
-  for (int d = 0; d < N; ++d) acc[d] = v16f(0.f);
-  Raw raw;
-  Place next;
+    for (int d = 0; d < N; ++d) acc[d] = v16f(0.f);
+    Raw raw;
+    Place next;
 
-  // Scores of tile i, masked, and their maxima for the other half.
-  auto score = [&](v16f& s, int32_t i) {
-    const int32_t t0 = w.t_begin + i * kTok;
-    scores(s, kl + half * KS * 64, qf, 0, KS);
-    if (t0 + kTok > w.full_hi || t0 < w.full_lo) mask(s, row, t0 + half * 32);
-    float top = s[0];
+    // Scores of tile i, masked, and their maxima for the other half.
+    auto score = [&](v16f& s, int32_t i) {
+      const int32_t t0 = w.t_begin + i * kTok;
+      scores(s, kl + half * KS * 64, qf, 0, KS);
+      if (t0 + kTok > w.full_hi || t0 < w.full_lo) mask(s, row, t0 + half * 32);
+      float top = s[0];
 #pragma unroll
-    for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
-    top = max_halves(top) * p.scale_log2;
-    if (lane < 32) tops[i & 1][rt][half][c] = top;
-  };
-  auto step = [&](v16f& s, v16f& sn, auto final, int32_t i) {
-    constexpr bool LAST = decltype(final)::value;
-    const int32_t t0 = w.t_begin + i * kTok;
-    const float top = fmaxf(tops[i & 1][rt][0][c], tops[i & 1][rt][1][c]);
-    // As in attn_many_kernel; both halves see the same maxima and move together.
-    if (__any(top > m + 8.f)) {
-      const float now = fmaxf(m, top);
-      const float f = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
-      m = now;
-      l *= f;
+      for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+      top = max_halves(top) * p.scale_log2;
+      if (lane < 32) tops[i & 1][rt][half][c] = top;
+    };
+    auto step = [&](v16f& s, v16f& sn, auto final, int32_t i) {
+      constexpr bool LAST = decltype(final)::value;
+      const int32_t t0 = w.t_begin + i * kTok;
+      const float top = fmaxf(tops[i & 1][rt][0][c], tops[i & 1][rt][1][c]);
+      // As in attn_many_kernel; both halves see the same maxima and move together.
+      if (__any(top > m + 8.f)) {
+        const float now = fmaxf(m, top);
+        const float f = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
+        m = now;
+        l *= f;
 #pragma unroll
-      for (int d = 0; d < N; ++d)
+        for (int d = 0; d < N; ++d)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[d][e] *= f;
-    }
-    const float sub = m == -kInf ? 0.f : m;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      pl[rt][(half * 2 + u) * 64 + lane] = __builtin_bit_cast(uint4, weights(s, 8 * u, p.scale_log2, sub, l));
-    if (half == 1) {
-      dec.decode_values(raw, t0, vl);
-      if constexpr (!LAST) {
-        dec.load_values(raw, next);
-        next = dec.place(t0 + 2 * kTok);
+          for (int e = 0; e < 16; ++e) acc[d][e] *= f;
       }
-    }
-    if constexpr (!LAST) score(sn, i + 1);
-    lds_barrier();
+      const float sub = m == -kInf ? 0.f : m;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const bf16x8 pf = __builtin_bit_cast(bf16x8, pl[rt][q * 64 + lane]);
+      for (int u = 0; u < 2; ++u)
+        pl[rt][(half * 2 + u) * 64 + lane] = __builtin_bit_cast(uint4, weights(s, 8 * u, p.scale_log2, sub, l));
+      if (half == 1) {
+        dec.decode_values(raw, t0, vl);
+        if constexpr (!LAST) {
+          dec.load_values(raw, next);
+          next = dec.place(t0 + 2 * kTok);
+        }
+      }
+      if constexpr (!LAST) score(sn, i + 1);
+      lds_barrier();
 #pragma unroll
-      for (int d = 0; d < N; ++d)
-        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8, vl[(q * DT + half * N + d) * 64 + lane]), pf, acc[d], 0, 0, 0);
-    }
-    if constexpr (!LAST) {
+      for (int q = 0; q < 4; ++q) {
+        const bf16x8 pf = __builtin_bit_cast(bf16x8, pl[rt][q * 64 + lane]);
+#pragma unroll
+        for (int d = 0; d < N; ++d)
+          acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8, vl[(q * DT + half * N + d) * 64 + lane]), pf, acc[d], 0, 0, 0);
+      }
+      if constexpr (!LAST) {
+        if (half == 0) {
+          dec.decode_keys(raw, kl);
+          dec.load_keys(raw, next);
+          next = dec.place(t0 + 4 * kTok);
+        }
+        lds_barrier();
+      }
+    };
+
+    if (w.tiles > 0) {
+      v16f sa, sb;
       if (half == 0) {
+        dec.load_keys(raw, dec.place(w.t_begin));
         dec.decode_keys(raw, kl);
-        dec.load_keys(raw, next);
-        next = dec.place(t0 + 4 * kTok);
+        dec.load_keys(raw, dec.place(w.t_begin + kTok));
+      } else {
+        dec.load_values(raw, dec.place(w.t_begin));
+        next = dec.place(w.t_begin + kTok);
       }
       lds_barrier();
+      score(sa, 0);
+      lds_barrier();                           // K(0) is read before K(1) overwrites it
+      if (half == 0) {
+        dec.decode_keys(raw, kl);
+        dec.load_keys(raw, dec.place(w.t_begin + 2 * kTok));
+        next = dec.place(w.t_begin + 3 * kTok);
+      }
+      lds_barrier();
+      int32_t i = 0;
+      for (; i + 2 < w.tiles; i += 2) {
+        step(sa, sb, IntC<0>{}, i);
+        step(sb, sa, IntC<0>{}, i + 1);
+      }
+      if (i + 1 < w.tiles) {
+        step(sa, sb, IntC<0>{}, i);
+        step(sb, sa, IntC<1>{}, i + 1);
+      } else {
+        step(sa, sb, IntC<1>{}, i);
+      }
     }
-  };
+    // A row's sum is that of its two halves' shares.
+    l += __shfl_xor(l, 32, 64);
+    lds_barrier();
+    if (lane < 32) tops[0][rt][half][c] = l;
+    lds_barrier();
+    l += tops[0][rt][half ^ 1][c];
 
-  if (w.tiles > 0) {
-    v16f sa, sb;
-    if (half == 0) {
-      dec.load_keys(raw, dec.place(w.t_begin));
-      dec.decode_keys(raw, kl);
-      dec.load_keys(raw, dec.place(w.t_begin + kTok));
-    } else {
-      dec.load_values(raw, dec.place(w.t_begin));
-      next = dec.place(w.t_begin + kTok);
-    }
-    lds_barrier();
-    score(sa, 0);
-    lds_barrier();                           // K(0) is read before K(1) overwrites it
-    if (half == 0) {
-      dec.decode_keys(raw, kl);
-      dec.load_keys(raw, dec.place(w.t_begin + 2 * kTok));
-      next = dec.place(w.t_begin + 3 * kTok);
-    }
-    lds_barrier();
-    int32_t i = 0;
-    for (; i + 2 < w.tiles; i += 2) {
-      step(sa, sb, IntC<0>{}, i);
-      step(sb, sa, IntC<0>{}, i + 1);
-    }
-    if (i + 1 < w.tiles) {
-      step(sa, sb, IntC<0>{}, i);
-      step(sb, sa, IntC<1>{}, i + 1);
-    } else {
-      step(sa, sb, IntC<1>{}, i);
-    }
+    finish<DT, kThreads>(p, w, row, slot, acc, m, l, half * N);
+    if constexpr (!DEALT) return;
+    lds_barrier();                           // before the next one's keys and values
   }
-  // A row's sum is that of its two halves' shares.
-  l += __shfl_xor(l, 32, 64);
-  lds_barrier();
-  if (lane < 32) tops[0][rt][half][c] = l;
-  lds_barrier();
-  l += tops[0][rt][half ^ 1][c];
-
-  finish<DT, kThreads>(p, w, row, splits, acc, m, l, half * N);
 }
 
 template <int D, int NW>
 hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
   constexpr int DT = D / 32, kThreads = D == 256 ? 512 : 64 * NW, N = D == 256 ? DT / 2 : DT;
   const int64_t units = static_cast<int64_t>(plan.row_blocks) * p.batch * p.cache.heads;
-  if (units * plan.splits > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(units * plan.splits));
-  if constexpr (D == 256)
-    hipLaunchKernelGGL(attn_wide_kernel, grid, dim3(kThreads), 0, stream, p, plan.row_blocks, plan.splits);
-  else
-    hipLaunchKernelGGL((attn_many_kernel<D, NW>), grid, dim3(kThreads), 0, stream, p, plan.row_blocks,
-                       plan.splits);
+  const int64_t most = std::max<int64_t>(units * plan.splits, plan.groups);
+  if (most > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(most));
+  auto attend = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p, plan.row_blocks, plan.splits, plan.groups);
+  };
+  if constexpr (D == 256) {
+    if (plan.groups) attend(attn_wide_kernel<true>);
+    else attend(attn_wide_kernel<false>);
+  } else {
+    if (plan.groups) attend(attn_many_kernel<D, NW, true>);
+    else attend(attn_many_kernel<D, NW, false>);
+  }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || plan.splits == 1) return e;
+  if (e != hipSuccess || (plan.splits == 1 && plan.groups == 0)) return e;
+  // At most so many units have parts: there are no more, and a run begins inside of each in a deal.
+  const int64_t joined = plan.groups ? std::min<int64_t>(units, plan.groups - 1) : units;
   hipLaunchKernelGGL((attn_join_kernel<DT, kThreads, N, D == 256 ? 2 : 1>),
-                     dim3(static_cast<unsigned>(units * (2 * N))), dim3(kThreads), 0, stream, p,
-                     plan.splits);
+                     dim3(static_cast<unsigned>(joined * (2 * N))), dim3(kThreads), 0, stream, p,
+                     plan.row_blocks, plan.splits, plan.groups);
   return hipGetLastError();
 }
 
@@ -689,9 +938,8 @@ constexpr int64_t few_part_bytes(int head_dim, int row_tiles) {
   return int64_t{2} * 256 * few_waves(head_dim, row_tiles) * 16 * row_tiles * (head_dim + 2) * 4;
 }
 
-// Threads of the workgroups that the parts of a problem of many rows keep at most: a workgroup for
-// every CU (two of four wavefronts).
-constexpr int64_t kPartThreads = 256 * 512;
+// Threads that the chip holds of these kernels: eight wavefronts a CU.
+constexpr int64_t kChipThreads = 256 * 512;
 
 }  // namespace
 
@@ -711,10 +959,11 @@ AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
   const int64_t block_rows = 32 * a.row_tiles, threads = head_dim == 256 ? 512 : 64 * a.row_tiles;
   const int64_t blocks = (rows + block_rows - 1) / block_rows;
   a.row_blocks = static_cast<int>(blocks);
-  const int64_t fit = kPartThreads / threads / (blocks * units);
+  const int64_t groups = kChipThreads / threads, fit = groups / (blocks * units);
   a.splits = static_cast<int>(fit < 1 ? 1 : fit > 64 ? 64 : fit);
-  if (a.splits > 1)
-    a.part_bytes = blocks * units * a.splits * 4 * part_floats(threads, head_dim == 64 ? 2 : 4);
+  if (batch > 1 && blocks * units < kDealUnits * groups) a.groups = static_cast<int>(groups);
+  if (a.splits > 1 || a.groups > 0)
+    a.part_bytes = 4 * (kStartFloats + (a.groups ? 2 : 1) * groups * part_floats(threads, head_dim == 64 ? 2 : 4));
   return a;
 }
 
@@ -724,7 +973,7 @@ int64_t most_part_bytes(int64_t max_q, int64_t group, int head_dim) {
   for (int t = 1; t <= few_tiles(head_dim); t *= 2)
     if (t == 1 || rows > 8 * t) most = std::max(most, few_part_bytes(head_dim, t));
   if (rows > 16 * few_tiles(head_dim))
-    most = std::max(most, kPartThreads * 4 * (16 * (head_dim == 64 ? 2 : 4) + 1));
+    most = std::max(most, 4 * (kStartFloats + 2 * kChipThreads * (16 * (head_dim == 64 ? 2 : 4) + 1)));
   return most;
 }
 

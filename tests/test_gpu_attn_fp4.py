@@ -102,6 +102,26 @@ def test_a_chunk_against_a_long_past_is_split(mx, D):
     attention_close(out, lse, oracle(paged, q, uniform(96, 2), D ** -0.5))
 
 
+@pytest.mark.parametrize("D,nq,hk,group,page", [(64, 70, 33, 2, 32), (128, 70, 33, 2, 64), (128, 35, 65, 2, 16),
+                                                (256, 40, 33, 1, 48)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1500)])
+def test_chunks_of_very_different_lengths_are_dealt(mx, D, nq, hk, group, page, causal, window):
+    # nearly all keys are one sequence's: its blocks' tiles are dealt to all workgroups, runs begin and
+    # end inside of them, and the rows of most heads are joined from several parts
+    rng = np.random.default_rng(11 * D + hk + window)
+    lens, news = [2200, 900, 0, 130], [nq, 3, 0, nq // 2]
+    starts = [0, *np.cumsum(news).tolist()]
+    paged = Paged(rng, lens, hk, D, page)
+    q = queries(rng, starts[-1], hk * group, D)
+    ws = torch.zeros(mx.mx_attn_fp4_workspace_size(4, nq, hk * group, hk, D), dtype=torch.uint8, device="cuda")
+    note(f"attn dealt D={D} nq={nq} hk={hk} group={group} causal={causal} window={window}")
+    how = dict(starts=starts, max_q=nq, ws=ws, causal=causal, window=window)
+    out, lse = run(mx, paged, q, **how)
+    attention_close(out, lse, oracle(paged, q, starts, D ** -0.5, causal=causal, window=window))
+    again, lse2 = run(mx, paged, q, **how)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_ragged_tokens_split_over_many_workgroups(mx):
     rng = np.random.default_rng(5)
     lens = [9000, 0, 1, 130, 4097, 17, 2, 640]
