@@ -102,7 +102,9 @@ constexpr int kLeastPart = 4;
 constexpr int kMostEntries = 2048;         // (sequence, block) pairs of a deal
 constexpr int kMostGroups = 512;
 
-__device__ __forceinline__ int parts_of(int tiles, int splits) { return max(1, min(splits, tiles / kLeastPart)); }
+__device__ __forceinline__ int parts_of(int tiles, int splits) {
+  return max(1, min(splits, tiles / kLeastPart));
+}
 
 // Where a run begins, and the unit it begins in: its first slot and the one after its last, its number
 // (head, sequence, block).  Left in the workspace for the join; the first run's holds the number of runs
@@ -192,8 +194,8 @@ __device__ __forceinline__ Deal deal(const AttnProblem& p, int block_rows, int r
   return d;
 }
 
-// The kernel's argument, read again: what a workgroup derives from it for one unit is not kept in
-// registers for the next (that cost spills in the loop over tokens).
+// The kernel's first argument, read again from its place: what a workgroup derives from it for one
+// unit is not kept in registers for the next (that cost spills in the loop over tokens).
 __device__ __forceinline__ AttnProblem argument() {
   auto at = reinterpret_cast<uintptr_t>(__builtin_amdgcn_kernarg_segment_ptr());
   asm volatile("" : "+s"(at));
@@ -208,8 +210,8 @@ struct Walk {
   uint32_t g, x, end;
   bool dealt;
 
-  __device__ __forceinline__ Walk(const AttnProblem& p, int block_rows, int row_blocks, int splits, int groups,
-                                  uint32_t* first) {
+  __device__ __forceinline__ Walk(const AttnProblem& p, int block_rows, int row_blocks, int splits,
+                                  int groups, uint32_t* first) {
     x = 0;
     end = 1;
     dealt = false;
