@@ -34,7 +34,7 @@ constexpr int kThreads = 256, kWaves = 4, kWaveTokens = 32, kTile = kWaves * kWa
 // One sequence's rows and keys.
 struct Sequence {
   int32_t len, rows, q0, n;    // cached tokens; query rows (n queries x group); first query
-  int32_t lo, hi;              // keys that any of its rows sees, lo down to a multiple of 32
+  int32_t low, lo, hi;         // keys that any of its rows sees: [low, hi); lo: low down to a multiple of 32
   int32_t tiles;               // 0: no rows; at least 1 otherwise (a row that sees nothing is written)
 };
 
@@ -48,7 +48,8 @@ __device__ __forceinline__ Sequence sequence_of(const AttnProblem& p, int32_t le
   s.rows = s.n * p.group;
   s.hi = s.len;
   const int32_t first = s.len - s.n;                     // the first query's position
-  s.lo = p.window > 0 ? max(first + 1 - p.window, 0) & ~31 : 0;
+  s.low = p.window > 0 ? max(first + 1 - p.window, 0) : 0;
+  s.lo = s.low & ~31;
   s.tiles = s.n == 0 ? 0 : max(1, (s.hi - s.lo + kTile - 1) / kTile);
   return s;
 }
@@ -402,8 +403,8 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
                                                        pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])));
       }
       // The values' scales: the scaled conversions read a scale's exponent field alone, so the word is
-      // rotated until the lane's byte lies there.  What lies past the keys is given scale 1: finite,
-      // and its weight is 0.
+      // rotated until the lane's byte lies there.  What lies past the keys, or before the oldest window,
+      // is given scale 1: finite, and its weight is 0.
       const int vs = static_cast<int>(rv.s);
       const uint32_t vss[2] = {
           static_cast<uint32_t>(__builtin_amdgcn_update_dpp(vs, vs, 0x114, 0xF, 0xA, false)),   // from quads 0, 2
@@ -412,10 +413,12 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         vsc[i] = scale_of_byte(quad_lane(vss[i >> 2], i & 3), turn_vs);
-      if (tok0 + kWaveTokens > sq.hi) {
+      if (tok0 + kWaveTokens > sq.hi || tok0 < sq.low) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (tok0 + (i >> 2) * 16 + (i & 3) * 4 + g >= sq.hi) vsc[i] = 1.f;
+        for (int i = 0; i < 8; ++i) {
+          const int32_t t = tok0 + (i >> 2) * 16 + (i & 3) * 4 + g;
+          if (t >= sq.hi || t < sq.low) vsc[i] = 1.f;
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       // D == 64: lane c loaded 8 codes of one token, lane c + 8 the same 8 of another; each keeps its

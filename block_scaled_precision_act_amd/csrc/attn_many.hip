@@ -39,7 +39,8 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 struct Work {
   int32_t b, h, blk;
   int32_t len, q0, rows, r0, first;       // first: the position of the sequence's first query
-  int32_t hi, t_begin, tiles;             // keys end; the run's first token and tiles of 64
+  int32_t low, hi;                        // keys that any of its rows sees: [low, hi)
+  int32_t t_begin, tiles;                 // the run's first token and tiles of 64
   int32_t full_hi, full_lo;               // tokens below and from which every row sees
   bool any;                               // the block has rows
 };
@@ -68,7 +69,8 @@ __device__ __forceinline__ Work unit_of(const AttnProblem& p, int block_rows, in
   w.first = w.len - n;
   const int32_t tok_lo = w.r0 / p.group, tok_hi = (min(w.r0 + block_rows, w.rows) - 1) / p.group;
   w.hi = p.causal ? min(max(w.first + tok_hi + 1, 0), w.len) : w.len;
-  w.t_begin = p.window > 0 ? max(w.first + tok_lo + 1 - p.window, 0) & ~(kTok - 1) : 0;
+  w.low = p.window > 0 ? max(w.first + tok_lo + 1 - p.window, 0) : 0;
+  w.t_begin = w.low & ~(kTok - 1);
   w.tiles = max(0, (w.hi - w.t_begin + kTok - 1) / kTok);
   w.full_hi = p.causal ? min(w.first + tok_lo + 1, w.len) : w.len;
   w.full_lo = p.window > 0 ? w.first + tok_hi + 1 - p.window : 0;
@@ -322,7 +324,7 @@ struct Decoder {
   const AttnProblem& p;
   const uint8_t *kbase, *vbase, *ksbase, *vsbase;
   int64_t trow;
-  int32_t hi, last16;
+  int32_t low, hi, last16;
   uint32_t page16, turn_k;
   int sub, k16, kq, vc, vh;
 
@@ -333,6 +335,7 @@ struct Decoder {
     ksbase = p.cache.ks + w.h * p.cache.scale_head;
     vsbase = p.cache.vs + w.h * p.cache.scale_head;
     trow = static_cast<int64_t>(w.b) * p.table_stride;
+    low = w.low;
     hi = w.hi;
     last16 = (w.hi - 1) >> 4;
     page16 = p.cache.page_size >> 4;
@@ -408,11 +411,14 @@ struct Decoder {
     for (int i = 0; i < 8; ++i)
       sc[i] = scale_of_byte(w.x[8 + (D == 64 ? 4 * (i >> 2) + ((i & 3) >> 1) : i)],
                             D == 64 && (i & 1) ? turn + 16 : turn);
-    // What lies past the keys is given scale 1: finite, and its weight is 0.
-    if (t0 + kTok > hi) {
+    // What lies past the keys, or before the block's oldest window, is given scale 1: finite, and its
+    // weight is 0.
+    if (t0 + kTok > hi || t0 < low) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (t0 + sub * 16 + (i >> 2) * 8 + vh * 4 + (i & 3) >= hi) sc[i] = 1.f;
+      for (int i = 0; i < 8; ++i) {
+        const int32_t t = t0 + sub * 16 + (i >> 2) * 8 + vh * 4 + (i & 3);
+        if (t >= hi || t < low) sc[i] = 1.f;
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll

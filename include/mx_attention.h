@@ -160,7 +160,10 @@ int mx_kv_append_fp4(const mx_kv_append_fp4_args* args, void* stream);
  *   s_t = scale * q . k_t;  out = sum_t softmax(s)_t v_t, rounded once to bf16;
  *   lse (or NULL) = ln sum_t exp(s_t), fp32 [total_q, q_heads].
  * A query that sees no key gets zeros and lse -infinity.  What lies in the cache beyond a
- * sequence's length is never used, whatever its bytes.
+ * sequence's length, or before the window of its first query, is never used, whatever its bytes
+ * (pages that hold nothing else may be freed, and their table entries be anything).  Among the tokens
+ * between, a query's mask hides keys of any bytes but only finite values: a value scale byte of 253
+ * to 255, which mx_kv_append_fp4 never stores, can make queries NaN that do not see its token.
  * |scale| must be below 1e30.
  * seq_lens, q_starts and page_table entries are read on the device: lengths are clamped to what
  * the table covers, and an entry outside [0, pages) reads page 0 instead of memory that is not

@@ -1,0 +1,59 @@
+"""Attention over the paged MXFP4 cache (mx_attn_fp4) at the edges of what it accepts, against the
+float64 oracle with the bounds of attention_util.attention_close."""
+import numpy as np
+import pytest
+import torch
+
+from attention_util import Paged, attention_close, f64, oracle
+from gpu_util import note
+from test_gpu_attn_fp4 import queries, run, uniform
+
+pytestmark = pytest.mark.gpu
+
+
+def evict(paged, news, window):
+    """Drops what lies before each sequence's oldest window: bytes 0xFF (every scale NaN), pages that
+    hold nothing else -1 in the table, and page 0, which is read in their place, 0xFF throughout."""
+    arrays = (paged.k, paged.ks, paged.v, paged.vs)
+    page = paged.page_size
+    free = next(i for i in range(len(paged.k)) if i not in paged.table)
+    for a in arrays:
+        a[free] = a[0]
+        a[0] = 0xFF
+    paged.table[paged.table == 0] = free
+    for b, (length, n) in enumerate(zip(paged.lens, news)):
+        low = max(length - n + 1 - window, 0)
+        for t in range(min(low, length)):
+            for a in arrays:
+                a[paged.table[b, t // page], :, t % page] = 0xFF
+        paged.table[b, :low // page] = -1
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq,group,window", [(1, 4, 1), (1, 8, 50), (1, 16, 501), (4, 8, 50), (5, 6, 200),
+                                             (70, 2, 50), (70, 4, 333), (300, 1, 37)])
+def test_what_lies_before_the_window_is_never_used(mx, D, nq, group, window):
+    # windows that begin inside a page, inside a step and inside a tile, and whole pages before them
+    rng = np.random.default_rng(D + nq + window)
+    lens = [nq + n for n in (0, 1, 17, 100, 395, 600, 1177)]
+    paged = Paged(rng, lens, 2, D, 16)
+    evict(paged, [nq] * len(lens), window)
+    q = queries(rng, nq * len(lens), 2 * group, D)
+    note(f"attn evicted D={D} nq={nq} group={group} window={window}")
+    out, lse = run(mx, paged, q, window=window)
+    ref = oracle(paged, q, uniform(nq, len(lens)), D ** -0.5, window=window)
+    assert not np.isnan(ref[0]).any()
+    attention_close(out, lse, ref)
+
+
+@pytest.mark.parametrize("D,nq,hk,page", [(128, 70, 33, 16), (256, 40, 33, 16)])
+def test_what_lies_before_the_window_is_never_used_in_a_deal(mx, D, nq, hk, page):
+    rng = np.random.default_rng(D + nq)
+    lens, news = [2600, 900, 0, 130], [nq, 3, 0, nq // 2]
+    starts = [0, *np.cumsum(news).tolist()]
+    paged = Paged(rng, lens, hk, D, page)
+    evict(paged, news, 2205)
+    q = queries(rng, starts[-1], 2 * hk, D)
+    note(f"attn evicted, dealt D={D} nq={nq}")
+    out, lse = run(mx, paged, q, starts=starts, max_q=nq, window=2205)
+    attention_close(out, lse, oracle(paged, q, starts, D ** -0.5, window=2205))
