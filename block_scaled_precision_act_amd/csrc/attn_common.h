@@ -87,6 +87,13 @@ __device__ __forceinline__ float max_halves(float v) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// The first key that a query at position `at` sees, or a number below 0.  A position is negative where a
+// sequence is shorter than its queries; such a query sees no key, and counting it as -1 keeps the
+// difference within 32 bits for windows of up to 2^31 - 1.
+__device__ __forceinline__ int32_t window_start(int32_t at, int32_t window) {
+  return max(at, -1) + 1 - window;
+}
+
 // Workgroup barrier for data passed through LDS: waits for the wavefront's LDS accesses only, so
 // loads from memory stay in flight across it.
 __device__ __forceinline__ void lds_barrier() {

@@ -48,7 +48,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttnProblem& p, int32_t le
   s.rows = s.n * p.group;
   s.hi = s.len;
   const int32_t first = s.len - s.n;                     // the first query's position
-  s.low = p.window > 0 ? max(first + 1 - p.window, 0) : 0;
+  s.low = p.window > 0 ? max(window_start(first, p.window), 0) : 0;
   s.lo = s.low & ~31;
   s.tiles = s.n == 0 ? 0 : max(1, (s.hi - s.lo + kTile - 1) / kTile);
   return s;
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       const int tok = r / p.group, hg = r - tok * p.group;
       const bool live = r < sq.rows;
       hi_row[mt] = live && p.causal ? first + tok + 1 : sq.len;
-      lo_row[mt] = live && p.window > 0 ? first + tok + 1 - p.window : 0;
+      lo_row[mt] = live && p.window > 0 ? window_start(first + tok, p.window) : 0;
       const uint16_t* row = p.q.p + static_cast<int64_t>(sq.q0 + tok) * p.q.token_stride +
                             static_cast<int64_t>(h * p.group + hg) * p.q.head_stride + g * (D / 4);
 #pragma unroll

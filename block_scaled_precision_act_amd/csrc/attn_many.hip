@@ -69,11 +69,11 @@ __device__ __forceinline__ Work unit_of(const AttnProblem& p, int block_rows, in
   w.first = w.len - n;
   const int32_t tok_lo = w.r0 / p.group, tok_hi = (min(w.r0 + block_rows, w.rows) - 1) / p.group;
   w.hi = p.causal ? min(max(w.first + tok_hi + 1, 0), w.len) : w.len;
-  w.low = p.window > 0 ? max(w.first + tok_lo + 1 - p.window, 0) : 0;
+  w.low = p.window > 0 ? max(window_start(w.first + tok_lo, p.window), 0) : 0;
   w.t_begin = w.low & ~(kTok - 1);
   w.tiles = max(0, (w.hi - w.t_begin + kTok - 1) / kTok);
   w.full_hi = p.causal ? min(w.first + tok_lo + 1, w.len) : w.len;
-  w.full_lo = p.window > 0 ? w.first + tok_hi + 1 - p.window : 0;
+  w.full_lo = p.window > 0 ? window_start(w.first + tok_hi, p.window) : 0;
   return w;
 }
 
@@ -283,7 +283,7 @@ __device__ __forceinline__ Row row_of(const AttnProblem& p, const Work& w, int t
   r.tok = r.live ? i / p.group : 0;
   r.hg = r.live ? i - r.tok * p.group : 0;
   r.hi = r.live && p.causal ? w.first + r.tok + 1 : w.len;
-  r.lo = r.live && p.window > 0 ? w.first + r.tok + 1 - p.window : 0;
+  r.lo = r.live && p.window > 0 ? window_start(w.first + r.tok, p.window) : 0;
   return r;
 }
 

@@ -57,3 +57,19 @@ def test_what_lies_before_the_window_is_never_used_in_a_deal(mx, D, nq, hk, page
     note(f"attn evicted, dealt D={D} nq={nq}")
     out, lse = run(mx, paged, q, starts=starts, max_q=nq, window=2205)
     attention_close(out, lse, oracle(paged, q, starts, D ** -0.5, window=2205))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq,group", [(4, 4), (9, 6), (70, 2), (300, 1)])
+def test_the_widest_windows_hide_nothing(mx, D, nq, group):
+    # sequences shorter than their queries: the first positions are negative
+    rng = np.random.default_rng(D + nq)
+    lens = [0, 1, nq // 3, nq - 1, nq, nq + 200]
+    paged = Paged(rng, lens, 2, D, 16)
+    q = queries(rng, nq * len(lens), 2 * group, D)
+    note(f"attn widest windows D={D} nq={nq} group={group}")
+    want, want_lse = run(mx, paged, q)
+    attention_close(want, want_lse, oracle(paged, q, uniform(nq, len(lens)), D ** -0.5))
+    for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - nq):
+        out, lse = run(mx, paged, q, window=window)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse), window
