@@ -272,8 +272,10 @@ int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
       !(std::fabs(a->scale) < 1e30))
     return MX_ERR_SHAPE;
   if (!a->q_starts && a->total_q != a->batch * a->max_q) return MX_ERR_SHAPE;
-  // Tokens a table row covers, and the exactness of the page number as a high product.
-  if (!fits31(a->table_width, c.page_size)) return MX_ERR_SHAPE;
+  // Tokens a table row covers: the kernels count in 31 bits, and look up to kLookAhead tokens past a
+  // length.  And the exactness of the page number as a high product.
+  if (!fits31(a->table_width, c.page_size) || a->table_width * c.page_size > kMax31 + 1 - mx::kLookAhead)
+    return MX_ERR_SHAPE;
   const int64_t d = c.page_size / 16;
   if (a->table_width * d * d >= (int64_t{1} << 32)) return MX_ERR_SHAPE;
   if (a->table_stride < 0 || (a->batch > 1 && a->table_stride < a->table_width))

@@ -86,6 +86,10 @@ struct AttnProblem {
   float* parts;
 };
 
+// Tokens past a sequence's length that the kernels' token numbers may reach (the rounding to a tile, and
+// the next tiles' places, looked up before it is known whether they are needed): 128 and 256 at most.
+constexpr int64_t kLookAhead = 1024;
+
 // A workspace begins with the arrival counters of few rows, one per (sequence, key/value head), zero
 // between calls; partial results follow at a fixed place, whatever the sizes, so calls of any sizes
 // can share a workspace.  Counters lie a cache line apart while that fits (arrivals on neighbouring

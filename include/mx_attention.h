@@ -164,7 +164,7 @@ int mx_kv_append_fp4(const mx_kv_append_fp4_args* args, void* stream);
  * (pages that hold nothing else may be freed, and their table entries be anything).  Among the tokens
  * between, a query's mask hides keys of any bytes but only finite values: a value scale byte of 253
  * to 255, which mx_kv_append_fp4 never stores, can make queries NaN that do not see its token.
- * |scale| must be below 1e30.
+ * |scale| must be below 1e30.  table_width * page_size is at most 2^31 - 1024.
  * seq_lens, q_starts and page_table entries are read on the device: lengths are clamped to what
  * the table covers, and an entry outside [0, pages) reads page 0 instead of memory that is not
  * the cache's.
