@@ -7,6 +7,9 @@
 
 namespace mx {
 
+// Workgroups of `threads` that one dimension of a grid holds: it counts fewer than 2^32 threads.
+constexpr int64_t most_groups(int threads) { return ((int64_t{1} << 32) - 1) / threads; }
+
 // Position rotation (see mx_attention.h).  positions == nullptr: none.
 struct Rotation {
   const int32_t* positions;

@@ -206,6 +206,10 @@ __device__ __forceinline__ AttnProblem argument() {
   return p;
 }
 
+// The workgroup's number: a grid of more workgroups than one dimension holds has a second one, and then
+// up to as many workgroups to spare.
+__device__ __forceinline__ uint32_t group_number() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // A workgroup's units or parts, one after the other.  `groups`: runs of a deal (DEALT).
 template <int THREADS, bool DEALT>
 struct Walk {
@@ -245,7 +249,8 @@ struct Walk {
     if (x >= end) return false;
     if (!DEALT || !dealt) {
       x = end;
-      const uint32_t heads = p.cache.heads, h = blockIdx.x % heads, r = blockIdx.x / heads, b = r % p.batch;
+      const uint32_t heads = p.cache.heads, id = group_number(), h = id % heads, r = id / heads, b = r % p.batch;
+      if (r / p.batch / splits >= static_cast<uint32_t>(row_blocks)) return false;
       const int part = r / p.batch % splits, blk = row_blocks - 1 - static_cast<int>(r / p.batch / splits);
       *w = unit_of(p, block_rows, h, b, blk);
       const int parts = parts_of(w->tiles, splits);
@@ -912,7 +917,9 @@ hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream
   const int64_t units = static_cast<int64_t>(plan.row_blocks) * p.batch * p.cache.heads;
   const int64_t most = std::max<int64_t>(units * plan.splits, plan.groups);
   if (most > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(most));
+  // A deal and the join have few workgroups.
+  const int64_t rows = (most + most_groups(kThreads) - 1) / most_groups(kThreads);
+  const dim3 grid(static_cast<unsigned>((most + rows - 1) / rows), static_cast<unsigned>(rows));
   auto attend = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p, plan.row_blocks, plan.splits, plan.groups);
   };

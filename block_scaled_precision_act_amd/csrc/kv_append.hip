@@ -12,6 +12,8 @@
 // thirds of it the launch.
 #include "attn_common.h"
 
+#include <algorithm>
+
 namespace mx {
 namespace {
 
@@ -179,13 +181,26 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvAppendProbl
 }
 
 template <int LR, int U>
-hipError_t launch_u(const KvAppendProblem& p, hipStream_t stream) {
-  constexpr int RG = kThreads / LR;
-  const uint32_t units = (p.cache.heads + U - 1) / U;
-  const uint64_t all = static_cast<uint64_t>(p.tokens) * units;
-  hipLaunchKernelGGL((kv_append_kernel<LR, U>), dim3(static_cast<unsigned>((all + RG - 1) / RG)),
-                     dim3(kThreads), 0, stream, p, units);
-  return hipGetLastError();
+hipError_t launch_u(KvAppendProblem p, hipStream_t stream) {
+  constexpr int64_t RG = kThreads / LR;
+  const uint32_t units = (p.cache.heads + U - 1) / U, tokens = p.tokens;
+  const uint32_t most = static_cast<uint32_t>(std::min<int64_t>(tokens, most_groups(kThreads) * RG / units));
+  for (uint32_t t = 0; t < tokens; t += most) {      // all at once, unless a grid does not hold them
+    p.tokens = std::min(most, tokens - t);
+    const int64_t all = static_cast<int64_t>(p.tokens) * units;
+    hipLaunchKernelGGL((kv_append_kernel<LR, U>), dim3(static_cast<unsigned>((all + RG - 1) / RG)),
+                       dim3(kThreads), 0, stream, p, units);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    p.k.p += p.tokens * p.k.token_stride;
+    p.v.p += p.tokens * p.v.token_stride;
+    p.slots += p.tokens;
+    if (p.rot.positions) p.rot.positions += p.tokens;
+    const int64_t values = static_cast<int64_t>(p.tokens) * p.cache.heads * (8 * LR);
+    if (p.k_out) p.k_out += values;
+    if (p.v_out) p.v_out += values;
+  }
+  return hipSuccess;
 }
 
 // From this many values on a row's owners take two heads at once; below, one, as the rows then do not

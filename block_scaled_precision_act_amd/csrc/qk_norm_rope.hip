@@ -13,6 +13,8 @@
 // are log2(D / 8) lane exchanges, and loads are 8 bytes a lane in runs of at least 32 bytes.
 #include "attn_common.h"
 
+#include <algorithm>
+
 namespace mx {
 namespace {
 
@@ -278,17 +280,30 @@ __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRope
 }
 
 template <int LR, int U>
-hipError_t launch_forward_u(const NormRopeProblem& p, hipStream_t stream) {
-  constexpr uint64_t RG = kThreads / LR;
+hipError_t launch_forward_u(NormRopeProblem p, hipStream_t stream) {
+  constexpr int64_t RG = kThreads / LR;
   const uint32_t units_q = (p.heads[0] + U - 1) / U, units = units_q + (p.heads[1] + U - 1) / U;
-  const dim3 grid(static_cast<unsigned>((static_cast<uint64_t>(p.tokens) * units + RG - 1) / RG));
-  if (p.rot.interleaved)
-    hipLaunchKernelGGL((norm_rope_kernel<LR, true, U>), grid, dim3(kThreads), 0, stream, p, units_q,
-                       units);
-  else
-    hipLaunchKernelGGL((norm_rope_kernel<LR, false, U>), grid, dim3(kThreads), 0, stream, p, units_q,
-                       units);
-  return hipGetLastError();
+  const uint32_t tokens = p.tokens;
+  const uint32_t most = static_cast<uint32_t>(std::min<int64_t>(tokens, most_groups(kThreads) * RG / units));
+  for (uint32_t t = 0; t < tokens; t += most) {      // all at once, unless a grid does not hold them
+    p.tokens = std::min(most, tokens - t);
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.tokens) * units + RG - 1) / RG));
+    if (p.rot.interleaved)
+      hipLaunchKernelGGL((norm_rope_kernel<LR, true, U>), grid, dim3(kThreads), 0, stream, p, units_q,
+                         units);
+    else
+      hipLaunchKernelGGL((norm_rope_kernel<LR, false, U>), grid, dim3(kThreads), 0, stream, p, units_q,
+                         units);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    for (int i = 0; i < 2; ++i) {
+      if (p.heads[i] == 0) continue;
+      p.x[i].p += p.tokens * p.x[i].token_stride;
+      p.out[i].p += p.tokens * p.out[i].token_stride;
+    }
+    if (p.rot.positions) p.rot.positions += p.tokens;
+  }
+  return hipSuccess;
 }
 
 template <int LR>
