@@ -66,6 +66,8 @@ __device__ __forceinline__ float scale_of_byte(uint32_t word, uint32_t turn) {
   return __uint_as_float(__builtin_amdgcn_alignbit(word, word, turn));
 }
 
+constexpr uint32_t kScalesOfOne = 0x7F7F7F7Fu;       // four E8M0 bytes
+
 // The value of lane `i` (0..3, constant after unrolling) of each group of four.
 __device__ __forceinline__ uint32_t quad_lane(uint32_t v, int i) {
   const int x = static_cast<int>(v);
@@ -92,6 +94,12 @@ __device__ __forceinline__ float max_halves(float v) {
 // difference within 32 bits for windows of up to 2^31 - 1.
 __device__ __forceinline__ int32_t window_start(int32_t at, int32_t window) {
   return max(at, -1) + 1 - window;
+}
+
+// The same value, but not known to be: what was computed from it before is computed again.
+__device__ __forceinline__ uint32_t again(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 
 // Workgroup barrier for data passed through LDS: waits for the wavefront's LDS accesses only, so

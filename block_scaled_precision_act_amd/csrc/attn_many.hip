@@ -249,8 +249,9 @@ struct Walk {
     if (x >= end) return false;
     if (!DEALT || !dealt) {
       x = end;
-      const uint32_t heads = p.cache.heads, id = group_number(), h = id % heads, r = id / heads, b = r % p.batch;
-      if (r / p.batch / splits >= static_cast<uint32_t>(row_blocks)) return false;
+      const uint32_t id = DEALT ? blockIdx.x : group_number();       // a deal's grid has one dimension
+      const uint32_t heads = p.cache.heads, h = id % heads, r = id / heads, b = r % p.batch;
+      if (!DEALT && r / p.batch / splits >= static_cast<uint32_t>(row_blocks)) return false;
       const int part = r / p.batch % splits, blk = row_blocks - 1 - static_cast<int>(r / p.batch / splits);
       *w = unit_of(p, block_rows, h, b, blk);
       const int parts = parts_of(w->tiles, splits);
@@ -281,9 +282,9 @@ struct Row {
   int32_t tok, hg, lo, hi;                // query, grouped head, the keys it sees
 };
 
-__device__ __forceinline__ Row row_of(const AttnProblem& p, const Work& w, int tile) {
+__device__ __forceinline__ Row row_of(const AttnProblem& p, const Work& w, int tile, uint32_t thread = threadIdx.x) {
   Row r;
-  const int32_t i = w.r0 + tile * 32 + (threadIdx.x & 31);
+  const int32_t i = w.r0 + tile * 32 + (thread & 31);
   r.live = i < w.rows;
   r.tok = r.live ? i / p.group : 0;
   r.hg = r.live ? i - r.tok * p.group : 0;
@@ -329,7 +330,7 @@ struct Decoder {
   const AttnProblem& p;
   const uint8_t *kbase, *vbase, *ksbase, *vsbase;
   int64_t trow;
-  int32_t low, hi, last16;
+  int32_t hi, last16;
   uint32_t page16, turn_k;
   int sub, k16, kq, vc, vh;
 
@@ -340,7 +341,6 @@ struct Decoder {
     ksbase = p.cache.ks + w.h * p.cache.scale_head;
     vsbase = p.cache.vs + w.h * p.cache.scale_head;
     trow = static_cast<int64_t>(w.b) * p.table_stride;
-    low = w.low;
     hi = w.hi;
     last16 = (w.hi - 1) >> 4;
     page16 = p.cache.page_size >> 4;
@@ -397,6 +397,19 @@ struct Decoder {
       }
     }
   }
+  // The same for what lies before the block's oldest window, of a run's first tile alone: here, as a test
+  // of every tile in decode_values takes 25 us more of a chunk's 495 (heads of 256).
+  __device__ __forceinline__ void load_first_values(Raw& w, const Work& u) const {
+    load_values(w, place(u.t_begin));
+    if (u.t_begin >= u.low) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (u.t_begin + sub * 16 + (i >> 2) * 8 + vh * 4 + (i & 3) >= u.low) continue;
+      uint32_t& x = w.x[8 + (D == 64 ? 4 * (i >> 2) + ((i & 3) >> 1) : i)];
+      const uint32_t mine = D == 64 ? 0xFFFFu << (16 * (i & 1)) : ~0u;      // heads of 64: two tokens a word
+      x = (x & ~mine) | (kScalesOfOne & mine);
+    }
+  }
   // Into [32-token half][k step][lane].
   __device__ __forceinline__ void decode_keys(const Raw& w, uint4* dst) const {
 #pragma unroll
@@ -416,14 +429,11 @@ struct Decoder {
     for (int i = 0; i < 8; ++i)
       sc[i] = scale_of_byte(w.x[8 + (D == 64 ? 4 * (i >> 2) + ((i & 3) >> 1) : i)],
                             D == 64 && (i & 1) ? turn + 16 : turn);
-    // What lies past the keys, or before the block's oldest window, is given scale 1: finite, and its
-    // weight is 0.
-    if (t0 + kTok > hi || t0 < low) {
+    // What lies past the keys is given scale 1: finite, and its weight is 0.
+    if (t0 + kTok > hi) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int32_t t = t0 + sub * 16 + (i >> 2) * 8 + vh * 4 + (i & 3);
-        if (t >= hi || t < low) sc[i] = 1.f;
-      }
+      for (int i = 0; i < 8; ++i)
+        if (t0 + sub * 16 + (i >> 2) * 8 + vh * 4 + (i & 3) >= hi) sc[i] = 1.f;
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -454,6 +464,11 @@ __device__ __forceinline__ void scores(v16f& s, const uint4* keys, const bf16x8 
     s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
         __builtin_bit_cast(bf16x8, keys[j * 64 + (threadIdx.x & 63)]), qf[j], j == 0 ? v16f(0.f) : s, 0, 0, 0);
 }
+
+// Orders what follows in a block of code: N reads from LDS, or N matrix products.
+constexpr int kLdsReads = 0x100, kProducts = 0x8;
+template <int KIND, int N>
+__device__ __forceinline__ void then() { __builtin_amdgcn_sched_group_barrier(KIND, N, 0); }
 
 // Masks the lane's 16 scores of the 32 tokens from t0.
 __device__ __forceinline__ void mask(v16f& s, const Row& r, int32_t t0) {
@@ -743,7 +758,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
         next_k = dec.place(w.t_begin + 3 * kTok);
       }
       if (values) {
-        dec.load_values(rv, dec.place(w.t_begin));
+        dec.load_first_values(rv, w);
         dec.decode_values(rv, w.t_begin, vl[0]);
         dec.load_values(rv, dec.place(w.t_begin + kTok));
         next_v = dec.place(w.t_begin + 2 * kTok);
@@ -814,6 +829,15 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
     auto score = [&](v16f& s, int32_t i) {
       const int32_t t0 = w.t_begin + i * kTok;
       scores(s, kl + half * KS * 64, qf, 0, KS);
+      // Each operand is read a product ahead.  Left to the compiler that depends on the registers it has
+      // over: where it reads into the same ones every time, a chunk takes 510 to 525 us for 495.
+      then<kLdsReads, 2>();
+#pragma unroll
+      for (int j = 0; j < KS - 2; ++j) {
+        then<kProducts, 1>();
+        then<kLdsReads, 1>();
+      }
+      then<kProducts, 2>();
       if (t0 + kTok > w.full_hi || t0 < w.full_lo) mask(s, row, t0 + half * 32);
       float top = s[0];
 #pragma unroll
@@ -874,7 +898,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
         dec.decode_keys(raw, kl);
         dec.load_keys(raw, dec.place(w.t_begin + kTok));
       } else {
-        dec.load_values(raw, dec.place(w.t_begin));
+        dec.load_first_values(raw, w);
         next = dec.place(w.t_begin + kTok);
       }
       lds_barrier();
@@ -905,7 +929,8 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
     lds_barrier();
     l += tops[0][rt][half ^ 1][c];
 
-    finish<DT, kThreads>(p, w, row, slot, acc, m, l, half * N);
+    // The row's numbers are worked out again: kept through the loop, they cost it registers.
+    finish<DT, kThreads>(p, w, row_of(p, w, rt, again(threadIdx.x)), slot, acc, m, l, half * N);
     if constexpr (!DEALT) return;
     lds_barrier();                           // before the next one's keys and values
   }
