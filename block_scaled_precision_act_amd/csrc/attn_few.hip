@@ -262,10 +262,12 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
 
     v4f acc[MT][EPL];
     float m[MT], l[MT];       // row c's running maximum (base 2) and the lane's share of the sum
+    float slack[MT];          // what a row's maximum may rise by before it is moved
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       m[mt] = -kInf;
       l[mt] = 0.f;
+      slack[mt] = kSlack;
 #pragma unroll
       for (int e = 0; e < EPL; ++e) acc[mt][e] = v4f{0.f, 0.f, 0.f, 0.f};
     }
@@ -380,9 +382,8 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
 #pragma unroll
         for (int i = 1; i < 8; ++i) top = fmaxf(top, s[mt][i >> 2][i & 3]);
         top = max_halves(max_rows(top)) * p.scale_log2;
-        // The maximum that is subtracted moves only when some row's rose by more than 2^8: until
-        // then weights stay below 2^8, and bf16 and fp32 hold them as well as those below one.
-        if (__any(top > m[mt] + 8.f)) {
+        float scale = p.scale_log2;
+        if (__any(top > m[mt] + slack[mt])) {
           const float now = fmaxf(m[mt], top);
           const float f = weight_of(m[mt], now);
           m[mt] = now;
@@ -391,12 +392,20 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
           for (int e = 0; e < EPL; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[mt][e][i] *= f;
+          slack[mt] = kSlack;
+          if (large_scores(now)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              s[mt][i >> 2][i & 3] = rounded_product(s[mt][i >> 2][i & 3], scale);
+            scale = 1.f;
+            slack[mt] = -kInf;
+          }
         }
         const float sub = m[mt] == -kInf ? 0.f : m[mt];
         float w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][i >> 2][i & 3], p.scale_log2, -sub));
+          w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][i >> 2][i & 3], scale, -sub));
           l[mt] += w[i];
         }
         pf[mt] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]),

@@ -685,6 +685,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
 
     v16f acc[DT];
     float m = -kInf, l = 0.f;
+    float slack = kSlack;                    // what a row's maximum may rise by before it is moved
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = v16f(0.f);
     // A wavefront that decodes one of the two holds one share.
@@ -709,9 +710,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
 #pragma unroll
       for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
       top = max_halves(top) * p.scale_log2;
-      // The maximum that is subtracted moves only when some row's rose by more than 2^8 (weights below
-      // that are held as exactly as those below one).  Moved at every rise: 551 us for 521 (8192 tokens).
-      if (__any(top > m + 8.f)) {
+      float scale = p.scale_log2;
+      if (__any(top > m + slack)) {
         const float now = fmaxf(m, top);
         const float f = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
         m = now;
@@ -720,11 +720,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
         for (int d = 0; d < DT; ++d)
 #pragma unroll
           for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+        slack = kSlack;
+        if (large_scores(now)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[e >> 4][e & 15] = rounded_product(s[e >> 4][e & 15], scale);
+          scale = 1.f;
+          slack = -kInf;
+        }
       }
       const float sub = m == -kInf ? 0.f : m;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {            // 16 tokens each
-        const bf16x8 pf = weights(s[q >> 1], 8 * (q & 1), p.scale_log2, sub, l);
+        const bf16x8 pf = weights(s[q >> 1], 8 * (q & 1), scale, sub, l);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
           acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
@@ -838,19 +845,22 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
         then<kLdsReads, 1>();
       }
       then<kProducts, 2>();
+      // Multiplied at once, which large scores need (see kLargeScore): a chunk takes 488 us, 484 without;
+      // 508 with a branch for them, as in attn_many_kernel, and this loop's registers.
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = rounded_product(s[e], p.scale_log2);
       if (t0 + kTok > w.full_hi || t0 < w.full_lo) mask(s, row, t0 + half * 32);
       float top = s[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
-      top = max_halves(top) * p.scale_log2;
+      top = max_halves(top);
       if (lane < 32) tops[i & 1][rt][half][c] = top;
     };
     auto step = [&](v16f& s, v16f& sn, auto final, int32_t i) {
       constexpr bool LAST = decltype(final)::value;
       const int32_t t0 = w.t_begin + i * kTok;
       const float top = fmaxf(tops[i & 1][rt][0][c], tops[i & 1][rt][1][c]);
-      // As in attn_many_kernel; both halves see the same maxima and move together.
-      if (__any(top > m + 8.f)) {
+      if (__any(top > m + kSlack)) {            // both halves see the same maxima and move together
         const float now = fmaxf(m, top);
         const float f = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
         m = now;
@@ -863,7 +873,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
       const float sub = m == -kInf ? 0.f : m;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        pl[rt][(half * 2 + u) * 64 + lane] = __builtin_bit_cast(uint4, weights(s, 8 * u, p.scale_log2, sub, l));
+        pl[rt][(half * 2 + u) * 64 + lane] = __builtin_bit_cast(uint4, weights(s, 8 * u, 1.f, sub, l));
       if (half == 1) {
         dec.decode_values(raw, t0, vl);
         if constexpr (!LAST) {

@@ -6,6 +6,7 @@ import torch
 
 from attention_util import Paged, attention_close, f64, oracle
 from gpu_util import note
+from oracle.attention_oracle import cache_rows
 from test_gpu_attn_fp4 import queries, run, uniform
 
 pytestmark = pytest.mark.gpu
@@ -73,3 +74,49 @@ def test_the_widest_windows_hide_nothing(mx, D, nq, group):
     for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - nq):
         out, lse = run(mx, paged, q, window=window)
         assert torch.equal(out, want) and torch.equal(lse, want_lse), window
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("sign", ["both", "negative"])
+def test_the_largest_score_wins_however_large(mx, D, nq, sign):
+    """Scores so large, and so far apart, that a row's output is the value of its largest score alone.
+
+    A score's fp32 sum and its product with the scale are off by at most d = 2^-20 scale sum |q k| each
+    (the rounded product by 2^-24 of it): a row whose largest score is more than 4 d + 200 above the
+    next has one weight, all others being below 2^-200 of it (0 in fp32).  Its output is that value:
+    the same bits from maxima of 2^28 (in base 2) on, where the weight is 1; below, the weight is 2 to
+    the power of the maximum's rounding error and rounded to bf16 once, and attention_close's bound
+    holds: 2^-8 for that and 2^-8 for the result's rounding.  Its log-sum-exp is the score."""
+    rng = np.random.default_rng(D + nq)
+    lens = [600, 1500, 129]
+    paged = Paged(rng, lens, 1, D, 16, lo=124, hi=130, junk=0x7F)
+    if sign == "negative":
+        paged.k &= 0x77                                       # keys above 0, queries below
+    q = queries(rng, nq * len(lens), 4, D)
+    if sign == "negative":
+        q = -q.abs()
+    for e in (20, 27, 28, 29, 31, 33, 60, 95):
+        scale = 2.0 ** e / D
+        note(f"attn scores of 2^{e} D={D} nq={nq} sign={sign}")
+        out, lse = run(mx, paged, q, scale=scale)
+        got, got_lse, rows = f64(out), f64(lse), 0
+        for b, n in enumerate(lens):
+            k = cache_rows(paged.k, paged.ks, paged.table[b], n)[0]
+            v = cache_rows(paged.v, paged.vs, paged.table[b], n)[0]
+            for i in range(nq):
+                seen = n - nq + i + 1
+                for h in range(4):
+                    x = f64(q[b * nq + i, h])
+                    s = scale * (k[:seen] @ x)
+                    d = 2.0 ** -20 * scale * (np.abs(k[:seen]) @ np.abs(x)).max()
+                    first, second = np.sort(s)[::-1][:2]
+                    if first - second <= 4 * d + 200:
+                        continue
+                    rows += 1
+                    where = (e, b, i, h)
+                    value = v[s.argmax()]
+                    tol = 0 if abs(first) * np.log2(np.e) >= 2.0 ** 28 * (1 + 2.0 ** -18) else 2.0 ** -7 * np.abs(value)
+                    assert (np.abs(got[b * nq + i, h] - value) <= tol).all(), where
+                    assert abs(got_lse[b * nq + i, h] - first) <= 2 * d, where
+        assert rows > nq * len(lens) * 2                      # of 4 heads
