@@ -174,7 +174,7 @@ int mx_qk_norm_rope_backward(const mx_qk_norm_rope_backward_args* a, void* strea
   if ((a->dq_weight && !a->q_weight) || (a->dk_weight && !a->k_weight)) return MX_ERR_NULL;
   const bool none = a->tokens == 0 || a->q_heads + k_heads == 0;
   if (none && !a->dq_weight && !a->dk_weight) return MX_OK;
-  // Without rows a weight's gradient is zero, and is written as such by the kernel.
+  // Without rows a weight's gradient is zero, and is written as such by the kernel; no workspace needed.
   if (a->tokens > 0 && a->q_heads > 0)
     st = first_error({rows_status(a->q, a->q_token_stride, a->q_head_stride, 4, false),
                       rows_status(a->dq_out, a->dq_out_token_stride, a->dq_out_head_stride, 4,
@@ -191,7 +191,8 @@ int mx_qk_norm_rope_backward(const mx_qk_norm_rope_backward_args* a, void* strea
   if (!aligned(a->q_weight, 8) || !aligned(a->k_weight, 8) || !aligned(a->dq_weight, 4) ||
       !aligned(a->dk_weight, 4))
     return MX_ERR_ALIGN;
-  if ((a->dq_weight || a->dk_weight) &&
+  const bool sums = a->tokens > 0 && ((a->dq_weight && a->q_heads > 0) || (a->dk_weight && k_heads > 0));
+  if (sums &&
       (!a->workspace || a->workspace_bytes < norm_back_workspace(a->head_dim) ||
        !aligned(a->workspace, 256)))
     return MX_ERR_WORKSPACE;

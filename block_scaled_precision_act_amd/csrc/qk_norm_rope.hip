@@ -242,6 +242,10 @@ __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRope
     }
   }
   if (!p.dweight[i]) return;
+  if (all == 0) {                            // no rows: a workgroup of its own, and no workspace
+    if (threadIdx.x < D) p.dweight[i][threadIdx.x] = 0.f;
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) sums[rg * D + (e < 4 ? lc.c0 + e : lc.c1 + e - 4)] = acc[e];
   __syncthreads();

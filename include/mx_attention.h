@@ -7,7 +7,7 @@
  *   - every buffer is device memory owned by the caller; nothing is allocated, freed or
  *     synchronized; work is enqueued on `stream` (a hipStream_t; NULL = the null stream);
  *   - argument errors are returned before any HIP call; calls with no tokens return MX_OK and
- *     enqueue nothing;
+ *     enqueue nothing (except mx_qk_norm_rope_backward's weight gradients, which are zero then);
  *   - strides are counted in elements of each buffer (bf16 elements for bf16 buffers, bytes for
  *     code and scale buffers).
  *
@@ -86,7 +86,8 @@ int mx_qk_norm_rope(const mx_qk_norm_rope_args* args, void* stream);
  * to), and may be NULL when not wanted (always when there is no weight).  The sums are taken in
  * one fixed order: the same call gives the same bits.
  * workspace: mx_qk_norm_rope_backward_workspace_size bytes, 256-byte aligned, zero before its
- * first use and left reusable by every call; needed only where a weight gradient is written.
+ * first use and left reusable by every call; needed only where a weight gradient is summed, so not
+ * without tokens (the size is 0 then).
  * Calls that may overlap need workspaces of their own.  Not to be shared with mx_attn_fp4: this call
  * leaves partial results where that one expects zeros.
  */
