@@ -131,8 +131,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvAppendProbl
   if (slot < 0 || slot >= static_cast<int64_t>(p.cache.pages) * p.cache.page_size) return;
   const uint32_t page = static_cast<uint32_t>(slot) / p.cache.page_size;
   const uint32_t off = static_cast<uint32_t>(slot) - page * p.cache.page_size;
-  const int64_t code0 = page * p.cache.code_page + off * (D / 2) + 4 * j;
-  const int64_t scale0 = page * p.cache.scale_page + off * (D / 32) + j / 4;
+  const int64_t code0 = page * p.cache.code_page + static_cast<int64_t>(off) * (D / 2) + 4 * j;
+  const int64_t scale0 = page * p.cache.scale_page + static_cast<int64_t>(off) * (D / 32) + j / 4;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t h = h0 + u;

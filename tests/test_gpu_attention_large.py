@@ -68,3 +68,24 @@ def test_attention_of_more_blocks_than_a_grid_holds(mx):
     note("attn of 8.8 million blocks")
     out, lse = run(mx, paged, q, starts=starts, max_q=max_q)
     attention_close(out, lse, oracle(paged, q, starts, D ** -0.5))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_into_a_page_of_more_than_4_gib(mx, D):
+    # one page of one head, whose codes pass 2^32 bytes
+    page = (1 << 33) // D + 160
+    rng = np.random.default_rng(D)
+    k, v = (bf16(rng.standard_normal((5, 1, D))).cuda() for _ in "kv")
+    cache = [torch.zeros((1, 1, page, D // n), dtype=torch.uint8, device="cuda") for n in (2, 32, 2, 32)]
+    at = (1 << 33) // D                                        # its codes begin at byte 2^32
+    slots = np.array([at + 5, 7, page - 1, at - 1, at], np.int64)
+    note(f"append into a page of {page} tokens, D={D}")
+    mx.mx_kv_append_fp4(mx.MxKvCacheFp4(*cache), k, v, torch.from_numpy(slots).cuda())
+    torch.cuda.synchronize()
+    kc, kb, _ = A.quantize_fp4(f64(k).astype(np.float32))
+    vc, vb, _ = A.quantize_fp4(f64(v).astype(np.float32))
+    for got, new in zip(cache, (kc, kb, vc, vb)):
+        for i, s in enumerate(slots):
+            assert np.array_equal(got[0, 0, s].cpu().numpy(), new[i, 0]), s
+        got[0, 0, torch.from_numpy(slots).cuda()] = 0          # nothing else is written
+        assert not any(bool(part.any()) for part in got.view(-1).split(1 << 30))
