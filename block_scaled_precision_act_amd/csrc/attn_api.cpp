@@ -41,24 +41,35 @@ mx::Rotation rotation(const int32_t* positions, const float* cos, const float* s
 }
 
 // Rows of `unit` elements' alignment: base and strides.
-int rows_status(const void* p, int64_t token_stride, int64_t head_stride, int64_t unit,
-                bool output) {
+int rows_status(const void* p, int64_t token_stride, int64_t head_stride, int64_t unit) {
   if (token_stride < 0 || head_stride < 0) return MX_ERR_STRIDE;
   if (!p) return MX_ERR_NULL;
   if (!aligned(p, 2 * unit) || token_stride % unit != 0 || head_stride % unit != 0)
     return MX_ERR_ALIGN;
-  (void)output;
   return MX_OK;
+}
+
+// Whether blocks of `size` at i a + j b, i < n and j < m, lie on each other.
+bool blocks_meet(int64_t n, int64_t a, int64_t m, int64_t b, int64_t size) {
+  if ((n > 1 && a < size) || (m > 1 && b < size)) return true;
+  if (n <= 1 || m <= 1) return false;
+  // The usual layouts: all of one index within a step of the other.
+  if (a <= (b - size) / (n - 1) || b <= (a - size) / (m - 1)) return false;
+  if (n > m) return blocks_meet(m, b, n, a, size);
+  for (int64_t i = 1; i < n; ++i) {          // the j's whose steps end around those of i
+    const __int128 at = static_cast<__int128>(i) * a, j = at / b;
+    if (j >= 1 && j < m && at - j * b < size) return true;
+    if (j + 1 < m && (j + 1) * b - at < size) return true;
+  }
+  return false;
 }
 
 // An output's rows must not lie on each other.
 int output_status(const void* p, int64_t token_stride, int64_t head_stride, int64_t tokens,
                   int64_t heads, int64_t head_dim, int64_t unit) {
-  const int st = rows_status(p, token_stride, head_stride, unit, true);
+  const int st = rows_status(p, token_stride, head_stride, unit);
   if (st != MX_OK) return st;
-  if ((tokens > 1 && token_stride < head_dim) || (heads > 1 && head_stride < head_dim))
-    return MX_ERR_STRIDE;
-  return MX_OK;
+  return blocks_meet(tokens, token_stride, heads, head_stride, head_dim) ? MX_ERR_STRIDE : MX_OK;
 }
 
 mx::HeadRows rows(const void* p, int64_t token_stride, int64_t head_stride) {
@@ -130,11 +141,11 @@ int mx_qk_norm_rope(const mx_qk_norm_rope_args* a, void* stream) {
     return st;
   if (a->tokens == 0 || a->q_heads + k_heads == 0) return MX_OK;
   if (a->q_heads > 0)
-    st = first_error({rows_status(a->q, a->q_token_stride, a->q_head_stride, 4, false),
+    st = first_error({rows_status(a->q, a->q_token_stride, a->q_head_stride, 4),
                       output_status(a->q_out, a->q_out_token_stride, a->q_out_head_stride,
                                     a->tokens, a->q_heads, a->head_dim, 4)});
   if (st == MX_OK && k_heads > 0)
-    st = first_error({rows_status(a->k, a->k_token_stride, a->k_head_stride, 4, false),
+    st = first_error({rows_status(a->k, a->k_token_stride, a->k_head_stride, 4),
                       output_status(a->k_out, a->k_out_token_stride, a->k_out_head_stride,
                                     a->tokens, k_heads, a->head_dim, 4)});
   if (st != MX_OK) return st;
@@ -176,15 +187,13 @@ int mx_qk_norm_rope_backward(const mx_qk_norm_rope_backward_args* a, void* strea
   if (none && !a->dq_weight && !a->dk_weight) return MX_OK;
   // Without rows a weight's gradient is zero, and is written as such by the kernel; no workspace needed.
   if (a->tokens > 0 && a->q_heads > 0)
-    st = first_error({rows_status(a->q, a->q_token_stride, a->q_head_stride, 4, false),
-                      rows_status(a->dq_out, a->dq_out_token_stride, a->dq_out_head_stride, 4,
-                                  false),
+    st = first_error({rows_status(a->q, a->q_token_stride, a->q_head_stride, 4),
+                      rows_status(a->dq_out, a->dq_out_token_stride, a->dq_out_head_stride, 4),
                       output_status(a->dq, a->dq_token_stride, a->dq_head_stride, a->tokens,
                                     a->q_heads, a->head_dim, 4)});
   if (st == MX_OK && a->tokens > 0 && k_heads > 0)
-    st = first_error({rows_status(a->k, a->k_token_stride, a->k_head_stride, 4, false),
-                      rows_status(a->dk_out, a->dk_out_token_stride, a->dk_out_head_stride, 4,
-                                  false),
+    st = first_error({rows_status(a->k, a->k_token_stride, a->k_head_stride, 4),
+                      rows_status(a->dk_out, a->dk_out_token_stride, a->dk_out_head_stride, 4),
                       output_status(a->dk, a->dk_token_stride, a->dk_head_stride, a->tokens,
                                     k_heads, a->head_dim, 4)});
   if (st != MX_OK) return st;
@@ -231,8 +240,8 @@ int mx_kv_append_fp4(const mx_kv_append_fp4_args* a, void* stream) {
     return st;
   if (a->tokens == 0) return MX_OK;
   if (!a->slots) return MX_ERR_NULL;
-  if ((st = first_error({rows_status(a->k, a->k_token_stride, a->k_head_stride, 8, false),
-                         rows_status(a->v, a->v_token_stride, a->v_head_stride, 8, false)})) !=
+  if ((st = first_error({rows_status(a->k, a->k_token_stride, a->k_head_stride, 8),
+                         rows_status(a->v, a->v_token_stride, a->v_head_stride, 8)})) !=
       MX_OK)
     return st;
   if (!aligned(a->k_out, 16) || !aligned(a->v_out, 16) || !aligned(a->slots, 8))
@@ -283,7 +292,7 @@ int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
     return MX_ERR_STRIDE;
   if (a->batch == 0 || a->total_q == 0 || a->max_q == 0) return MX_OK;
   if (!a->seq_lens || (a->table_width > 0 && !a->page_table)) return MX_ERR_NULL;
-  if ((st = first_error({rows_status(a->q, a->q_token_stride, a->q_head_stride, 8, false),
+  if ((st = first_error({rows_status(a->q, a->q_token_stride, a->q_head_stride, 8),
                          output_status(a->out, a->out_token_stride, a->out_head_stride, a->total_q,
                                        a->q_heads, c.head_dim, 8)})) != MX_OK)
     return st;

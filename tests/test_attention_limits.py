@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import block_scaled_precision_act_amd as mx
-from test_attention_abi import A, ATTN, _cache_address, _pack, lib  # noqa: F401 (lib: a fixture)
+from test_attention_abi import A, ATTN, NORM, _cache_address, _pack, lib  # noqa: F401 (lib: a fixture)
 
 host_only = pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses must not reach a GPU")
 
@@ -38,3 +38,31 @@ def test_weight_gradients_without_rows_need_no_workspace(lib):  # noqa: F811
     rows = dict(dk_out=A, dk=A, **{f"{t}_{s}_stride": 256 for t in ("dk_out", "k", "dk") for s in ("token", "head")})
     assert status(tokens=5, q_heads=0, k_heads=1, **rows) == mx.MX_ERR_WORKSPACE
     assert status(tokens=5, q_heads=0, k_heads=1, dk_weight=0, **rows) == mx.MX_ERR_DEVICE
+
+
+def _meet(n, a, m, b, size):
+    at = sorted(i * a + j * b for i in range(n) for j in range(m))
+    return any(y - x < size for x, y in zip(at, at[1:]))
+
+
+@host_only
+def test_outputs_whose_rows_lie_on_each_other_are_refused(lib):  # noqa: F811
+    # every pair of strides of up to 9 rows, against all rows' places written out
+    D, keep = 64, []
+    cache = _cache_address(keep, kv_heads=1, head_dim=D)
+    seen = set()
+    for tokens, heads in ((2, 2), (3, 2), (2, 5), (4, 3), (3, 7)):
+        for a in range(D // 2, 9 * D + 1, D // 2):
+            for b in range(D // 2, 9 * D + 1, D // 2):
+                want = mx.MX_ERR_STRIDE if _meet(tokens, a, heads, b, D) else mx.MX_ERR_DEVICE
+                out = dict(q_out_token_stride=a, q_out_head_stride=b)
+                args = {**NORM, **out, "k": 0, "tokens": tokens, "q_heads": heads, "head_dim": D, "rot": D}
+                assert lib.mx_qk_norm_rope(_pack("mx_qk_norm_rope_args", args), None) == want, (tokens, heads, a, b)
+                args = {**ATTN, "cache": cache, "total_q": tokens, "batch": 1, "max_q": tokens, "q_heads": heads,
+                        "out_token_stride": a, "out_head_stride": b}
+                assert lib.mx_attn_fp4(_pack("mx_attn_fp4_args", args), None) == want, (tokens, heads, a, b)
+                seen.add((want, a < b, a >= D and b >= D))
+    assert len(seen) == 6                                  # each answer on either side, also where no stride is short
+    for huge in (1 << 62, (1 << 62) + 64):                 # products beyond 64 bits
+        args = {**NORM, "k": 0, "q_out_token_stride": huge, "q_out_head_stride": huge}
+        assert lib.mx_qk_norm_rope(_pack("mx_qk_norm_rope_args", args), None) == mx.MX_ERR_STRIDE
