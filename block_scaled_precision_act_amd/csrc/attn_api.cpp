@@ -239,6 +239,10 @@ int mx_kv_append_fp4(const mx_kv_append_fp4_args* a, void* stream) {
       MX_OK)
     return st;
   if (a->tokens == 0) return MX_OK;
+  // Written blocks must not lie on each other (attention may read any).
+  if (blocks_meet(c.pages, c.code_page_stride, c.kv_heads, c.code_head_stride, c.page_size * c.head_dim / 2) ||
+      blocks_meet(c.pages, c.scale_page_stride, c.kv_heads, c.scale_head_stride, c.page_size * c.head_dim / 32))
+    return MX_ERR_STRIDE;
   if (!a->slots) return MX_ERR_NULL;
   if ((st = first_error({rows_status(a->k, a->k_token_stride, a->k_head_stride, 8),
                          rows_status(a->v, a->v_token_stride, a->v_head_stride, 8)})) !=

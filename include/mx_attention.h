@@ -16,7 +16,8 @@
  * [head_dim / 32].  `page_size` tokens of one head form a block with its tokens contiguous:
  * codes [pages, kv_heads, page_size, head_dim / 2], scales [pages, kv_heads, page_size,
  * head_dim / 32], with any page and head strides (multiples of 16 bytes, the same for keys and
- * values).  Slot s of the cache is token s % page_size of page s / page_size.
+ * values).  Slot s of the cache is token s % page_size of page s / page_size.  Where tokens are
+ * appended, blocks must not lie on each other.
  * head_dim is 64, 128 or 256; page_size is a positive multiple of 16; pages * page_size < 2^31.
  *
  * Arguments travel in structs of 8-byte fields (pointers, int64_t, double): no padding, and a

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import block_scaled_precision_act_amd as mx
-from test_attention_abi import A, ATTN, NORM, _cache_address, _pack, lib  # noqa: F401 (lib: a fixture)
+from test_attention_abi import A, APPEND, ATTN, NORM, _cache_address, _pack, lib  # noqa: F401 (lib: a fixture)
 
 host_only = pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses must not reach a GPU")
 
@@ -66,3 +66,14 @@ def test_outputs_whose_rows_lie_on_each_other_are_refused(lib):  # noqa: F811
     for huge in (1 << 62, (1 << 62) + 64):                 # products beyond 64 bits
         args = {**NORM, "k": 0, "q_out_token_stride": huge, "q_out_head_stride": huge}
         assert lib.mx_qk_norm_rope(_pack("mx_qk_norm_rope_args", args), None) == mx.MX_ERR_STRIDE
+
+
+@host_only
+@pytest.mark.parametrize("kind,block", [("code", 16 * 64), ("scale", 16 * 4)])
+def test_caches_whose_blocks_lie_on_each_other_are_not_written(lib, kind, block):  # noqa: F811
+    for page, head, status in ((block, block, mx.MX_ERR_STRIDE), (2 * block, 4 * block, mx.MX_ERR_STRIDE),
+                               (2 * block, block, mx.MX_ERR_DEVICE), (block, 10 * block, mx.MX_ERR_DEVICE),
+                               (2 * block, 3 * block, mx.MX_ERR_DEVICE), (3 * block, 2 * block, mx.MX_ERR_DEVICE)):
+        keep = []
+        c = _cache_address(keep, **{f"{kind}_page_stride": page, f"{kind}_head_stride": head})
+        assert lib.mx_kv_append_fp4(_pack("mx_kv_append_fp4_args", {**APPEND, "cache": c}), None) == status, (page, head)
