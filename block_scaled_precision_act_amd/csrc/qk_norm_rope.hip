@@ -168,17 +168,37 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(const NormRopeProbl
   }
 }
 
+// Rows after which a lane's sums are folded into its totals in LDS, with what each addition rounds off
+// carried on: no chain of plain additions is longer, however many rows there are.  Calls of fewer rows a
+// lane (of 16384 x 40 heads of 128, 81) do without: folding costs them 3%.
+constexpr int kFoldRows = 256;
+
+// total[0 .. 4) += v, the carry of the total's rounding errors beside it.
+__device__ __forceinline__ void fold4(float4* total, float4* carry, const float* v) {
+  const float4 s = *total, c = *carry;
+  const float t[4] = {s.x, s.y, s.z, s.w}, k[4] = {c.x, c.y, c.z, c.w};
+  float nt[4], nk[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float y = v[e] - k[e];
+    nt[e] = t[e] + y;
+    const float off = (nt[e] - t[e]) - y;
+    nk[e] = fabsf(off) < kInf ? off : 0.f;   // an infinite total has no rounding error
+  }
+  *total = make_float4(nt[0], nt[1], nt[2], nt[3]);
+  *carry = make_float4(nk[0], nk[1], nk[2], nk[3]);
+}
+
 // Workgroups [0, groups_q) take the queries' rows, the rest the keys'; rows are dealt round robin,
-// RG at a time.  A lane sums its 8 weight gradients over its rows in fp32 (at most a few hundred
-// rows a chain), the workgroup's lanes are summed through LDS, and the last workgroup of a tensor
-// to arrive sums all its workgroups' partials in their order, so the result does not depend on
-// which one that is.
-template <int LR, bool INTER, int U>
+// RG at a time.  A lane sums its 8 weight gradients over its rows in fp32 (kFoldRows a chain), the
+// workgroup's lanes are summed through LDS, and the last workgroup of a tensor to arrive sums all its
+// workgroups' partials in their order, so the result does not depend on which one that is.
+template <int LR, bool INTER, int U, bool FOLD>
 __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRopeBackProblem p,
                                                                   uint32_t groups_q,
                                                                   uint32_t groups_k) {
   constexpr int D = 8 * LR, RG = kThreads / LR;
-  __shared__ float sums[RG * D];
+  __shared__ __align__(16) float sums[RG * D], carries[FOLD ? RG * D : 4];
   __shared__ uint32_t flag;
   const int i = blockIdx.x >= groups_q;
   const uint32_t group = blockIdx.x - (i ? groups_q : 0), groups = i ? groups_k : groups_q;
@@ -191,6 +211,20 @@ __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRope
   for (int e = 0; e < 8; ++e) w[e] = 1.f, acc[e] = 0.f;
   if (norm) load8(p.weight[i], lc, w);
   const HeadRows &gy = p.dy[i], &in = p.x[i], &gx = p.dx[i];
+  int unfolded = 0;                          // units since the last fold
+  auto fold = [&]() {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int at = rg * D + (c ? lc.c1 : lc.c0);
+      fold4(reinterpret_cast<float4*>(sums + at), reinterpret_cast<float4*>(carries + at), acc + 4 * c);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  };
+  if constexpr (FOLD) {
+    for (int e = threadIdx.x; e < RG * D; e += kThreads) sums[e] = carries[e] = 0.f;
+    __syncthreads();
+  }
   // Every owner walks the same number of units (the row sums need every lane); past the last one it
   // repeats it, writes nothing and adds nothing.
   for (uint32_t base = group * RG; base < all; base += groups * RG) {
@@ -240,14 +274,22 @@ __global__ __launch_bounds__(kThreads) void norm_rope_back_kernel(const NormRope
       }
       if (live) store8(gx.p + t * gx.token_stride + (h0 + u) * gx.head_stride, lc, dy);
     }
+    if (FOLD && ++unfolded == kFoldRows / U) {
+      fold();
+      unfolded = 0;
+    }
   }
   if (!p.dweight[i]) return;
   if (all == 0) {                            // no rows: a workgroup of its own, and no workspace
     if (threadIdx.x < D) p.dweight[i][threadIdx.x] = 0.f;
     return;
   }
+  if constexpr (FOLD) {
+    fold();
+  } else {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sums[rg * D + (e < 4 ? lc.c0 + e : lc.c1 + e - 4)] = acc[e];
+    for (int e = 0; e < 8; ++e) sums[rg * D + (e < 4 ? lc.c0 + e : lc.c1 + e - 4)] = acc[e];
+  }
   __syncthreads();
   float* const parts = p.parts + static_cast<int64_t>(blockIdx.x) * D;
   if (threadIdx.x < D) {
@@ -331,13 +373,19 @@ hipError_t launch_backward_u(const NormRopeBackProblem& p, hipStream_t stream) {
     if (groups[i] == 0 && (units > 0 || p.dweight[i])) groups[i] = 1;
   }
   if (groups[0] + groups[1] == 0) return hipSuccess;
+  bool fold = false;
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t units = static_cast<uint64_t>(p.tokens) * ((p.heads[i] + U - 1) / U);
+    if (p.dweight[i] && units * U > groups[i] * RG * kFoldRows) fold = true;
+  }
   const dim3 grid(groups[0] + groups[1]);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p, groups[0], groups[1]);
+  };
   if (p.rot.interleaved)
-    hipLaunchKernelGGL((norm_rope_back_kernel<LR, true, U>), grid, dim3(kThreads), 0, stream, p,
-                       groups[0], groups[1]);
+    fold ? go(norm_rope_back_kernel<LR, true, U, true>) : go(norm_rope_back_kernel<LR, true, U, false>);
   else
-    hipLaunchKernelGGL((norm_rope_back_kernel<LR, false, U>), grid, dim3(kThreads), 0, stream, p,
-                       groups[0], groups[1]);
+    fold ? go(norm_rope_back_kernel<LR, false, U, true>) : go(norm_rope_back_kernel<LR, false, U, false>);
   return hipGetLastError();
 }
 
