@@ -110,7 +110,9 @@ class MxKvCacheFp4:
     """A paged MXFP4 key/value cache over the caller's tensors: codes k, v uint8
     [pages, kv_heads, page_size, head_dim / 2] and E8M0 scales k_scale, v_scale uint8
     [pages, kv_heads, page_size, head_dim / 32], with any page and head strides that are multiples
-    of 16 bytes (the same for k and v, and for their scales)."""
+    of 16 bytes (the same for k and v, and for their scales).  page_size: a multiple of 16; appending
+    takes any, mx_attn_fp4 pages of fewer than 2^20 tokens and page tables with
+    width * (page_size / 16) ** 2 < 2 ** 32."""
 
     def __init__(self, k, k_scale, v, v_scale):
         fn, dev = "MxKvCacheFp4", _current_device()

@@ -19,6 +19,7 @@
  * values).  Slot s of the cache is token s % page_size of page s / page_size.  Where tokens are
  * appended, blocks must not lie on each other.
  * head_dim is 64, 128 or 256; page_size is a positive multiple of 16; pages * page_size < 2^31.
+ * Attention takes no page of 2^20 tokens or more (its limits on pages and tables are with it, below).
  *
  * Arguments travel in structs of 8-byte fields (pointers, int64_t, double): no padding, and a
  * caller in any language can pack them.
@@ -166,7 +167,10 @@ int mx_kv_append_fp4(const mx_kv_append_fp4_args* args, void* stream);
  * (pages that hold nothing else may be freed, and their table entries be anything).  Among the tokens
  * between, a query's mask hides keys of any bytes but only finite values: a value scale byte of 253
  * to 255, which mx_kv_append_fp4 never stores, can make queries NaN that do not see its token.
- * |scale| must be below 1e30.  table_width * page_size is at most 2^31 - 1024.
+ * |scale| must be below 1e30.
+ * Pages and tables that attention takes: table_width * page_size at most 2^31 - 1024, and
+ * table_width * (page_size / 16)^2 < 2^32.  The second allows pages of up to 2^20 - 16 tokens, in
+ * tables of 1 page then; pages of 65536 tokens in tables of 255; pages of 496 and less in any.
  * seq_lens, q_starts and page_table entries are read on the device: lengths are clamped to what
  * the table covers, and an entry outside [0, pages) reads page 0 instead of memory that is not
  * the cache's.
@@ -180,7 +184,9 @@ int mx_kv_append_fp4(const mx_kv_append_fp4_args* args, void* stream);
  * matrix instructions.
  * Rounding: products of bf16 queries and exactly decoded keys are summed in fp32; weights
  * exp(s - m) are rounded to bf16 for their product with the exactly decoded values, summed in
- * fp32; the softmax's maximum and sum stay in fp32.
+ * fp32; the softmax's maximum and sum stay in fp32.  The sum over the values is divided by that of
+ * the weights at the end, and a weight may reach 2^8: values times 2^8 times the number of tokens
+ * that share the weight have to stay within fp32's range.
  */
 typedef struct mx_attn_fp4_args {
   const mx_kv_cache_fp4* cache;

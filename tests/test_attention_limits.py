@@ -1,9 +1,11 @@
 """The attention operators' limits on the host, with no GPU: what lies on both sides of each."""
+import re
+
 import pytest
 import torch
 
 import block_scaled_precision_act_amd as mx
-from test_attention_abi import A, APPEND, ATTN, NORM, _cache_address, _pack, lib  # noqa: F401 (lib: a fixture)
+from test_attention_abi import A, APPEND, ATTN, HEADER, NORM, _cache_address, _pack, lib  # noqa: F401 (lib: a fixture)
 
 host_only = pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses must not reach a GPU")
 
@@ -77,3 +79,23 @@ def test_caches_whose_blocks_lie_on_each_other_are_not_written(lib, kind, block)
         keep = []
         c = _cache_address(keep, **{f"{kind}_page_stride": page, f"{kind}_head_stride": head})
         assert lib.mx_kv_append_fp4(_pack("mx_kv_append_fp4_args", {**APPEND, "cache": c}), None) == status, (page, head)
+
+
+def test_the_limits_of_pages_and_tables_are_documented():
+    text = " ".join(re.sub(r"^ \* ", "", HEADER, flags=re.M).split())
+    for said in ("table_width * page_size at most 2^31 - 1024", "table_width * (page_size / 16)^2 < 2^32",
+                 "Attention takes no page of 2^20 tokens or more"):
+        assert said in text
+    assert "width * (page_size / 16) ** 2 < 2 ** 32" in mx.MxKvCacheFp4.__doc__
+
+
+@host_only
+@pytest.mark.parametrize("page_size,most", [((1 << 20) - 16, 1), (1 << 16, 255), (1 << 14, 4095), (496, (2 ** 31 - 1024) // 496)])
+def test_the_widest_table_of_large_pages(lib, page_size, most):  # noqa: F811
+    keep = []
+    block = page_size * 64
+    cache = _cache_address(keep, page_size=page_size, code_head_stride=block, code_page_stride=2 * block,
+                           scale_head_stride=block // 16, scale_page_stride=block // 8)
+    for width, status in ((most, mx.MX_ERR_DEVICE), (most + 1, mx.MX_ERR_SHAPE)):
+        args = {**ATTN, "cache": cache, "batch": 1, "total_q": 1, "table_width": width, "table_stride": width}
+        assert lib.mx_attn_fp4(_pack("mx_attn_fp4_args", args), None) == status, width
