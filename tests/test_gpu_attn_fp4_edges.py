@@ -120,3 +120,65 @@ def test_the_largest_score_wins_however_large(mx, D, nq, sign):
                     assert (np.abs(got[b * nq + i, h] - value) <= tol).all(), where
                     assert abs(got_lse[b * nq + i, h] - first) <= 2 * d, where
         assert rows > nq * len(lens) * 2                      # of 4 heads
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,nq,group", [(65, 1, 4), (130, 2, 5), (300, 1, 16)])
+def test_more_than_64_sequences_cut_between_workgroups(mx, D, B, nq, group):
+    # the deal of more than 64 sequences, with units of up to 40 tiles where a run is a few
+    rng = np.random.default_rng(D + B)
+    lens = rng.integers(0, 1500, B).tolist()
+    lens[3], lens[B // 2], lens[B - 1] = 5000, 3333, 4001
+    news = [int(n) for n in rng.integers(0, nq + 1, B)]
+    news[3] = news[B - 1] = nq
+    starts = [0, *np.cumsum(news).tolist()]
+    paged = Paged(rng, lens, 1, D, 32)
+    q = queries(rng, starts[-1], group, D)
+    tiles = [(n // 128 + 2) for n, m in zip(lens, news) if m]
+    assert max(tiles) > 4 * (sum(tiles) // 256 + 1)                # one is cut whatever the number of workgroups
+    ws = torch.zeros(mx.mx_attn_fp4_workspace_size(B, nq, group, 1, D), dtype=torch.uint8, device="cuda")
+    note(f"attn {B} sequences cut D={D} nq={nq} group={group}")
+    how = dict(starts=starts, max_q=nq, ws=ws)
+    out, lse = run(mx, paged, q, **how)
+    attention_close(out, lse, oracle(paged, q, starts, D ** -0.5))
+    again, lse2 = run(mx, paged, q, **how)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,nq,hk,lens", [(1, 150, 2, [2500]), (4, 70, 33, [2600, 900, 0, 130])])
+def test_many_rows_on_other_streams_and_in_graphs(mx, D, B, nq, hk, lens):
+    # keys in parts, joined by a second launch: split, and dealt by lengths that change between replays
+    rng = np.random.default_rng(D + B)
+    news = [nq, 3, 0, nq // 2][:B]
+    starts = [0, *np.cumsum(news).tolist()]
+    paged = Paged(rng, lens, hk, D, 32)
+    cache = mx.MxKvCacheFp4(*paged.tensors())
+    q = queries(rng, starts[-1], 2 * hk, D)
+    want, _ = run(mx, paged, q, starts=starts, max_q=nq, lse=False)
+    table = torch.from_numpy(paged.table).cuda()
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ds = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(mx.mx_attn_fp4_workspace_size(B, nq, 2 * hk, hk, D), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    note(f"attn many rows on a side stream D={D} B={B}")
+    with torch.cuda.stream(side):
+        mx.mx_attn_fp4(cache, q, table, dl, out, ws, q_starts=ds, max_q=nq)
+    side.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    note("attn many rows captured")
+    with torch.cuda.graph(graph, stream=side):
+        mx.mx_attn_fp4(cache, q, table, dl, out, ws, q_starts=ds, max_q=nq)
+    for step, share in enumerate((1.0, 0.5, 0.9, 0.05, 1.0)):
+        dl.copy_(torch.tensor([int(n * share) for n in lens], dtype=torch.int32))
+        q.copy_(queries(rng, starts[-1], 2 * hk, D))
+        eager = torch.empty_like(q)
+        mx.mx_attn_fp4(cache, q, table, dl, eager, torch.zeros_like(ws), q_starts=ds, max_q=nq)
+        torch.cuda.synchronize()
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), step
