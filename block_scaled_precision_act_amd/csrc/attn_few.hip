@@ -408,6 +408,7 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
           w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][i >> 2][i & 3], scale, -sub));
           l[mt] += w[i];
         }
+        // In bf16, the product's type; summed unrounded (weights in attn_many.hip).
         pf[mt] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]),
                                                        pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])));
       }

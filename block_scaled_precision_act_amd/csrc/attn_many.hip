@@ -15,14 +15,14 @@
 // wavefronts share 32 rows, each scoring half of the tokens and summing half of the head's values;
 // their weights pass through LDS.
 //
-// Measured: a prompt of 8192 tokens, 32 heads of 128 on 8: 520 us, 1050 TFLOP/s (a large library
-// product: 1172), the matrix instructions busy 43% of the cycles; 512 and 386 queries of 16 heads of
-// 256 on 2 against 32768 and 27891 tokens: 495 us, 905 TFLOP/s.  Power does not bound them (2.35 GHz
-// sustained): for every matrix instruction a wavefront reads 1 KB from LDS, which takes about as long,
-// and decoding and softmax take as many cycles again; with the decoding left out the first takes 410 us
-// and the second two thirds, without those reads the first takes 355.  More rows a wavefront would need
-// fewer reads: 64 (four wavefronts, every register of the CU) leave one wavefront a SIMD and nothing to
-// cover its waits with, 595 us.
+// Measured: a prompt of 8192 tokens, 32 heads of 128 on 8: 517 to 527 us (by box), 1045 TFLOP/s (a large
+// library product reaches 1172, this library's own 8192^3 GEMM 1415), the matrix instructions busy 43% of
+// the cycles; 512 and 386 queries of 16 heads of 256 on 2 against 32768 and 27891 tokens: 488 to 496 us,
+// 910 TFLOP/s.  Power does not bound them (2.38 GHz after 200 calls): for every matrix instruction a
+// wavefront reads 1 KB from LDS, which takes about as long, and decoding and softmax take as many cycles
+// again; with the decoding left out the first takes 410 us and the second two thirds, without those reads
+// the first takes 355.  More rows a wavefront would need fewer reads: 64 (four wavefronts, every register
+// of the CU) leave one wavefront a SIMD and nothing to cover its waits with, 595 us.
 #include "attn_common.h"
 
 #include <algorithm>
@@ -93,7 +93,8 @@ __device__ __forceinline__ Work unit_of(const AttnProblem& p, int block_rows, in
 // they are last as long as the longest one's part, or as the average in rounds.  One sequence is not
 // dealt, nor are kDealUnits or more units a workgroup, which fill the chip evenly enough.  Dealt and not:
 // 4 sequences of 5000 to 32768 tokens, up to 500 queries, 32 heads of 128 on 4: 515 and 915 us; 4 of 1000
-// to 9000, up to 300, 16 of 256 on 2: 137 and 304 us; the two above with heads of 256: 495 and 545.
+// to 9000, up to 300, 16 of 256 on 2: 137 and 304 us; the two above with heads of 256: 495 and 545 (488
+// since that kernel orders its reads).
 // Looking at it costs about 5 us (4 x 300 queries of 200 to 300 tokens: 20 us, 25 when looked at), so the
 // host spares it where the table is short.
 //
@@ -481,7 +482,10 @@ __device__ __forceinline__ void mask(v16f& s, const Row& r, int32_t t0) {
   }
 }
 
-// The weights of 8 of the lane's scores as a B operand; their sum is added to l.
+// The weights of 8 of the lane's scores as a B operand; their sum is added to l.  bf16 is the matrix
+// instruction's type, the one that holds every decoded value exactly; the sum adds the weights unrounded,
+// as the log-sum-exp needs them.  (Outputs are off from 64 bits by 0.0017 of their size, their own
+// rounding; so they are with weights in fp32.)
 __device__ __forceinline__ bf16x8 weights(const v16f& s, int at, float scale, float sub, float& l) {
   float w[8];
 #pragma unroll
@@ -845,8 +849,8 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
         then<kLdsReads, 1>();
       }
       then<kProducts, 2>();
-      // Multiplied at once, which large scores need (see kLargeScore): a chunk takes 488 us, 484 without;
-      // 508 with a branch for them, as in attn_many_kernel, and this loop's registers.
+      // Multiplied at once, which large scores need (see kLargeScore): a chunk takes 488 us, 484 without.
+      // (A branch for them, as in attn_many_kernel, takes 5% of a chunk in this loop, by its registers.)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = rounded_product(s[e], p.scale_log2);
       if (t0 + kTok > w.full_hi || t0 < w.full_lo) mask(s, row, t0 + half * 32);
