@@ -1,5 +1,5 @@
 """The attention operators' calls of more workgroups than one dimension of a grid holds (2^32 threads),
-and caches of very large pages."""
+caches of very large pages, and the longest sequence."""
 import numpy as np
 import pytest
 import torch
@@ -89,3 +89,22 @@ def test_append_into_a_page_of_more_than_4_gib(mx, D):
             assert np.array_equal(got[0, 0, s].cpu().numpy(), new[i, 0]), s
         got[0, 0, torch.from_numpy(slots).cuda()] = 0          # nothing else is written
         assert not any(bool(part.any()) for part in got.view(-1).split(1 << 30))
+
+
+def test_attention_at_the_longest_length(mx):
+    """2^31 - 1024 tokens through a table of 2^27 - 64 entries, all of them one page of 16 tokens: the mean is
+    that page's, and the log-sum-exp larger by ln of the entries.
+
+    Each of 768 workgroups' four wavefronts walks about 21845 steps of 32 tokens.  A lane's sum of weights is a
+    chain of 8 additions a step, less than 2^18 in all: 2^-6 of it at most; the sums of values are chains of
+    less than 2^15 products of 32 tokens, 2^-8 with the weights' rounding and the result's 2^-8."""
+    D, page, width = 64, 16, (1 << 27) - 64
+    rng = np.random.default_rng(4)
+    paged = Paged(rng, [page], 1, D, page, spare=0, width_extra=0)
+    q = queries(rng, 1, 4, D)
+    o, l, mag, _ = oracle(paged, q, [0, 1], D ** -0.5)
+    paged.lens, paged.table = [page * width], np.zeros((1, width), np.int32)
+    note("attn of 2^31 - 1024 tokens")
+    out, lse = run(mx, paged, q)
+    assert (np.abs(f64(out) - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -6 + 2.0 ** -7) * mag).all()
+    assert (np.abs(f64(lse) - l - np.log(width)) <= 2.0 ** -6).all()
