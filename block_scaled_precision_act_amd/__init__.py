@@ -74,12 +74,15 @@ for _n in ("fp8_fp4", "fp8_fp8", "fp4_fp4"):
         _SIGS[f"mx_gemm_{_n}{_v}_strided_batched"] = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I,
                                                       _I, _I, _I, _I, _I, _I, _I, _P]
 # Attention operators (include/mx_attention.h): an argument struct and the stream.
-for _n in ("mx_qk_norm_rope", "mx_qk_norm_rope_backward", "mx_kv_append_fp4", "mx_attn_fp4"):
+# So do the draft operators (include/mx_draft.h).
+for _n in ("mx_qk_norm_rope", "mx_qk_norm_rope_backward", "mx_kv_append_fp4", "mx_attn_fp4",
+           "mx_tree_mask", "mx_attn_tree_fp4", "mx_tree_verify", "mx_kv_accept_fp4"):
     _SIGS[_n] = [ctypes.c_char_p, _P]
 _SIGS["mx_qk_norm_rope_backward_workspace_size"] = [_I, _I, _I, _I]
 _SIGS["mx_attn_fp4_workspace_size"] = [_I, _I, _I, _I, _I]
+_SIGS["mx_tree_verify_workspace_size"] = [_I]
 _INT64_RESULTS = ("mx_gemm_splitk_workspace_size", "mx_qk_norm_rope_backward_workspace_size",
-                  "mx_attn_fp4_workspace_size")
+                  "mx_attn_fp4_workspace_size", "mx_tree_verify_workspace_size")
 
 
 def load(path: str | None = None) -> ctypes.CDLL:
@@ -620,15 +623,20 @@ def mx_gemm_e5m2_e4m3_splitk(a, a_s, b, b_s, c, workspace, stream=None):
                                            K, _ptr(workspace), ws_bytes, _stream(stream)))
 
 
-# The attention operators (include/mx_attention.h) are in attention.py, imported when first used.
-_ATTENTION = ("MxKvCacheFp4", "mx_attn_fp4", "mx_attn_fp4_workspace_size", "mx_kv_append_fp4",
-              "mx_qk_norm_rope", "mx_qk_norm_rope_backward",
-              "mx_qk_norm_rope_backward_workspace_size")
+# The attention operators (include/mx_attention.h) are in attention.py, the draft operators
+# (include/mx_draft.h) in drafts.py, imported when first used.
+_LATER = {"attention": ("MxKvCacheFp4", "mx_attn_fp4", "mx_attn_fp4_workspace_size", "mx_kv_append_fp4",
+                        "mx_qk_norm_rope", "mx_qk_norm_rope_backward",
+                        "mx_qk_norm_rope_backward_workspace_size"),
+          "drafts": ("mx_attn_tree_fp4", "mx_kv_accept_fp4", "mx_tree_mask", "mx_tree_verify",
+                     "mx_tree_verify_workspace_size")}
 
 
 def __getattr__(name):
-    if name not in _ATTENTION:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import attention
-    globals().update({n: getattr(attention, n) for n in _ATTENTION})
-    return globals()[name]
+    for part, names in _LATER.items():
+        if name in names:
+            import importlib
+            m = importlib.import_module(f".{part}", __name__)
+            globals().update({n: getattr(m, n) for n in names})
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

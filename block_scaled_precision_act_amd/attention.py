@@ -106,6 +106,28 @@ def _workspace(fn: str, ws, dev: int):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _table(fn: str, page_table, dev: int):
+    """Pointer and row stride of a page table, sequences, pages of a sequence."""
+    _need(fn, page_table, "page_table", _i32, dev)
+    if page_table.dim() != 2:
+        raise MxError(fn, MX_ERR_SHAPE, f"page_table has shape {tuple(page_table.shape)}, expected "
+                                        "[batch, pages of a sequence]")
+    B, width = page_table.shape
+    if width > 1 and page_table.stride(1) != 1:
+        raise MxError(fn, MX_ERR_STRIDE, f"page_table's rows are not contiguous "
+                                         f"({page_table.stride()})")
+    return page_table.data_ptr(), page_table.stride(0) if B > 1 else width, B, width
+
+
+def _starts(fn: str, q_starts, max_q, rows: int, B: int, dev: int):
+    """Pointer of q_starts (None: rows / B each) and max_q."""
+    if q_starts is not None:
+        if max_q is None:
+            raise TypeError(f"{fn}: q_starts needs max_q")
+        return _flat(fn, q_starts, "q_starts", _i32, dev, (B + 1,)), max_q
+    return 0, (rows // B if B else 0) if max_q is None else max_q
+
+
 class MxKvCacheFp4:
     """A paged MXFP4 key/value cache over the caller's tensors: codes k, v uint8
     [pages, kv_heads, page_size, head_dim / 2] and E8M0 scales k_scale, v_scale uint8
@@ -148,9 +170,9 @@ class MxKvCacheFp4:
         self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, dim
         self.device_index = dev
-        self._struct = ctypes.create_string_buffer(
-            _CACHE.pack(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(), pages,
-                        heads, size, dim, *code, *scale), _CACHE.size)
+        self._packed = _CACHE.pack(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(),
+                                   pages, heads, size, dim, *code, *scale)
+        self._struct = ctypes.create_string_buffer(self._packed, _CACHE.size)
         self._addr = ctypes.addressof(self._struct)
 
 
@@ -274,33 +296,27 @@ def mx_attn_fp4(cache, q, page_table, seq_lens, out, workspace, q_starts=None, m
     sees, itself included (0: all).  lse: fp32 [total_q, q_heads] or None.  workspace: a tensor of
     mx_attn_fp4_workspace_size bytes, zero before its first use, reusable."""
     fn, dev = "mx_attn_fp4", _current_device()
+    (qp, op, lp, tp, lens, starts, wp, wb, strides, table, B, N, max_q, H, scale) = _attn(
+        fn, dev, cache, q, page_table, seq_lens, out, workspace, q_starts, max_q, scale, lse)
+    st = load().mx_attn_fp4(
+        _ATTN.pack(cache._addr, qp, op, lp, tp, lens, starts, wp, wb, *strides, *table, B, N, max_q, H,
+                   causal, window, scale), _stream(stream, dev))
+    if st != MX_OK:
+        raise MxError(fn, st)
+
+
+def _attn(fn, dev, cache, q, page_table, seq_lens, out, workspace, q_starts, max_q, scale, lse):
+    """What every attention call checks and passes: pointers, strides of q and out, of the table, sizes."""
     _cache(fn, cache, dev)
     qp, qt, qh = _heads(fn, q, "q", dev)
     N, H, D = q.shape
     if D != cache.head_dim:
         raise MxError(fn, MX_ERR_SHAPE, f"q has head_dim {D}, the cache {cache.head_dim}")
     op, ot, oh = _heads(fn, out, "out", dev, q.shape)
-    _need(fn, page_table, "page_table", _i32, dev)
-    if page_table.dim() != 2:
-        raise MxError(fn, MX_ERR_SHAPE, f"page_table has shape {tuple(page_table.shape)}, expected "
-                                        "[batch, pages of a sequence]")
-    B, width = page_table.shape
-    if width > 1 and page_table.stride(1) != 1:
-        raise MxError(fn, MX_ERR_STRIDE, f"page_table's rows are not contiguous "
-                                         f"({page_table.stride()})")
+    tp, stride, B, width = _table(fn, page_table, dev)
     lens = _flat(fn, seq_lens, "seq_lens", _i32, dev, (B,))
-    starts = 0
-    if q_starts is not None:
-        starts = _flat(fn, q_starts, "q_starts", _i32, dev, (B + 1,))
-        if max_q is None:
-            raise TypeError(f"{fn}: q_starts needs max_q")
-    elif max_q is None:
-        max_q = N // B if B else 0
+    starts, max_q = _starts(fn, q_starts, max_q, N, B, dev)
     lp = 0 if lse is None else _flat(fn, lse, "lse", _f32, dev, (N, H))
     wp, wb = _workspace(fn, workspace, dev)
-    st = load().mx_attn_fp4(
-        _ATTN.pack(cache._addr, qp, op, lp, page_table.data_ptr(), lens, starts, wp, wb, qt, qh,
-                   ot, oh, page_table.stride(0) if B > 1 else width, width, B, N, max_q, H, causal,
-                   window, D ** -0.5 if scale is None else scale), _stream(stream, dev))
-    if st != MX_OK:
-        raise MxError(fn, st)
+    return (qp, op, lp, tp, lens, starts, wp, wb, (qt, qh, ot, oh), (stride, width), B, N, max_q, H,
+            D ** -0.5 if scale is None else scale)

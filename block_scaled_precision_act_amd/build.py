@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libmx_gfx950.so")
 
 SOURCES = ["mx_api.cpp", "act_quant.hip", "quant_transpose.hip", "gemm_fp4.hip", "gemm_bf16.hip",
            "gemm_mx.hip", "gemm_small.hip", "gemm_scratch.hip", "attn_api.cpp", "qk_norm_rope.hip",
-           "kv_append.hip", "attn_few.hip", "attn_many.hip"]
+           "kv_append.hip", "attn_few.hip", "attn_many.hip", "draft_api.cpp", "tree_mask.hip",
+           "tree_verify.hip", "kv_accept.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

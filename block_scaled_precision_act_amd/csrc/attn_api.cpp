@@ -1,28 +1,15 @@
-// C ABI of the attention operators (declared in include/mx_attention.h): argument checks on the
-// host, then one launch on the caller's stream.
-#include "../../include/mx_attention.h"
-#include "attn_internal.h"
-#include "mx_internal.h"
+// C ABI of the attention operators (declared in include/mx_attention.h, and the attention of a tree of
+// drafted tokens in include/mx_draft.h): argument checks on the host, then one launch on the caller's
+// stream.
+#include "../../include/mx_draft.h"
+#include "attn_checks.h"
 
 #include <cfloat>
 #include <cmath>
 
 namespace {
 
-constexpr int64_t kMax31 = (int64_t{1} << 31) - 1;
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-bool head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256; }
-
-// a * b <= 2^31 - 1, both non-negative
-bool fits31(int64_t a, int64_t b) { return a == 0 || b <= kMax31 / a; }
-
-int device_status() {
-  mx::DeviceInfo dev;
-  if (!mx::current_device(&dev) || !dev.gfx950) return MX_ERR_DEVICE;
-  return MX_OK;
-}
+using namespace mx;
 
 int rotation_status(const int32_t* positions, const float* cos, const float* sin, int64_t rows,
                     int64_t rot, int64_t head_dim) {
@@ -40,72 +27,6 @@ mx::Rotation rotation(const int32_t* positions, const float* cos, const float* s
                       interleaved != 0};
 }
 
-// Rows of `unit` elements' alignment: base and strides.
-int rows_status(const void* p, int64_t token_stride, int64_t head_stride, int64_t unit) {
-  if (token_stride < 0 || head_stride < 0) return MX_ERR_STRIDE;
-  if (!p) return MX_ERR_NULL;
-  if (!aligned(p, 2 * unit) || token_stride % unit != 0 || head_stride % unit != 0)
-    return MX_ERR_ALIGN;
-  return MX_OK;
-}
-
-// Whether blocks of `size` at i a + j b, i < n and j < m, lie on each other.
-bool blocks_meet(int64_t n, int64_t a, int64_t m, int64_t b, int64_t size) {
-  if ((n > 1 && a < size) || (m > 1 && b < size)) return true;
-  if (n <= 1 || m <= 1) return false;
-  // The usual layouts: all of one index within a step of the other.
-  if (a <= (b - size) / (n - 1) || b <= (a - size) / (m - 1)) return false;
-  if (n > m) return blocks_meet(m, b, n, a, size);
-  for (int64_t i = 1; i < n; ++i) {          // the j's whose steps end around those of i
-    const __int128 at = static_cast<__int128>(i) * a, j = at / b;
-    if (j >= 1 && j < m && at - j * b < size) return true;
-    if (j + 1 < m && (j + 1) * b - at < size) return true;
-  }
-  return false;
-}
-
-// An output's rows must not lie on each other.
-int output_status(const void* p, int64_t token_stride, int64_t head_stride, int64_t tokens,
-                  int64_t heads, int64_t head_dim, int64_t unit) {
-  const int st = rows_status(p, token_stride, head_stride, unit);
-  if (st != MX_OK) return st;
-  return blocks_meet(tokens, token_stride, heads, head_stride, head_dim) ? MX_ERR_STRIDE : MX_OK;
-}
-
-mx::HeadRows rows(const void* p, int64_t token_stride, int64_t head_stride) {
-  return mx::HeadRows{static_cast<uint16_t*>(const_cast<void*>(p)), token_stride, head_stride};
-}
-
-int cache_status(const mx_kv_cache_fp4* c) {
-  if (!c) return MX_ERR_NULL;
-  if (!head_dim_ok(c->head_dim) || c->kv_heads <= 0 || c->kv_heads > 65535 || c->pages < 0 ||
-      c->page_size <= 0 || c->page_size % 16 != 0 || !fits31(c->page_size, c->pages))
-    return MX_ERR_SHAPE;
-  if (c->code_page_stride < 0 || c->code_head_stride < 0 || c->scale_page_stride < 0 ||
-      c->scale_head_stride < 0)
-    return MX_ERR_STRIDE;
-  const int64_t code_block = c->page_size * c->head_dim / 2;
-  const int64_t scale_block = c->page_size * c->head_dim / 32;
-  if ((c->pages > 1 && (c->code_page_stride < code_block || c->scale_page_stride < scale_block)) ||
-      (c->kv_heads > 1 && (c->code_head_stride < code_block || c->scale_head_stride < scale_block)))
-    return MX_ERR_STRIDE;
-  if (c->pages > 0 && (!c->k || !c->k_scale || !c->v || !c->v_scale)) return MX_ERR_NULL;
-  if (!aligned(c->k, 16) || !aligned(c->k_scale, 16) || !aligned(c->v, 16) ||
-      !aligned(c->v_scale, 16) || c->code_page_stride % 16 != 0 || c->code_head_stride % 16 != 0 ||
-      c->scale_page_stride % 16 != 0 || c->scale_head_stride % 16 != 0)
-    return MX_ERR_ALIGN;
-  return MX_OK;
-}
-
-mx::KvCache cache_of(const mx_kv_cache_fp4& c) {
-  return mx::KvCache{static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.k_scale),
-                     static_cast<uint8_t*>(c.v), static_cast<uint8_t*>(c.v_scale),
-                     c.code_page_stride, c.code_head_stride, c.scale_page_stride,
-                     c.scale_head_stride, static_cast<uint32_t>(c.pages),
-                     static_cast<uint32_t>(c.kv_heads), static_cast<uint32_t>(c.page_size),
-                     static_cast<int>(c.head_dim)};
-}
-
 // tokens and heads of the norm calls; k_heads counts only when there are keys.
 int norm_shape_status(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t head_dim,
                       double eps) {
@@ -115,16 +36,101 @@ int norm_shape_status(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t 
   return MX_OK;
 }
 
-int first_error(std::initializer_list<int> all) {
-  for (int s : all)
-    if (s != MX_OK) return s;
-  return MX_OK;
-}
-
-int status_of(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ERR_LAUNCH; }
-
 int64_t norm_back_workspace(int64_t head_dim) {
   return mx::kNormBackCounterBytes + mx::kNormBackGroups * head_dim * 4;
+}
+
+// A tree's mask (mx_draft.h), in place of a causal one.
+struct Tree {
+  const int32_t* mask;
+  const int32_t* positions;
+  int64_t stride, words;
+};
+constexpr int64_t kMostMaskedQueries = 65536;
+
+int tree_status(const Tree& t, int64_t max_q, int64_t window) {
+  if (max_q > kMostMaskedQueries || t.words < (max_q + 31) / 32 || t.words > kMax31) return MX_ERR_SHAPE;
+  if (t.stride < 0) return MX_ERR_STRIDE;
+  if (!t.mask || (window > 0 && !t.positions)) return MX_ERR_NULL;
+  return aligned(t.mask, 4) && aligned(t.positions, 4) ? MX_OK : MX_ERR_ALIGN;
+}
+
+int attend(const mx_attn_fp4_args& args, const Tree* tree, void* stream) {
+  const mx_attn_fp4_args* const a = &args;
+  int st = cache_status(a->cache);
+  if (st != MX_OK) return st;
+  const mx_kv_cache_fp4& c = *a->cache;
+  if (a->batch < 0 || a->batch > 65535 || a->total_q < 0 || a->max_q < 0 || a->q_heads <= 0 ||
+      a->q_heads % c.kv_heads != 0 || !fits31(a->total_q, a->q_heads) ||
+      !fits31(a->max_q, a->q_heads) || !fits31(a->batch, c.kv_heads) || a->table_width < 0 ||
+      a->window < 0 || a->window > kMax31 || (a->window > 0 && !a->causal && !tree) ||
+      !(std::fabs(a->scale) < 1e30))
+    return MX_ERR_SHAPE;
+  if (!a->q_starts && a->total_q != a->batch * a->max_q) return MX_ERR_SHAPE;
+  // Tokens a table row covers: the kernels count in 31 bits, and look up to kLookAhead tokens past a
+  // length.  And the exactness of the page number as a high product.
+  if (!fits31(a->table_width, c.page_size) || a->table_width * c.page_size > kMax31 + 1 - mx::kLookAhead)
+    return MX_ERR_SHAPE;
+  const int64_t d = c.page_size / 16;
+  if (a->table_width * d * d >= (int64_t{1} << 32)) return MX_ERR_SHAPE;
+  if (a->table_stride < 0 || (a->batch > 1 && a->table_stride < a->table_width))
+    return MX_ERR_STRIDE;
+  if (a->batch == 0 || a->total_q == 0 || a->max_q == 0) return MX_OK;
+  if (!a->seq_lens || (a->table_width > 0 && !a->page_table)) return MX_ERR_NULL;
+  if (tree && (st = tree_status(*tree, a->max_q, a->window)) != MX_OK) return st;
+  if ((st = first_error({rows_status(a->q, a->q_token_stride, a->q_head_stride, 8),
+                         output_status(a->out, a->out_token_stride, a->out_head_stride, a->total_q,
+                                       a->q_heads, c.head_dim, 8)})) != MX_OK)
+    return st;
+  mx::AttnPlan plan = mx::plan_attn(a->batch, a->max_q, a->q_heads, c.kv_heads,
+                                    static_cast<int>(c.head_dim));
+  // The deal of tiles of 128 tokens (plus a few slots for each sequence and head) counts in 31 bits.
+  const int64_t units = a->batch * c.kv_heads;
+  if (plan.few && (units > mx::kMaxUnits || !fits31(units, a->table_width * c.page_size / 128 + 8)))
+    return MX_ERR_SHAPE;
+  // So does that of tiles of 64 tokens; past it there is none.  Nor is there one where the table's tokens
+  // are too few for it to gain what looking costs (the longest part's tiles; looking takes about 5 us, a
+  // tile 2).
+  const int64_t tiles = a->table_width * c.page_size / 64;
+  if (!plan.few && plan.groups > 0 &&
+      (tiles / plan.splits <= mx::kLeastDealTiles || !fits31(units * plan.row_blocks, tiles + 8)))
+    plan.groups = 0;
+  if (plan.part_bytes > 0 && (!a->workspace || a->workspace_bytes < mx::kCounterBytes + plan.part_bytes ||
+                              !aligned(a->workspace, 256)))
+    return MX_ERR_WORKSPACE;
+  if ((st = device_status()) != MX_OK) return st;
+  mx::AttnProblem p;
+  p.cache = cache_of(c);
+  p.q = rows(a->q, a->q_token_stride, a->q_head_stride);
+  p.out = rows(a->out, a->out_token_stride, a->out_head_stride);
+  p.lse = a->lse;
+  p.table = a->page_table;
+  p.lens = a->seq_lens;
+  p.starts = a->q_starts;
+  p.table_stride = a->table_stride;
+  // An empty cache holds nothing that a length could speak of.
+  p.table_width = static_cast<int32_t>(c.pages > 0 ? a->table_width : 0);
+  p.page_div = static_cast<uint32_t>(((uint64_t{1} << 32) + d - 1) / d);   // d == 1: wraps to 0
+  p.batch = static_cast<int32_t>(a->batch);
+  p.total_q = static_cast<int32_t>(a->total_q);
+  p.max_q = static_cast<int32_t>(a->max_q);
+  p.group = static_cast<int32_t>(a->q_heads / c.kv_heads);
+  // A scale of zero becomes the smallest normal number: every finite score still counts as zero, and
+  // the -infinity of a masked one stays what it is.
+  p.scale_log2 = static_cast<float>(std::fabs(a->scale) * 1.4426950408889634);
+  if (p.scale_log2 < FLT_MIN) p.scale_log2 = FLT_MIN;
+  p.flip = a->scale < 0 ? 0x80008000u : 0u;
+  p.causal = a->causal != 0;
+  p.window = static_cast<int32_t>(a->window);
+  p.counters = static_cast<uint32_t*>(a->workspace);
+  p.counter_stride = mx::counter_stride(units);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + mx::kCounterBytes);
+  p.tree = tree ? reinterpret_cast<const uint32_t*>(tree->mask) : nullptr;
+  p.tree_at = tree ? tree->positions : nullptr;
+  p.tree_stride = tree ? tree->stride : 0;
+  p.tree_words = tree ? static_cast<int32_t>(tree->words) : 0;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return status_of(plan.few ? mx::launch_attn_few(p, plan, s) : mx::launch_attn_many(p, plan, s));
 }
 
 }  // namespace
@@ -275,76 +281,17 @@ int64_t mx_attn_fp4_workspace_size(int64_t batch, int64_t max_q, int64_t q_heads
 }
 
 int mx_attn_fp4(const mx_attn_fp4_args* a, void* stream) {
+  return a ? attend(*a, nullptr, stream) : MX_ERR_NULL;
+}
+
+int mx_attn_tree_fp4(const mx_attn_tree_fp4_args* a, void* stream) {
   if (!a) return MX_ERR_NULL;
-  int st = cache_status(a->cache);
-  if (st != MX_OK) return st;
-  const mx_kv_cache_fp4& c = *a->cache;
-  if (a->batch < 0 || a->batch > 65535 || a->total_q < 0 || a->max_q < 0 || a->q_heads <= 0 ||
-      a->q_heads % c.kv_heads != 0 || !fits31(a->total_q, a->q_heads) ||
-      !fits31(a->max_q, a->q_heads) || !fits31(a->batch, c.kv_heads) || a->table_width < 0 ||
-      a->window < 0 || a->window > kMax31 || (a->window > 0 && !a->causal) ||
-      !(std::fabs(a->scale) < 1e30))
-    return MX_ERR_SHAPE;
-  if (!a->q_starts && a->total_q != a->batch * a->max_q) return MX_ERR_SHAPE;
-  // Tokens a table row covers: the kernels count in 31 bits, and look up to kLookAhead tokens past a
-  // length.  And the exactness of the page number as a high product.
-  if (!fits31(a->table_width, c.page_size) || a->table_width * c.page_size > kMax31 + 1 - mx::kLookAhead)
-    return MX_ERR_SHAPE;
-  const int64_t d = c.page_size / 16;
-  if (a->table_width * d * d >= (int64_t{1} << 32)) return MX_ERR_SHAPE;
-  if (a->table_stride < 0 || (a->batch > 1 && a->table_stride < a->table_width))
-    return MX_ERR_STRIDE;
-  if (a->batch == 0 || a->total_q == 0 || a->max_q == 0) return MX_OK;
-  if (!a->seq_lens || (a->table_width > 0 && !a->page_table)) return MX_ERR_NULL;
-  if ((st = first_error({rows_status(a->q, a->q_token_stride, a->q_head_stride, 8),
-                         output_status(a->out, a->out_token_stride, a->out_head_stride, a->total_q,
-                                       a->q_heads, c.head_dim, 8)})) != MX_OK)
-    return st;
-  mx::AttnPlan plan = mx::plan_attn(a->batch, a->max_q, a->q_heads, c.kv_heads,
-                                    static_cast<int>(c.head_dim));
-  // The deal of tiles of 128 tokens (plus a few slots for each sequence and head) counts in 31 bits.
-  const int64_t units = a->batch * c.kv_heads;
-  if (plan.few && (units > mx::kMaxUnits || !fits31(units, a->table_width * c.page_size / 128 + 8)))
-    return MX_ERR_SHAPE;
-  // So does that of tiles of 64 tokens; past it there is none.  Nor is there one where the table's tokens
-  // are too few for it to gain what looking costs (the longest part's tiles; looking takes about 5 us, a
-  // tile 2).
-  const int64_t tiles = a->table_width * c.page_size / 64;
-  if (!plan.few && plan.groups > 0 &&
-      (tiles / plan.splits <= mx::kLeastDealTiles || !fits31(units * plan.row_blocks, tiles + 8)))
-    plan.groups = 0;
-  if (plan.part_bytes > 0 && (!a->workspace || a->workspace_bytes < mx::kCounterBytes + plan.part_bytes ||
-                              !aligned(a->workspace, 256)))
-    return MX_ERR_WORKSPACE;
-  if ((st = device_status()) != MX_OK) return st;
-  mx::AttnProblem p;
-  p.cache = cache_of(c);
-  p.q = rows(a->q, a->q_token_stride, a->q_head_stride);
-  p.out = rows(a->out, a->out_token_stride, a->out_head_stride);
-  p.lse = a->lse;
-  p.table = a->page_table;
-  p.lens = a->seq_lens;
-  p.starts = a->q_starts;
-  p.table_stride = a->table_stride;
-  // An empty cache holds nothing that a length could speak of.
-  p.table_width = static_cast<int32_t>(c.pages > 0 ? a->table_width : 0);
-  p.page_div = static_cast<uint32_t>(((uint64_t{1} << 32) + d - 1) / d);   // d == 1: wraps to 0
-  p.batch = static_cast<int32_t>(a->batch);
-  p.total_q = static_cast<int32_t>(a->total_q);
-  p.max_q = static_cast<int32_t>(a->max_q);
-  p.group = static_cast<int32_t>(a->q_heads / c.kv_heads);
-  // A scale of zero becomes the smallest normal number: every finite score still counts as zero, and
-  // the -infinity of a masked one stays what it is.
-  p.scale_log2 = static_cast<float>(std::fabs(a->scale) * 1.4426950408889634);
-  if (p.scale_log2 < FLT_MIN) p.scale_log2 = FLT_MIN;
-  p.flip = a->scale < 0 ? 0x80008000u : 0u;
-  p.causal = a->causal != 0;
-  p.window = static_cast<int32_t>(a->window);
-  p.counters = static_cast<uint32_t*>(a->workspace);
-  p.counter_stride = mx::counter_stride(units);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + mx::kCounterBytes);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  return status_of(plan.few ? mx::launch_attn_few(p, plan, s) : mx::launch_attn_many(p, plan, s));
+  const mx_attn_fp4_args call = {
+      a->cache, a->q, a->out, a->lse, a->page_table, a->seq_lens, a->q_starts, a->workspace,
+      a->workspace_bytes, a->q_token_stride, a->q_head_stride, a->out_token_stride, a->out_head_stride,
+      a->table_stride, a->table_width, a->batch, a->total_q, a->max_q, a->q_heads, 0, a->window, a->scale};
+  const Tree tree = {a->mask, a->positions, a->mask_stride, a->mask_words};
+  return attend(call, &tree, stream);
 }
 
 }  // extern "C"

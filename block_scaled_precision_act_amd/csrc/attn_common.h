@@ -96,6 +96,23 @@ __device__ __forceinline__ int32_t window_start(int32_t at, int32_t window) {
   return max(at, -1) + 1 - window;
 }
 
+// Of a tree's query, which of the 32 tokens from `d` tokens behind the first node on it sees: its own
+// bits from there on, ones for what lies before the tree.  A word is read where it exists.
+__device__ __forceinline__ uint32_t tree_bits(const AttnProblem& p, int32_t query, int32_t d) {
+  const uint32_t* row = p.tree + query * p.tree_stride;
+  const int32_t w = d >> 5;
+  const uint32_t lo = w < 0 ? ~0u : w < p.tree_words ? row[w] : 0u;
+  const uint32_t hi = w < -1 ? ~0u : w + 1 < p.tree_words ? row[w + 1] : 0u;
+  return __builtin_amdgcn_alignbit(hi, lo, d & 31);
+}
+
+// The first key before the tree that its query sees: the query's position lies within the tree's
+// [first, end), as its depth does (whatever the caller's says).
+__device__ __forceinline__ int32_t tree_window_start(const AttnProblem& p, int32_t query, int32_t first,
+                                                     int32_t end) {
+  return window_start(min(max(p.tree_at[query], first), end - 1), p.window);
+}
+
 // A row's weights are exp2(s scale - m), one fused multiply-add each, with m the rounded product of its
 // largest score and the scale.  The maximum that is subtracted moves only when some row's rose by more
 // than `kSlack`: until then weights stay below 2^8, and bf16 and fp32 hold them as well as those below

@@ -131,7 +131,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return __builtin_amdgcn_readfirstlane(v);
 }
 
-template <int D, int MT>
+template <int D, int MT, bool TREE>
 __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(const AttnProblem p) {
   constexpr int KS = D / 32;               // k steps of a score product
   constexpr int EPL = D / 16;              // head values a lane decodes of a token's value row
@@ -239,6 +239,7 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
     // Query rows, as B operands: lane (c, g) holds row c's values [g D/4, (g+1) D/4).
     bf16x8 qf[MT][KS];
     int32_t hi_row[MT], lo_row[MT];
+    int32_t query[MT];                       // TREE: the row's query, its mask's row
     const int32_t first = sq.len - sq.n;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -246,7 +247,12 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       const int tok = r / p.group, hg = r - tok * p.group;
       const bool live = r < sq.rows;
       hi_row[mt] = live && p.causal ? first + tok + 1 : sq.len;
-      lo_row[mt] = live && p.window > 0 ? window_start(first + tok, p.window) : 0;
+      if constexpr (TREE) {
+        query[mt] = sq.q0 + (live ? tok : 0);
+        lo_row[mt] = p.window > 0 ? tree_window_start(p, query[mt], first, sq.len) : 0;
+      } else {
+        lo_row[mt] = live && p.window > 0 ? window_start(first + tok, p.window) : 0;
+      }
       const uint16_t* row = p.q.p + static_cast<int64_t>(sq.q0 + tok) * p.q.token_stride +
                             static_cast<int64_t>(h * p.group + hg) * p.q.head_stride + g * (D / 4);
 #pragma unroll
@@ -257,7 +263,7 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       }
     }
     // Tokens below `full_hi` and from `full_lo` on are seen by every row.
-    const int32_t full_hi = p.causal ? min(first + 1, sq.len) : sq.len;
+    const int32_t full_hi = TREE ? first : p.causal ? min(first + 1, sq.len) : sq.len;
     const int32_t full_lo = p.window > 0 ? sq.len - p.window : 0;
 
     v4f acc[MT][EPL];
@@ -367,12 +373,18 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       if constexpr (decltype(more)::value) load_keys(rk, next);
       if (tok0 + kWaveTokens > full_hi || tok0 < full_lo) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint32_t bits = TREE ? tree_bits(p, query[mt], tok0 - first) : ~0u;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int32_t t = tok0 + (i >> 2) * 16 + (i & 3) * 4 + g;
-            if (t >= hi_row[mt] || t < lo_row[mt]) s[mt][i >> 2][i & 3] = -kInf;
+            const int32_t o = (i >> 2) * 16 + (i & 3) * 4 + g, t = tok0 + o;
+            bool hidden = t >= hi_row[mt];
+            // A window takes of what lies before the tree; of the tree the mask alone does.
+            if constexpr (TREE) hidden = hidden || !(bits >> o & 1) || (t < first && t < lo_row[mt]);
+            else hidden = hidden || t < lo_row[mt];
+            if (hidden) s[mt][i >> 2][i & 3] = -kInf;
           }
+        }
         __builtin_amdgcn_sched_barrier(0);        // keeps the masks a branch
       }
       bf16x8 pf[MT];
@@ -637,8 +649,9 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
 
 template <int D, int MT>
 hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_few_kernel<D, MT>), dim3(static_cast<unsigned>(plan.groups)),
-                     dim3(kThreads), 0, stream, p);
+  const dim3 grid(static_cast<unsigned>(plan.groups)), block(kThreads);
+  if (p.tree) hipLaunchKernelGGL((attn_few_kernel<D, MT, true>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((attn_few_kernel<D, MT, false>), grid, block, 0, stream, p);
   return hipGetLastError();
 }
 

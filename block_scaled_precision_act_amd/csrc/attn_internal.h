@@ -87,6 +87,12 @@ struct AttnProblem {
   uint32_t* counters;
   uint32_t counter_stride;
   float* parts;
+  // A tree of drafted tokens instead of a causal mask (tree != nullptr, causal false): which of a
+  // sequence's last tokens, as many as its queries, a query sees, one bit each, and where it stands.
+  const uint32_t* tree;      // [total_q] rows of tree_words
+  const int32_t* tree_at;    // [total_q], read where there is a window
+  int64_t tree_stride;
+  int32_t tree_words;
 };
 
 // Tokens past a sequence's length that the kernels' token numbers may reach (the rounding to a tile, and

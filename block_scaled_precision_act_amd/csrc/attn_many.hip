@@ -46,6 +46,7 @@ struct Work {
 };
 
 // A whole unit.
+template <bool TREE>
 __device__ __forceinline__ Work unit_of(const AttnProblem& p, int block_rows, int h, int b, int blk) {
   Work w;
   w.h = h;
@@ -74,6 +75,13 @@ __device__ __forceinline__ Work unit_of(const AttnProblem& p, int block_rows, in
   w.tiles = max(0, (w.hi - w.t_begin + kTok - 1) / kTok);
   w.full_hi = p.causal ? min(w.first + tok_lo + 1, w.len) : w.len;
   w.full_lo = p.window > 0 ? window_start(w.first + tok_hi, p.window) : 0;
+  if constexpr (TREE) {                   // any of its queries may stand anywhere in the tree
+    w.low = p.window > 0 ? max(window_start(w.first, p.window), 0) : 0;
+    w.t_begin = w.low & ~(kTok - 1);
+    w.tiles = max(0, (w.hi - w.t_begin + kTok - 1) / kTok);
+    w.full_hi = w.first;
+    w.full_lo = p.window > 0 ? window_start(w.len - 1, p.window) : 0;
+  }
   return w;
 }
 
@@ -147,7 +155,7 @@ struct Deal {
 
 // Called by all THREADS of a workgroup; `first` has room for kMostEntries + 3.  The slots of all heads
 // number less than 2^31.
-template <int THREADS>
+template <int THREADS, bool TREE>
 __device__ __forceinline__ Deal deal(const AttnProblem& p, int block_rows, int row_blocks, int splits,
                                      int groups, uint32_t* first) {
   Deal d;
@@ -156,7 +164,7 @@ __device__ __forceinline__ Deal deal(const AttnProblem& p, int block_rows, int r
   d.heads = p.cache.heads;
   for (uint32_t e = threadIdx.x; e < d.entries; e += THREADS) {
     const uint32_t b = e / row_blocks;
-    const Work w = unit_of(p, block_rows, 0, b, e - b * row_blocks);
+    const Work w = unit_of<TREE>(p, block_rows, 0, b, e - b * row_blocks);
     first[e + 1] = w.any ? static_cast<uint32_t>(w.tiles) + kUnitSlots : 0u;
   }
   __syncthreads();
@@ -212,7 +220,7 @@ __device__ __forceinline__ AttnProblem argument() {
 __device__ __forceinline__ uint32_t group_number() { return blockIdx.y * gridDim.x + blockIdx.x; }
 
 // A workgroup's units or parts, one after the other.  `groups`: runs of a deal (DEALT).
-template <int THREADS, bool DEALT>
+template <int THREADS, bool DEALT, bool TREE>
 struct Walk {
   uint32_t g, x, end;
   bool dealt;
@@ -223,7 +231,7 @@ struct Walk {
     end = 1;
     dealt = false;
     if constexpr (DEALT) {
-      const Deal d = deal<THREADS>(p, block_rows, row_blocks, splits, groups, first);
+      const Deal d = deal<THREADS, TREE>(p, block_rows, row_blocks, splits, groups, first);
       RunStart* const starts = reinterpret_cast<RunStart*>(p.parts);
       if (blockIdx.x == 0 && threadIdx.x == 0) starts[0] = RunStart{0, 0, 0, d.groups};
       if (d.groups == 0) {
@@ -254,7 +262,7 @@ struct Walk {
       const uint32_t heads = p.cache.heads, h = id % heads, r = id / heads, b = r % p.batch;
       if (!DEALT && r / p.batch / splits >= static_cast<uint32_t>(row_blocks)) return false;
       const int part = r / p.batch % splits, blk = row_blocks - 1 - static_cast<int>(r / p.batch / splits);
-      *w = unit_of(p, block_rows, h, b, blk);
+      *w = unit_of<TREE>(p, block_rows, h, b, blk);
       const int parts = parts_of(w->tiles, splits);
       if (!w->any || part >= parts) return false;
       if (parts == 1) return true;
@@ -266,7 +274,7 @@ struct Walk {
     }
     const Deal d = {first, static_cast<uint32_t>(p.batch * row_blocks), 0, 0};
     const uint32_t per = d.per_head(), head = x / per, base = head * per, e = d.entry(x - base);
-    *w = unit_of(p, block_rows, head, e / row_blocks, e % row_blocks);
+    *w = unit_of<TREE>(p, block_rows, head, e / row_blocks, e % row_blocks);
     const uint32_t s = base + d.slot_of(e), stop = base + d.slot_of(e + 1), upto = min(end, stop);
     const uint32_t tile0 = x > s ? x - s - kUnitSlots : 0;
     if (x > s || upto < stop) *slot = 2 * g + (x == s);
@@ -283,6 +291,7 @@ struct Row {
   int32_t tok, hg, lo, hi;                // query, grouped head, the keys it sees
 };
 
+template <bool TREE>
 __device__ __forceinline__ Row row_of(const AttnProblem& p, const Work& w, int tile, uint32_t thread = threadIdx.x) {
   Row r;
   const int32_t i = w.r0 + tile * 32 + (thread & 31);
@@ -290,7 +299,8 @@ __device__ __forceinline__ Row row_of(const AttnProblem& p, const Work& w, int t
   r.tok = r.live ? i / p.group : 0;
   r.hg = r.live ? i - r.tok * p.group : 0;
   r.hi = r.live && p.causal ? w.first + r.tok + 1 : w.len;
-  r.lo = r.live && p.window > 0 ? window_start(w.first + r.tok, p.window) : 0;
+  if constexpr (TREE) r.lo = p.window > 0 ? tree_window_start(p, w.q0 + r.tok, w.first, w.len) : 0;
+  else r.lo = r.live && p.window > 0 ? window_start(w.first + r.tok, p.window) : 0;
   return r;
 }
 
@@ -471,13 +481,19 @@ constexpr int kLdsReads = 0x100, kProducts = 0x8;
 template <int KIND, int N>
 __device__ __forceinline__ void then() { __builtin_amdgcn_sched_group_barrier(KIND, N, 0); }
 
-// Masks the lane's 16 scores of the 32 tokens from t0.
-__device__ __forceinline__ void mask(v16f& s, const Row& r, int32_t t0) {
-  const int32_t at = t0 + 4 * ((threadIdx.x & 63) >> 5);
+// Masks the lane's 16 scores of the 32 tokens from t0.  A tree's window takes of what lies before the
+// tree; of the tree the mask alone does.
+template <bool TREE>
+__device__ __forceinline__ void mask(v16f& s, const AttnProblem& p, const Work& w, const Row& r, int32_t t0) {
+  const int32_t half = 4 * ((threadIdx.x & 63) >> 5), at = t0 + half;
+  const uint32_t bits = TREE ? tree_bits(p, w.q0 + r.tok, t0 - w.first) >> half : ~0u;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    const int32_t key = at + (e & 3) + 8 * (e >> 2);
-    if (key >= r.hi || key < r.lo) s[e] = -kInf;
+    const int32_t o = (e & 3) + 8 * (e >> 2), key = at + o;
+    bool hidden = key >= r.hi;
+    if constexpr (TREE) hidden = hidden || !(bits >> o & 1) || (key < w.first && key < r.lo);
+    else hidden = hidden || key < r.lo;
+    if (hidden) s[e] = -kInf;
     if (e % 8 == 7) __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -561,7 +577,7 @@ __device__ __forceinline__ void finish(const AttnProblem& p, const Work& w, cons
 // four lots of 4 for two of its N sums.  A launch of its own: the parts of one unit would be joined
 // by one workgroup otherwise (128 rows of 60000 keys in 64 parts: 110 us, 63 us so).
 // HALVES: 2 where two wavefronts share rows (attn_wide_kernel).
-template <int DT, int THREADS, int N, int HALVES>
+template <int DT, int THREADS, int N, int HALVES, bool TREE>
 __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p, int row_blocks, int splits,
                                                             int groups) {
   constexpr int kSlices = 4 * N / 2, kTiles = THREADS / 64 / HALVES;
@@ -574,7 +590,7 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p,
   if (runs == 0) {                           // the units as they are
     const uint32_t heads = p.cache.heads;
     if (splits == 1 || left >= heads * p.batch * row_blocks) return;
-    w = unit_of(p, 32 * kTiles, left % heads, left / heads % p.batch, left / heads / p.batch);
+    w = unit_of<TREE>(p, 32 * kTiles, left % heads, left / heads % p.batch, left / heads / p.batch);
     parts = parts_of(w.tiles, splits);
     if (!w.any || parts == 1) return;
     base = left * splits;
@@ -612,7 +628,7 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p,
     }
     if (parts == 0) return;
     const uint32_t entries = p.batch * row_blocks, h = unit / entries, e = unit - h * entries;
-    w = unit_of(p, 32 * kTiles, h, e / row_blocks, e % row_blocks);
+    w = unit_of<TREE>(p, 32 * kTiles, h, e / row_blocks, e % row_blocks);
     base = 2 * (g0 - 1);
     lead = 1;
     step = 2;
@@ -654,7 +670,7 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p,
       acc[1][0] += x[i][1] * f;
     }
   }
-  const Row r = row_of(p, w, wave % kTiles);
+  const Row r = row_of<TREE>(p, w, wave % kTiles);
   if (!r.live) return;
   const int d0 = wave / kTiles * N + d;
   if (q == 0) write_values<DT, 2, 0, 1>(p, w, r, acc, l, d0);
@@ -666,7 +682,7 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p,
 
 // NW wavefronts of 32 query rows each.  Of 8, the first four decode keys and the others values (one
 // of each to a SIMD); of 4, all decode both.
-template <int D, int NW, bool DEALT>
+template <int D, int NW, bool DEALT, bool TREE>
 __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem args, int row_blocks,
                                                                int splits, int groups) {
   constexpr int KS = D / 16, DT = D / 32, kThreads = 64 * NW;
@@ -676,13 +692,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool keys = NW == 4 || wave < 4, values = NW == 4 || wave >= 4;
-  Walk<kThreads, DEALT> walk(args, 32 * NW, row_blocks, splits, groups, first);
+  Walk<kThreads, DEALT, TREE> walk(args, 32 * NW, row_blocks, splits, groups, first);
   for (;;) {
     const AttnProblem p = DEALT ? argument() : args;
     Work w;
     int slot;
     if (!walk.next(p, 32 * NW, row_blocks, splits, first, &w, &slot)) return;
-    const Row row = row_of(p, w, wave);
+    const Row row = row_of<TREE>(p, w, wave);
     bf16x8 qf[KS];
     load_query(p, w, row, qf);
     const Decoder<D> dec(p, w, wave & 3);
@@ -707,8 +723,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
       constexpr bool LAST = decltype(final)::value;
       const int32_t t0 = w.t_begin + i * kTok;
       if (t0 + kTok > w.full_hi || t0 < w.full_lo) {
-        mask(s[0], row, t0);
-        mask(s[1], row, t0 + 32);
+        mask<TREE>(s[0], p, w, row, t0);
+        mask<TREE>(s[1], p, w, row, t0 + 32);
       }
       float top = s[0][0];
 #pragma unroll
@@ -806,7 +822,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
 //   second  the products of tile i's weights and values; half 0 decodes the keys of tile i + 2
 // so that each of the matrix runs has the other side's decoding beside it, and one buffer of keys,
 // values and weights is enough.
-template <bool DEALT>
+template <bool DEALT, bool TREE>
 __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem args, int row_blocks, int splits,
                                                            int groups) {
   constexpr int D = 256, KS = D / 16, DT = D / 32, N = DT / 2, kThreads = 512;
@@ -818,13 +834,13 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
   const int lane = threadIdx.x & 63, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rt = wave & 3, half = wave >> 2;
-  Walk<kThreads, DEALT> walk(args, 128, row_blocks, splits, groups, first);
+  Walk<kThreads, DEALT, TREE> walk(args, 128, row_blocks, splits, groups, first);
   for (;;) {
     const AttnProblem p = DEALT ? argument() : args;
     Work w;
     int slot;
     if (!walk.next(p, 128, row_blocks, splits, first, &w, &slot)) return;
-    const Row row = row_of(p, w, rt);
+    const Row row = row_of<TREE>(p, w, rt);
     bf16x8 qf[KS];
     load_query(p, w, row, qf);
     const Decoder<D> dec(p, w, rt);
@@ -853,7 +869,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
       // (A branch for them, as in attn_many_kernel, takes 5% of a chunk in this loop, by its registers.)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = rounded_product(s[e], p.scale_log2);
-      if (t0 + kTok > w.full_hi || t0 < w.full_lo) mask(s, row, t0 + half * 32);
+      if (t0 + kTok > w.full_hi || t0 < w.full_lo) mask<TREE>(s, p, w, row, t0 + half * 32);
       float top = s[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
@@ -944,13 +960,13 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
     l += tops[0][rt][half ^ 1][c];
 
     // The row's numbers are worked out again: kept through the loop, they cost it registers.
-    finish<DT, kThreads>(p, w, row_of(p, w, rt, again(threadIdx.x)), slot, acc, m, l, half * N);
+    finish<DT, kThreads>(p, w, row_of<TREE>(p, w, rt, again(threadIdx.x)), slot, acc, m, l, half * N);
     if constexpr (!DEALT) return;
     lds_barrier();                           // before the next one's keys and values
   }
 }
 
-template <int D, int NW>
+template <int D, int NW, bool TREE>
 hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
   constexpr int DT = D / 32, kThreads = D == 256 ? 512 : 64 * NW, N = D == 256 ? DT / 2 : DT;
   const int64_t units = static_cast<int64_t>(plan.row_blocks) * p.batch * p.cache.heads;
@@ -963,17 +979,17 @@ hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p, plan.row_blocks, plan.splits, plan.groups);
   };
   if constexpr (D == 256) {
-    if (plan.groups) attend(attn_wide_kernel<true>);
-    else attend(attn_wide_kernel<false>);
+    if (plan.groups) attend(attn_wide_kernel<true, TREE>);
+    else attend(attn_wide_kernel<false, TREE>);
   } else {
-    if (plan.groups) attend(attn_many_kernel<D, NW, true>);
-    else attend(attn_many_kernel<D, NW, false>);
+    if (plan.groups) attend(attn_many_kernel<D, NW, true, TREE>);
+    else attend(attn_many_kernel<D, NW, false, TREE>);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (plan.splits == 1 && plan.groups == 0)) return e;
   // At most so many units have parts: there are no more, and a run begins inside of each in a deal.
   const int64_t joined = plan.groups ? std::min<int64_t>(units, plan.groups - 1) : units;
-  hipLaunchKernelGGL((attn_join_kernel<DT, kThreads, N, D == 256 ? 2 : 1>),
+  hipLaunchKernelGGL((attn_join_kernel<DT, kThreads, N, D == 256 ? 2 : 1, TREE>),
                      dim3(static_cast<unsigned>(joined * (2 * N))), dim3(kThreads), 0, stream, p,
                      plan.row_blocks, plan.splits, plan.groups);
   return hipGetLastError();
@@ -1031,12 +1047,22 @@ int64_t most_part_bytes(int64_t max_q, int64_t group, int head_dim) {
   return most;
 }
 
-hipError_t launch_attn_many(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
+namespace {
+
+template <bool TREE>
+hipError_t launch_any(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
   const bool eight = plan.row_tiles == 8;
-  if (p.cache.head_dim == 64) return eight ? launch<64, 8>(p, plan, stream) : launch<64, 4>(p, plan, stream);
+  if (p.cache.head_dim == 64)
+    return eight ? launch<64, 8, TREE>(p, plan, stream) : launch<64, 4, TREE>(p, plan, stream);
   if (p.cache.head_dim == 128)
-    return eight ? launch<128, 8>(p, plan, stream) : launch<128, 4>(p, plan, stream);
-  return launch<256, 4>(p, plan, stream);
+    return eight ? launch<128, 8, TREE>(p, plan, stream) : launch<128, 4, TREE>(p, plan, stream);
+  return launch<256, 4, TREE>(p, plan, stream);
+}
+
+}  // namespace
+
+hipError_t launch_attn_many(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
+  return p.tree ? launch_any<true>(p, plan, stream) : launch_any<false>(p, plan, stream);
 }
 
 }  // namespace mx
