@@ -24,7 +24,8 @@ Nodes nodes(int64_t batch, int64_t total_q, int64_t max_q, const int32_t* starts
   return Nodes{starts, static_cast<int32_t>(batch), static_cast<int32_t>(total_q), static_cast<int32_t>(max_q)};
 }
 
-constexpr int64_t kVerifyWorkspace = kCounterBytes + kVerifyGroups * 8;
+// Behind the counters, 64 sums of each sequence whose rows are cut: at most every second workgroup's.
+constexpr int64_t kVerifyWorkspace = kCounterBytes + kVerifyGroups / 2 * 64 * 8;
 
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -100,7 +101,6 @@ int mx_tree_verify(const mx_tree_verify_args* a, void* stream) {
   p.type = static_cast<int>(a->type);
   p.replacement = a->replacement != 0;
   p.counters = static_cast<uint32_t*>(a->workspace);
-  p.counter_stride = counter_stride(a->batch);
   p.parts = reinterpret_cast<double*>(static_cast<uint8_t*>(a->workspace) + kCounterBytes);
   return status_of(launch_tree_verify(p, static_cast<hipStream_t>(stream)));
 }

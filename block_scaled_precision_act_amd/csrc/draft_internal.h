@@ -41,12 +41,13 @@ struct TreeVerifyProblem {
   int32_t vocab, width;
   int type;                  // 0 fp32, 1 bf16, 2 fp16
   bool replacement;
-  uint32_t* counters;
-  uint32_t counter_stride;
-  double* parts;             // kVerifyGroups of them
+  uint32_t* counters;        // kTeamWords of each
+  double* parts;             // 64 of each sequence whose rows are cut
 };
-// Workgroups that a row's slices are dealt to, over all sequences: two a CU.
-constexpr int64_t kVerifyGroups = 512;
+// Workgroups that a row's slices are dealt to, over all sequences: one a CU.
+constexpr int64_t kVerifyGroups = 256;
+constexpr int64_t kTeamWords = 32;       // a cache line
+static_assert(kTeamWords * 65535 <= kMaxUnits, "every batch's counters lie in the workspace's first part");
 hipError_t launch_tree_verify(const TreeVerifyProblem& p, hipStream_t stream);
 
 constexpr int kLayersALaunch = 64;       // four pointers each: 2 KB of arguments
