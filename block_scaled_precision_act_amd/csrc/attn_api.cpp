@@ -83,7 +83,7 @@ int attend(const mx_attn_fp4_args& args, const Tree* tree, void* stream) {
                                        a->q_heads, c.head_dim, 8)})) != MX_OK)
     return st;
   mx::AttnPlan plan = mx::plan_attn(a->batch, a->max_q, a->q_heads, c.kv_heads,
-                                    static_cast<int>(c.head_dim));
+                                    static_cast<int>(c.head_dim), tree != nullptr);
   // The deal of tiles of 128 tokens (plus a few slots for each sequence and head) counts in 31 bits.
   const int64_t units = a->batch * c.kv_heads;
   if (plan.few && (units > mx::kMaxUnits || !fits31(units, a->table_width * c.page_size / 128 + 8)))
@@ -99,7 +99,7 @@ int attend(const mx_attn_fp4_args& args, const Tree* tree, void* stream) {
                               !aligned(a->workspace, 256)))
     return MX_ERR_WORKSPACE;
   if ((st = device_status()) != MX_OK) return st;
-  mx::AttnProblem p;
+  mx::AttnTreeProblem p;
   p.cache = cache_of(c);
   p.q = rows(a->q, a->q_token_stride, a->q_head_stride);
   p.out = rows(a->out, a->out_token_stride, a->out_head_stride);

@@ -4,6 +4,8 @@
 #include "attn_internal.h"
 #include "mx_quant.h"
 
+#include <type_traits>
+
 namespace mx {
 namespace {
 
@@ -96,9 +98,12 @@ __device__ __forceinline__ int32_t window_start(int32_t at, int32_t window) {
   return max(at, -1) + 1 - window;
 }
 
+template <bool TREE>
+using ProblemOf = std::conditional_t<TREE, AttnTreeProblem, AttnProblem>;
+
 // Of a tree's query, which of the 32 tokens from `d` tokens behind the first node on it sees: its own
 // bits from there on, ones for what lies before the tree.  A word is read where it exists.
-__device__ __forceinline__ uint32_t tree_bits(const AttnProblem& p, int32_t query, int32_t d) {
+__device__ __forceinline__ uint32_t tree_bits(const AttnTreeProblem& p, int32_t query, int32_t d) {
   const uint32_t* row = p.tree + query * p.tree_stride;
   const int32_t w = d >> 5;
   const uint32_t lo = w < 0 ? ~0u : w < p.tree_words ? row[w] : 0u;
@@ -108,7 +113,7 @@ __device__ __forceinline__ uint32_t tree_bits(const AttnProblem& p, int32_t quer
 
 // The first key before the tree that its query sees: the query's position lies within the tree's
 // [first, end), as its depth does (whatever the caller's says).
-__device__ __forceinline__ int32_t tree_window_start(const AttnProblem& p, int32_t query, int32_t first,
+__device__ __forceinline__ int32_t tree_window_start(const AttnTreeProblem& p, int32_t query, int32_t first,
                                                      int32_t end) {
   return window_start(min(max(p.tree_at[query], first), end - 1), p.window);
 }

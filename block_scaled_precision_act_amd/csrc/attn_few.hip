@@ -108,6 +108,9 @@ constexpr uint32_t kUnitSlots = 2;
 // What joining one part costs, counted in tiles: a sequence and head of n tiles cut into runs of s
 // takes about s + kJoinCost * n / s, least at s = sqrt(kJoinCost * n), so runs are no shorter.
 constexpr float kJoinCost = 0.2f;
+// A tree's, for each 16 rows: what a part leaves grows with them.  (32 rows of 1000 keys, 8 heads: 14 us, 16
+// with 0.2 whatever the rows; 4 x 26 rows of 700 to 1500, 12 heads of 64: 15 and 20; twice that, 16 and 19.)
+constexpr float kTreeJoin = 0.3f;
 
 // The slots of a sequence: for each head, kUnitSlots and its tiles.
 __device__ __forceinline__ uint32_t slots(const Sequence& s, int heads) {
@@ -132,7 +135,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 }
 
 template <int D, int MT, bool TREE>
-__global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(const AttnProblem p) {
+__global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(const ProblemOf<TREE> p) {
   constexpr int KS = D / 32;               // k steps of a score product
   constexpr int EPL = D / 16;              // head values a lane decodes of a token's value row
   constexpr int PAD = D + 4;
@@ -157,7 +160,7 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
   Sequence mine_of = {};                   // up to 64 sequences: the lane's
   auto share_of = [&]() {
     const uint32_t even = (total + gridDim.x - 1) / gridDim.x;
-    const float least = __builtin_sqrtf(kJoinCost * static_cast<float>(longest));
+    const float least = __builtin_sqrtf((TREE ? kTreeJoin * MT : kJoinCost) * static_cast<float>(longest));
     return max(max(even, 1u), static_cast<uint32_t>(least));
   };
   if (p.batch <= 64) {                     // a lane each, every wavefront for itself
@@ -374,7 +377,8 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
       if (tok0 + kWaveTokens > full_hi || tok0 < full_lo) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const uint32_t bits = TREE ? tree_bits(p, query[mt], tok0 - first) : ~0u;
+          uint32_t bits = ~0u;
+          if constexpr (TREE) bits = tree_bits(p, query[mt], tok0 - first);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int32_t o = (i >> 2) * 16 + (i & 3) * 4 + g, t = tok0 + o;
@@ -648,15 +652,16 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
 }
 
 template <int D, int MT>
-hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
+hipError_t launch(const AttnTreeProblem& p, const AttnPlan& plan, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(plan.groups)), block(kThreads);
+  const AttnProblem& plain = p;
   if (p.tree) hipLaunchKernelGGL((attn_few_kernel<D, MT, true>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((attn_few_kernel<D, MT, false>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((attn_few_kernel<D, MT, false>), grid, block, 0, stream, plain);
   return hipGetLastError();
 }
 
 template <int D>
-hipError_t launch_d(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
+hipError_t launch_d(const AttnTreeProblem& p, const AttnPlan& plan, hipStream_t stream) {
   if (plan.row_tiles == 1) return launch<D, 1>(p, plan, stream);
   if (plan.row_tiles == 2) return launch<D, 2>(p, plan, stream);
   if constexpr (D < 256) return launch<D, 4>(p, plan, stream);
@@ -665,7 +670,7 @@ hipError_t launch_d(const AttnProblem& p, const AttnPlan& plan, hipStream_t stre
 
 }  // namespace
 
-hipError_t launch_attn_few(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
+hipError_t launch_attn_few(const AttnTreeProblem& p, const AttnPlan& plan, hipStream_t stream) {
   if (p.cache.head_dim == 64) return launch_d<64>(p, plan, stream);
   if (p.cache.head_dim == 128) return launch_d<128>(p, plan, stream);
   return launch_d<256>(p, plan, stream);

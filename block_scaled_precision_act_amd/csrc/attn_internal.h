@@ -87,8 +87,11 @@ struct AttnProblem {
   uint32_t* counters;
   uint32_t counter_stride;
   float* parts;
-  // A tree of drafted tokens instead of a causal mask (tree != nullptr, causal false): which of a
-  // sequence's last tokens, as many as its queries, a query sees, one bit each, and where it stands.
+};
+// With a tree of drafted tokens instead of a causal mask (tree != nullptr, causal false): which of a
+// sequence's last tokens, as many as its queries, a query sees, one bit each, and where it stands.  The
+// kernels without one take the first part alone.
+struct AttnTreeProblem : AttnProblem {
   const uint32_t* tree;      // [total_q] rows of tree_words
   const int32_t* tree_at;    // [total_q], read where there is a window
   int64_t tree_stride;
@@ -115,7 +118,8 @@ constexpr uint32_t counter_stride(int64_t units) {
 // head are its (query, grouped head) pairs, max_q * group of them at most.
 struct AttnPlan {
   bool few;                  // few rows: the cache is what costs (attn_few.hip), else attn_many.hip
-  int row_tiles;             // of a workgroup: 16-row tiles (few), wavefronts of 32 rows (many)
+  int row_tiles;             // few: 16-row tiles of a workgroup
+  int waves, split;          // many: wavefronts of a workgroup, and how many of them share 32 rows
   int groups;                // workgroups that the cached tokens are dealt to (many: 0: no deal)
   int row_blocks, splits;    // many: blocks of rows of each (sequence, head), parts of their keys at most
   int64_t part_bytes;        // of partial results
@@ -127,11 +131,12 @@ constexpr int few_waves(int head_dim, int row_tiles) {
 // A deal among many rows (attn_many.hip) is looked at where a part of a unit may have more tiles of 64
 // tokens.
 constexpr int64_t kLeastDealTiles = 32;
-AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim);
+AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim,
+                   bool tree = false);
 // Partial results of any plan with at most max_q queries a sequence.
 int64_t most_part_bytes(int64_t max_q, int64_t group, int head_dim);
 
-hipError_t launch_attn_few(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream);
-hipError_t launch_attn_many(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream);
+hipError_t launch_attn_few(const AttnTreeProblem& p, const AttnPlan& plan, hipStream_t stream);
+hipError_t launch_attn_many(const AttnTreeProblem& p, const AttnPlan& plan, hipStream_t stream);
 
 }  // namespace mx

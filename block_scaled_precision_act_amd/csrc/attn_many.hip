@@ -207,11 +207,12 @@ __device__ __forceinline__ Deal deal(const AttnProblem& p, int block_rows, int r
 
 // The kernel's first argument, read again from its place: what a workgroup derives from it for one
 // unit is not kept in registers for the next (that cost spills in the loop over tokens).
-__device__ __forceinline__ AttnProblem argument() {
+template <bool TREE>
+__device__ __forceinline__ ProblemOf<TREE> argument() {
   auto at = reinterpret_cast<uintptr_t>(__builtin_amdgcn_kernarg_segment_ptr());
   asm volatile("" : "+s"(at));
-  AttnProblem p;
-  __builtin_memcpy(&p, reinterpret_cast<const __attribute__((address_space(4))) AttnProblem*>(at), sizeof(p));
+  ProblemOf<TREE> p;
+  __builtin_memcpy(&p, reinterpret_cast<const __attribute__((address_space(4))) ProblemOf<TREE>*>(at), sizeof(p));
   return p;
 }
 
@@ -292,7 +293,7 @@ struct Row {
 };
 
 template <bool TREE>
-__device__ __forceinline__ Row row_of(const AttnProblem& p, const Work& w, int tile, uint32_t thread = threadIdx.x) {
+__device__ __forceinline__ Row row_of(const ProblemOf<TREE>& p, const Work& w, int tile, uint32_t thread = threadIdx.x) {
   Row r;
   const int32_t i = w.r0 + tile * 32 + (thread & 31);
   r.live = i < w.rows;
@@ -484,9 +485,10 @@ __device__ __forceinline__ void then() { __builtin_amdgcn_sched_group_barrier(KI
 // Masks the lane's 16 scores of the 32 tokens from t0.  A tree's window takes of what lies before the
 // tree; of the tree the mask alone does.
 template <bool TREE>
-__device__ __forceinline__ void mask(v16f& s, const AttnProblem& p, const Work& w, const Row& r, int32_t t0) {
+__device__ __forceinline__ void mask(v16f& s, const ProblemOf<TREE>& p, const Work& w, const Row& r, int32_t t0) {
   const int32_t half = 4 * ((threadIdx.x & 63) >> 5), at = t0 + half;
-  const uint32_t bits = TREE ? tree_bits(p, w.q0 + r.tok, t0 - w.first) >> half : ~0u;
+  uint32_t bits = ~0u;
+  if constexpr (TREE) bits = tree_bits(p, w.q0 + r.tok, t0 - w.first) >> half;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int32_t o = (e & 3) + 8 * (e >> 2), key = at + o;
@@ -545,9 +547,10 @@ __device__ __forceinline__ void write_lse(const AttnProblem& p, const Work& w, c
 constexpr int64_t part_floats(int threads, int n) { return static_cast<int64_t>(threads) * (16 * n + 1); }
 
 // The rows are written, or a part of them left for the join.
-template <int DT, int THREADS, int N>
+template <int DT, int THREADS, bool TREE, int N>
 __device__ __forceinline__ void finish(const AttnProblem& p, const Work& w, const Row& r, int slot,
                                        const v16f (&acc)[N], float m, float l, int d0) {
+  if (TREE && !r.live) return;             // what the join does not read
   if (slot < 0) {
     if (!r.live) return;
     v4f x[N][4];
@@ -578,7 +581,7 @@ __device__ __forceinline__ void finish(const AttnProblem& p, const Work& w, cons
 // by one workgroup otherwise (128 rows of 60000 keys in 64 parts: 110 us, 63 us so).
 // HALVES: 2 where two wavefronts share rows (attn_wide_kernel).
 template <int DT, int THREADS, int N, int HALVES, bool TREE>
-__global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p, int row_blocks, int splits,
+__global__ __launch_bounds__(THREADS) void attn_join_kernel(const ProblemOf<TREE> p, int row_blocks, int splits,
                                                             int groups) {
   constexpr int kSlices = 4 * N / 2, kTiles = THREADS / 64 / HALVES;
   const RunStart* const starts = reinterpret_cast<const RunStart*>(p.parts);
@@ -597,36 +600,62 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p,
     lead = 0;
     step = 1;
   } else {
-    // Those that runs begin inside of, the i-th by the workgroups i of each slice: the part of the
-    // workgroup before the first of these runs, and theirs.
-    constexpr int kChunks = kMostGroups / 64;
-    RunStart all[kChunks];
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) all[i] = starts[i * 64 + lane];
-    uint32_t g0 = 0, before = ~0u, unit = ~0u;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const uint32_t g = i * 64 + lane;
-      const bool in = g > 0 && g < runs && all[i].at > all[i].unit_first && all[i].at < all[i].unit_end;
-      const uint32_t its = in ? all[i].unit : ~0u;
-      uint32_t prev = __shfl_up(its, 1, 64);
-      if (lane == 0) prev = before;
-      before = __builtin_amdgcn_readlane(its, 63);
-      if (parts == 0) {
-        uint64_t firsts = __ballot(in && prev != its);
-        const uint32_t n = __builtin_popcountll(firsts);
-        if (left < n) {
-          for (; left > 0; --left) firsts &= firsts - 1;
-          g0 = i * 64 + __builtin_ctzll(firsts);
-          unit = __builtin_amdgcn_readlane(its, g0 & 63);
-          parts = 1;
+    uint32_t g0 = 0, unit = ~0u;
+    if constexpr (TREE) {
+      // Those that runs begin inside of, each by the workgroups of the first of these runs: the part of the run
+      // before it, and theirs.  (A run's neighbours are all it looks at: 41 sequences of up to 8192 tokens, 84
+      // rows of 8 heads: 8 us; 14 where every workgroup counted the units before its own.)
+      g0 = left + 1;
+      if (g0 >= runs) return;
+      for (uint32_t at = g0 - 1;; at += 64) {            // lane i: run at + i
+        const uint32_t g = at + lane;
+        const RunStart s = starts[min(g, runs - 1)];
+        const bool in = g > 0 && g < runs && s.at > s.unit_first && s.at < s.unit_end;
+        const uint32_t its = in ? s.unit : ~0u;
+        uint64_t same;
+        if (at < g0) {
+          unit = __builtin_amdgcn_readlane(its, 1);
+          if (unit == ~0u || static_cast<uint32_t>(__builtin_amdgcn_readlane(its, 0)) == unit) return;
+          same = __ballot(its == unit) | 1u;             // lane 0: the part that begins the unit
         } else {
-          left -= n;
+          same = __ballot(its == unit);
         }
+        const int n = ~same ? __builtin_ctzll(~same) : 64;
+        parts += n;
+        if (n < 64) break;
       }
-      if (parts > 0) parts += __builtin_popcountll(__ballot(its == unit));
+    } else {
+      // Those that runs begin inside of, the i-th by the workgroups i of each slice: the part of the
+      // workgroup before the first of these runs, and theirs.
+      constexpr int kChunks = kMostGroups / 64;
+      RunStart all[kChunks];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) all[i] = starts[i * 64 + lane];
+      uint32_t before = ~0u;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const uint32_t g = i * 64 + lane;
+        const bool in = g > 0 && g < runs && all[i].at > all[i].unit_first && all[i].at < all[i].unit_end;
+        const uint32_t its = in ? all[i].unit : ~0u;
+        uint32_t prev = __shfl_up(its, 1, 64);
+        if (lane == 0) prev = before;
+        before = __builtin_amdgcn_readlane(its, 63);
+        if (parts == 0) {
+          uint64_t firsts = __ballot(in && prev != its);
+          const uint32_t n = __builtin_popcountll(firsts);
+          if (left < n) {
+            for (; left > 0; --left) firsts &= firsts - 1;
+            g0 = i * 64 + __builtin_ctzll(firsts);
+            unit = __builtin_amdgcn_readlane(its, g0 & 63);
+            parts = 1;
+          } else {
+            left -= n;
+          }
+        }
+        if (parts > 0) parts += __builtin_popcountll(__ballot(its == unit));
+      }
+      if (parts == 0) return;
     }
-    if (parts == 0) return;
     const uint32_t entries = p.batch * row_blocks, h = unit / entries, e = unit - h * entries;
     w = unit_of<TREE>(p, 32 * kTiles, h, e / row_blocks, e % row_blocks);
     base = 2 * (g0 - 1);
@@ -634,6 +663,8 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p,
     step = 2;
   }
   const int wave = threadIdx.x / 64, row = wave * 32 + (threadIdx.x & 31);
+  if constexpr (TREE)                      // a block of few rows: others leave nothing
+    if (!row_of<TREE>(p, w, wave % kTiles).live) return;
   const int q = slice % 4, d = slice / 4 * 2;
   constexpr int64_t kPart = part_floats(THREADS, N);
   const float* src = p.parts + kStartFloats + base * kPart;
@@ -680,25 +711,77 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const AttnProblem p,
   if (q == 0 && d0 == 0) write_lse(p, w, r, m, l);
 }
 
-// NW wavefronts of 32 query rows each.  Of 8, the first four decode keys and the others values (one
-// of each to a SIMD); of 4, all decode both.
-template <int D, int NW, bool DEALT, bool TREE>
-__global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem args, int row_blocks,
+// What two wavefronts that share rows have of them, put together in the first one's registers: the second
+// leaves its share in LDS, half of the sums at a time (`room` holds that of every pair; nobody else uses it).
+template <int DT, int PAIRS>
+__device__ __forceinline__ void join_pair(bool second, int pair, v16f (&acc)[DT], float& m, float& l, float* room,
+                                          float (*stats)[2][64]) {
+  const int lane = threadIdx.x & 63;
+  if (second) {
+    stats[pair][0][lane] = m;
+    stats[pair][1][lane] = l;
+  }
+  float mine = 1.f, its = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float4* const at = reinterpret_cast<float4*>(room) + pair * (DT / 2 * 4 * 64) + lane;
+    if (second) {
+#pragma unroll
+      for (int d = 0; d < DT / 2; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          at[(d * 4 + i) * 64] = make_float4(acc[k * (DT / 2) + d][4 * i], acc[k * (DT / 2) + d][4 * i + 1],
+                                             acc[k * (DT / 2) + d][4 * i + 2], acc[k * (DT / 2) + d][4 * i + 3]);
+    }
+    lds_barrier();
+    if (!second) {
+      if (k == 0) {
+        const float om = stats[pair][0][lane], now = fmaxf(m, om);
+        mine = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
+        its = om == -kInf ? 0.f : __builtin_amdgcn_exp2f(om - now);
+        m = now;
+        l = l * mine + stats[pair][1][lane] * its;
+      }
+#pragma unroll
+      for (int d = 0; d < DT / 2; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = at[(d * 4 + i) * 64];
+          v16f& a = acc[k * (DT / 2) + d];
+          a[4 * i] = a[4 * i] * mine + x.x * its;
+          a[4 * i + 1] = a[4 * i + 1] * mine + x.y * its;
+          a[4 * i + 2] = a[4 * i + 2] * mine + x.z * its;
+          a[4 * i + 3] = a[4 * i + 3] * mine + x.w * its;
+        }
+    }
+    lds_barrier();
+  }
+}
+
+// NW wavefronts.  Of 8, the first four decode keys and the others values (one of each to a SIMD); of 4,
+// all decode both.  Each has 32 query rows and all 64 tokens of a tile (SPLIT 1); or two share 32 rows,
+// with 32 tokens each (SPLIT 2), so that few rows keep every wavefront at work.
+template <int D, int NW, bool DEALT, bool TREE, int SPLIT>
+__global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const ProblemOf<TREE> args, int row_blocks,
                                                                int splits, int groups) {
   constexpr int KS = D / 16, DT = D / 32, kThreads = 64 * NW;
+  constexpr int kAhead = SPLIT;            // tiles whose codes are loaded before they are decoded
+  constexpr int kTiles = NW / SPLIT, kHalves = 2 / SPLIT;     // of rows; of a tile's tokens, a wavefront's
   __shared__ uint4 kl[2][2 * KS * 64];
   __shared__ uint4 vl[2][4 * DT * 64];
+  __shared__ float stats[SPLIT == 2 ? kTiles : 1][2][64];
   __shared__ uint32_t first[DEALT ? kMostEntries + 3 : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rows_of = SPLIT == 1 ? wave : wave % kTiles, half = SPLIT == 1 ? 0 : wave / kTiles;
   const bool keys = NW == 4 || wave < 4, values = NW == 4 || wave >= 4;
-  Walk<kThreads, DEALT, TREE> walk(args, 32 * NW, row_blocks, splits, groups, first);
+  Walk<kThreads, DEALT, TREE> walk(args, 32 * kTiles, row_blocks, splits, groups, first);
   for (;;) {
-    const AttnProblem p = DEALT ? argument() : args;
+    const ProblemOf<TREE> p = DEALT ? argument<TREE>() : args;
     Work w;
     int slot;
-    if (!walk.next(p, 32 * NW, row_blocks, splits, first, &w, &slot)) return;
-    const Row row = row_of<TREE>(p, w, wave);
+    if (!walk.next(p, 32 * kTiles, row_blocks, splits, first, &w, &slot)) return;
+    const Row row = row_of<TREE>(p, w, rows_of);
     bf16x8 qf[KS];
     load_query(p, w, row, qf);
     const Decoder<D> dec(p, w, wave & 3);
@@ -708,9 +791,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
     float slack = kSlack;                    // what a row's maximum may rise by before it is moved
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = v16f(0.f);
-    // A wavefront that decodes one of the two holds one share.
-    Raw rk, rv_own;
-    Raw& rv = NW == 4 ? rv_own : rk;
+    // A wavefront that decodes one of the two holds one share; of two tiles where the registers are there.
+    Raw rk[kAhead], rv_own[NW == 4 ? kAhead : 1];
+    Raw* const rv = NW == 4 ? rv_own : rk;
     Place next_k, next_v_own;
     Place& next_v = NW == 4 ? next_v_own : next_k;
 
@@ -718,17 +801,17 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
     // are (into `sn`), the keys after those and the next tile's values are decoded, and the ones after
     // them loaded.  One barrier a tile: K(i + 2) goes where K(i) was, V(i + 1) where V(i - 1) was, both
     // read by every wavefront before the last barrier.
-    auto step = [&](v16f (&s)[2], v16f (&sn)[2], auto odd, auto final, int32_t i) {
+    auto step = [&](v16f (&s)[kHalves], v16f (&sn)[kHalves], auto odd, auto final, int32_t i) {
       constexpr int B = decltype(odd)::value;
       constexpr bool LAST = decltype(final)::value;
       const int32_t t0 = w.t_begin + i * kTok;
       if (t0 + kTok > w.full_hi || t0 < w.full_lo) {
-        mask<TREE>(s[0], p, w, row, t0);
-        mask<TREE>(s[1], p, w, row, t0 + 32);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) mask<TREE>(s[h], p, w, row, t0 + (half + h) * 32);
       }
       float top = s[0][0];
 #pragma unroll
-      for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
+      for (int e = 1; e < 16 * kHalves; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
       top = max_halves(top) * p.scale_log2;
       float scale = p.scale_log2;
       if (__any(top > m + slack)) {
@@ -743,56 +826,67 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
         slack = kSlack;
         if (large_scores(now)) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e >> 4][e & 15] = rounded_product(s[e >> 4][e & 15], scale);
+          for (int e = 0; e < 16 * kHalves; ++e) s[e >> 4][e & 15] = rounded_product(s[e >> 4][e & 15], scale);
           scale = 1.f;
           slack = -kInf;
         }
       }
       const float sub = m == -kInf ? 0.f : m;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {            // 16 tokens each
+      for (int q = 0; q < 2 * kHalves; ++q) {  // 16 tokens each
         const bf16x8 pf = weights(s[q >> 1], 8 * (q & 1), scale, sub, l);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
           acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(bf16x8, vl[B][(q * DT + d) * 64 + lane]), pf, acc[d], 0, 0, 0);
+              __builtin_bit_cast(bf16x8, vl[B][((2 * half + q) * DT + d) * 64 + lane]), pf, acc[d], 0, 0, 0);
         if constexpr (!LAST)
-          scores(sn[q >> 1], kl[B ^ 1] + (q >> 1) * KS * 64, qf, (q & 1) * (KS / 2), ((q & 1) + 1) * (KS / 2));
+          scores(sn[q >> 1], kl[B ^ 1] + (half + (q >> 1)) * KS * 64, qf, (q & 1) * (KS / 2), ((q & 1) + 1) * (KS / 2));
       }
       if constexpr (!LAST) {
+        constexpr int R = kAhead == 2 ? B : 0;
         if (keys) {
-          dec.decode_keys(rk, kl[B]);
-          dec.load_keys(rk, next_k);
-          next_k = dec.place(t0 + 4 * kTok);
+          dec.decode_keys(rk[R], kl[B]);
+          dec.load_keys(rk[R], next_k);
+          next_k = dec.place(t0 + (3 + kAhead) * kTok);
         }
         if (values) {
-          dec.decode_values(rv, t0 + kTok, vl[B ^ 1]);
-          dec.load_values(rv, next_v);
-          next_v = dec.place(t0 + 3 * kTok);
+          dec.decode_values(rv[R], t0 + kTok, vl[B ^ 1]);
+          dec.load_values(rv[R], next_v);
+          next_v = dec.place(t0 + (2 + kAhead) * kTok);
         }
         lds_barrier();
       }
     };
 
     if (w.tiles > 0) {
-      v16f sa[2], sb[2];
+      v16f sa[kHalves], sb[kHalves];
       if (keys) {
-        dec.load_keys(rk, dec.place(w.t_begin));
-        dec.decode_keys(rk, kl[0]);
-        dec.load_keys(rk, dec.place(w.t_begin + kTok));
-        dec.decode_keys(rk, kl[1]);
-        dec.load_keys(rk, dec.place(w.t_begin + 2 * kTok));
-        next_k = dec.place(w.t_begin + 3 * kTok);
+        dec.load_keys(rk[0], dec.place(w.t_begin));
+        if constexpr (kAhead == 2) {
+          dec.load_keys(rk[1], dec.place(w.t_begin + kTok));
+          if constexpr (NW == 4) dec.load_first_values(rv[0], w);
+          dec.decode_keys(rk[0], kl[0]);
+          dec.load_keys(rk[0], dec.place(w.t_begin + 2 * kTok));
+          dec.decode_keys(rk[1], kl[1]);
+          dec.load_keys(rk[1], dec.place(w.t_begin + 3 * kTok));
+        } else {
+          dec.decode_keys(rk[0], kl[0]);
+          dec.load_keys(rk[0], dec.place(w.t_begin + kTok));
+          dec.decode_keys(rk[0], kl[1]);
+          dec.load_keys(rk[0], dec.place(w.t_begin + 2 * kTok));
+        }
+        next_k = dec.place(w.t_begin + (2 + kAhead) * kTok);
       }
       if (values) {
-        dec.load_first_values(rv, w);
-        dec.decode_values(rv, w.t_begin, vl[0]);
-        dec.load_values(rv, dec.place(w.t_begin + kTok));
-        next_v = dec.place(w.t_begin + 2 * kTok);
+        if (kAhead == 1 || NW == 8) dec.load_first_values(rv[0], w);
+        if constexpr (kAhead == 2) dec.load_values(rv[1], dec.place(w.t_begin + 2 * kTok));
+        dec.decode_values(rv[0], w.t_begin, vl[0]);
+        dec.load_values(rv[0], dec.place(w.t_begin + kTok));
+        next_v = dec.place(w.t_begin + (1 + kAhead) * kTok);
       }
       lds_barrier();
-      scores(sa[0], kl[0], qf, 0, KS);
-      scores(sa[1], kl[0] + KS * 64, qf, 0, KS);
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) scores(sa[h], kl[0] + (half + h) * KS * 64, qf, 0, KS);
       lds_barrier();                           // K(0) is read before K(2) overwrites it
       int32_t i = 0;
       for (; i + 2 < w.tiles; i += 2) {
@@ -808,7 +902,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
     }
     l += __shfl_xor(l, 32, 64);
 
-    finish<DT, kThreads>(p, w, row, slot, acc, m, l, 0);
+    if constexpr (SPLIT == 2) {
+      lds_barrier();                         // the last tile's values are read
+      join_pair<DT, kTiles>(half == 1, rows_of, acc, m, l, reinterpret_cast<float*>(vl), stats);
+    }
+    if (SPLIT == 1 || half == 0) finish<DT, 64 * kTiles, TREE>(p, w, row, slot, acc, m, l, 0);
     if constexpr (!DEALT) return;
     lds_barrier();                           // before the next one's keys and values
   }
@@ -823,7 +921,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const AttnProblem
 // so that each of the matrix runs has the other side's decoding beside it, and one buffer of keys,
 // values and weights is enough.
 template <bool DEALT, bool TREE>
-__global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem args, int row_blocks, int splits,
+__global__ __launch_bounds__(512, 2) void attn_wide_kernel(const ProblemOf<TREE> args, int row_blocks, int splits,
                                                            int groups) {
   constexpr int D = 256, KS = D / 16, DT = D / 32, N = DT / 2, kThreads = 512;
   __shared__ uint4 kl[2 * KS * 64];
@@ -836,7 +934,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
   const int rt = wave & 3, half = wave >> 2;
   Walk<kThreads, DEALT, TREE> walk(args, 128, row_blocks, splits, groups, first);
   for (;;) {
-    const AttnProblem p = DEALT ? argument() : args;
+    const ProblemOf<TREE> p = DEALT ? argument<TREE>() : args;
     Work w;
     int slot;
     if (!walk.next(p, 128, row_blocks, splits, first, &w, &slot)) return;
@@ -960,15 +1058,16 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const AttnProblem arg
     l += tops[0][rt][half ^ 1][c];
 
     // The row's numbers are worked out again: kept through the loop, they cost it registers.
-    finish<DT, kThreads>(p, w, row_of<TREE>(p, w, rt, again(threadIdx.x)), slot, acc, m, l, half * N);
+    finish<DT, kThreads, TREE>(p, w, row_of<TREE>(p, w, rt, again(threadIdx.x)), slot, acc, m, l, half * N);
     if constexpr (!DEALT) return;
     lds_barrier();                           // before the next one's keys and values
   }
 }
 
-template <int D, int NW, bool TREE>
-hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
+template <int D, int NW, bool TREE, int SPLIT = 1>
+hipError_t launch(const ProblemOf<TREE>& p, const AttnPlan& plan, hipStream_t stream) {
   constexpr int DT = D / 32, kThreads = D == 256 ? 512 : 64 * NW, N = D == 256 ? DT / 2 : DT;
+  constexpr int kOwners = D == 256 ? 512 : kThreads / SPLIT;           // threads that a part's rows are left by
   const int64_t units = static_cast<int64_t>(plan.row_blocks) * p.batch * p.cache.heads;
   const int64_t most = std::max<int64_t>(units * plan.splits, plan.groups);
   if (most > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
@@ -982,15 +1081,18 @@ hipError_t launch(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream
     if (plan.groups) attend(attn_wide_kernel<true, TREE>);
     else attend(attn_wide_kernel<false, TREE>);
   } else {
-    if (plan.groups) attend(attn_many_kernel<D, NW, true, TREE>);
-    else attend(attn_many_kernel<D, NW, false, TREE>);
+    if (plan.groups) attend(attn_many_kernel<D, NW, true, TREE, SPLIT>);
+    else attend(attn_many_kernel<D, NW, false, TREE, SPLIT>);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (plan.splits == 1 && plan.groups == 0)) return e;
-  // At most so many units have parts: there are no more, and a run begins inside of each in a deal.
-  const int64_t joined = plan.groups ? std::min<int64_t>(units, plan.groups - 1) : units;
-  hipLaunchKernelGGL((attn_join_kernel<DT, kThreads, N, D == 256 ? 2 : 1, TREE>),
-                     dim3(static_cast<unsigned>(joined * (2 * N))), dim3(kThreads), 0, stream, p,
+  // The units; of a deal those that have parts (there are no more of them than units, and a run begins inside
+  // of each), or for a tree the runs but the first.
+  const int64_t joined = !plan.groups ? units
+                         : TREE ? std::max<int64_t>(plan.splits > 1 ? units : 0, plan.groups - 1)
+                                : std::min<int64_t>(units, plan.groups - 1);
+  hipLaunchKernelGGL((attn_join_kernel<DT, kOwners, N, D == 256 ? 2 : 1, TREE>),
+                     dim3(static_cast<unsigned>(joined * (2 * N))), dim3(kOwners), 0, stream, p,
                      plan.row_blocks, plan.splits, plan.groups);
   return hipGetLastError();
 }
@@ -1003,6 +1105,9 @@ namespace {
 // rows of 8000 keys: 71 us, 83 us with the many), 2 with heads of 256 (32 rows of 8000 keys: 45 us, 96
 // with the many).
 constexpr int few_tiles(int head_dim) { return head_dim == 256 ? 2 : 4; }
+// Of a tree, heads of 128: 2 (16 x 64 rows of 4000 to 8192 keys, 8 heads: 62 us with the many, 79 us with the
+// few; heads of 64, 32 x 64 rows of 1536 to 6144, 12 heads: 71 and 72).
+constexpr int few_tree_tiles(int head_dim) { return head_dim == 64 ? 4 : 2; }
 
 constexpr int64_t few_part_bytes(int head_dim, int row_tiles) {
   return int64_t{2} * 256 * few_waves(head_dim, row_tiles) * 16 * row_tiles * (head_dim + 2) * 4;
@@ -1013,10 +1118,10 @@ constexpr int64_t kChipThreads = 256 * 512;
 
 }  // namespace
 
-AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim) {
+AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_heads, int head_dim, bool tree) {
   AttnPlan a = {};
   const int64_t rows = max_q * (q_heads / kv_heads), units = batch * kv_heads;
-  a.few = rows <= 16 * few_tiles(head_dim);
+  a.few = rows <= 16 * (tree ? few_tree_tiles(head_dim) : few_tiles(head_dim));
   if (a.few) {
     a.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     a.groups = 256 * few_waves(head_dim, a.row_tiles);
@@ -1025,15 +1130,19 @@ AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
   }
   // Eight wavefronts of 32 rows share the decoding where there are rows for them; with heads of 256,
   // eight share 128 rows.
-  a.row_tiles = head_dim == 256 || rows <= 128 ? 4 : 8;
-  const int64_t block_rows = 32 * a.row_tiles, threads = head_dim == 256 ? 512 : 64 * a.row_tiles;
+  a.waves = head_dim == 256 || rows <= 128 ? 4 : 8;
+  a.split = 1;
+  // A tree's 33 to 64 rows: two wavefronts share 32.  (65 to 128 rows, eight wavefronts in pairs: 87 to 90 us
+  // where four with rows of their own take 83 to 89.)
+  if (tree && head_dim == 128 && rows <= 64) a.split = 2;
+  const int64_t block_rows = 32 * (a.waves / a.split), threads = head_dim == 256 ? 512 : 64 * a.waves;
   const int64_t blocks = (rows + block_rows - 1) / block_rows;
   a.row_blocks = static_cast<int>(blocks);
   const int64_t groups = kChipThreads / threads, fit = groups / (blocks * units);
   a.splits = static_cast<int>(fit < 1 ? 1 : fit > 64 ? 64 : fit);
   if (batch > 1 && blocks * units < kDealUnits * groups) a.groups = static_cast<int>(groups);
   if (a.splits > 1 || a.groups > 0)
-    a.part_bytes = 4 * (kStartFloats + (a.groups ? 2 : 1) * groups * part_floats(threads, head_dim == 64 ? 2 : 4));
+    a.part_bytes = 4 * (kStartFloats + (a.groups ? 2 : 1) * groups * part_floats(threads / a.split, head_dim == 64 ? 2 : 4));
   return a;
 }
 
@@ -1042,6 +1151,9 @@ int64_t most_part_bytes(int64_t max_q, int64_t group, int head_dim) {
   int64_t most = 0;
   for (int t = 1; t <= few_tiles(head_dim); t *= 2)
     if (t == 1 || rows > 8 * t) most = std::max(most, few_part_bytes(head_dim, t));
+  // A tree's rows go with the many from fewer on, with two wavefronts to a part's rows there.
+  if (rows > 16 * few_tree_tiles(head_dim) && rows <= 16 * few_tiles(head_dim))
+    most = std::max(most, 4 * (kStartFloats + kChipThreads * (16 * (head_dim == 64 ? 2 : 4) + 1)));
   if (rows > 16 * few_tiles(head_dim))
     most = std::max(most, 4 * (kStartFloats + 2 * kChipThreads * (16 * (head_dim == 64 ? 2 : 4) + 1)));
   return most;
@@ -1050,8 +1162,11 @@ int64_t most_part_bytes(int64_t max_q, int64_t group, int head_dim) {
 namespace {
 
 template <bool TREE>
-hipError_t launch_any(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
-  const bool eight = plan.row_tiles == 8;
+hipError_t launch_any(const ProblemOf<TREE>& p, const AttnPlan& plan, hipStream_t stream) {
+  const bool eight = plan.waves == 8;
+  if constexpr (TREE) {
+    if (plan.split == 2) return launch<128, 4, true, 2>(p, plan, stream);
+  }
   if (p.cache.head_dim == 64)
     return eight ? launch<64, 8, TREE>(p, plan, stream) : launch<64, 4, TREE>(p, plan, stream);
   if (p.cache.head_dim == 128)
@@ -1061,7 +1176,7 @@ hipError_t launch_any(const AttnProblem& p, const AttnPlan& plan, hipStream_t st
 
 }  // namespace
 
-hipError_t launch_attn_many(const AttnProblem& p, const AttnPlan& plan, hipStream_t stream) {
+hipError_t launch_attn_many(const AttnTreeProblem& p, const AttnPlan& plan, hipStream_t stream) {
   return p.tree ? launch_any<true>(p, plan, stream) : launch_any<false>(p, plan, stream);
 }
 
