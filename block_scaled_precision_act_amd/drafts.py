@@ -159,11 +159,10 @@ def mx_kv_accept_fp4(caches, page_table, seq_lens, path, count, lens_out=None, q
     fn, dev = "mx_kv_accept_fp4", _current_device()
     if isinstance(caches, MxKvCacheFp4):
         caches = (caches,)
-    packed = []
-    for c in caches:
-        if type(c) is not MxKvCacheFp4 or c.device_index != dev:
+    if any(type(c) is not MxKvCacheFp4 or c.device_index != dev for c in caches):
+        for c in caches:
             _cache(fn, c, dev)
-        packed.append(c._packed)
+    packed = [c._packed for c in caches]
     tp, stride, B, width = _table(fn, page_table, dev)
     lens = _flat(fn, seq_lens, "seq_lens", _i32, dev, (B,))
     _need(fn, path, "path", _i32, dev)
