@@ -11,6 +11,7 @@ namespace {
 using namespace mx;
 
 constexpr int64_t kMostVocab = int64_t{1} << 30;
+constexpr int64_t kMostStride = int64_t{1} << 30;      // elements: rows' addresses fit 64 bits
 constexpr int64_t kMostLayers = 1024;
 
 int nodes_status(int64_t batch, int64_t total_q, int64_t max_q, const int32_t* starts) {
@@ -27,9 +28,32 @@ Nodes nodes(int64_t batch, int64_t total_q, int64_t max_q, const int32_t* starts
 // Behind the counters, 64 sums of each sequence whose rows are cut: at most every second workgroup's.
 constexpr int64_t kVerifyWorkspace = kCounterBytes + kVerifyGroups / 2 * 64 * 8;
 
-bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
+// A buffer's address (nullptr: none) and bytes.
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+
+bool meet(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) &&
+         y < x + static_cast<uintptr_t>(a.bytes);
+}
+
+// Whether an output lies on an input or another output: workgroups read what others may have written.
+bool outputs_meet(std::initializer_list<Range> outputs, std::initializer_list<Range> inputs) {
+  for (const Range* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Range& i : inputs)
+      if (meet(*o, i)) return true;
+    for (const Range* q = outputs.begin(); q != o; ++q)
+      if (meet(*o, *q)) return true;
+  }
+  return false;
+}
+
+// Bytes of `rows` rows.
+int64_t row_bytes(int64_t rows, int64_t stride, int64_t width, int64_t unit) {
+  return rows > 0 ? ((rows - 1) * stride + width) * unit : 0;
 }
 
 }  // namespace
@@ -46,6 +70,9 @@ int mx_tree_mask(const mx_tree_mask_args* a, void* stream) {
   if (!a->parents || !a->mask || !a->seq_lens != !a->positions) return MX_ERR_NULL;
   if (!aligned(a->parents, 4) || !aligned(a->mask, 4) || !aligned(a->seq_lens, 4) || !aligned(a->positions, 4))
     return MX_ERR_ALIGN;
+  if (outputs_meet({{a->mask, row_bytes(a->total_q, a->mask_stride, a->mask_words, 4)}, {a->positions, 4 * a->total_q}},
+                   {{a->parents, 4 * a->total_q}, {a->seq_lens, 4 * a->batch}, {a->q_starts, 4 * (a->batch + 1)}}))
+    return MX_ERR_STRIDE;
   if ((st = device_status()) != MX_OK) return st;
   TreeMaskProblem p;
   p.nodes = nodes(a->batch, a->total_q, a->max_q, a->q_starts);
@@ -66,9 +93,10 @@ int mx_tree_verify(const mx_tree_verify_args* a, void* stream) {
   if (!a) return MX_ERR_NULL;
   int st = nodes_status(a->batch, a->total_q, a->max_q, a->q_starts);
   if (st != MX_OK) return st;
-  if (a->vocab < 1 || a->vocab > kMostVocab || a->width < 1 || a->width > kMax31 || a->type < 0 || a->type > 2)
+  if (a->vocab < 1 || a->vocab > kMostVocab || a->width < 1 || !fits31(a->batch, a->width) || a->type < 0 || a->type > 2)
     return MX_ERR_SHAPE;
-  if (a->target_stride < 0 || (a->total_q > 1 && a->target_stride < a->vocab) || a->draft_stride < 0 ||
+  if (a->target_stride < 0 || a->target_stride > kMostStride || a->draft_stride > kMostStride ||
+      (a->total_q > 1 && a->target_stride < a->vocab) || a->draft_stride < 0 ||
       (a->draft && a->draft_stride > 0 && a->draft_stride < a->vocab))
     return MX_ERR_STRIDE;
   if (a->batch == 0) return MX_OK;
@@ -80,6 +108,13 @@ int mx_tree_verify(const mx_tree_verify_args* a, void* stream) {
       !aligned(a->accept_u, 4) || !aligned(a->sample_u, 4) || !aligned(a->path, 4) || !aligned(a->tokens_out, 4) ||
       !aligned(a->count, 4))
     return MX_ERR_ALIGN;
+  const int64_t out = 4 * a->batch * a->width, each = 4 * a->total_q, width = unit;
+  if (outputs_meet({{a->path, out}, {a->tokens_out, out}, {a->count, 4 * a->batch}},
+                   {{a->tokens, each}, {a->parents, each}, {a->accept_u, each}, {a->sample_u, 4 * a->batch},
+                    {a->q_starts, 4 * (a->batch + 1)},
+                    {a->target, row_bytes(a->total_q, a->target_stride, a->vocab, width)},
+                    {a->draft, row_bytes(a->total_q, a->draft_stride, a->vocab, width)}}))
+    return MX_ERR_STRIDE;
   if (!a->workspace || a->workspace_bytes < kVerifyWorkspace || !aligned(a->workspace, 256))
     return MX_ERR_WORKSPACE;
   if ((st = device_status()) != MX_OK) return st;
@@ -109,7 +144,7 @@ int mx_kv_accept_fp4(const mx_kv_accept_fp4_args* a, void* stream) {
   if (!a) return MX_ERR_NULL;
   int st = nodes_status(a->batch, a->total_q, a->max_q, a->q_starts);
   if (st != MX_OK) return st;
-  if (a->layers < 0 || a->layers > kMostLayers || a->width < 0 || a->width > kMax31 || a->table_width < 0)
+  if (a->layers < 0 || a->layers > kMostLayers || a->width < 0 || !fits31(a->batch, a->width) || a->table_width < 0)
     return MX_ERR_SHAPE;
   if (a->layers == 0 || a->batch == 0) return MX_OK;
   if (!a->caches) return MX_ERR_NULL;
@@ -138,7 +173,11 @@ int mx_kv_accept_fp4(const mx_kv_accept_fp4_args* a, void* stream) {
   if (!aligned(a->seq_lens, 4) || !aligned(a->count, 4) || !aligned(a->path, 4) || !aligned(a->page_table, 4) ||
       !aligned(a->lens_out, 4))
     return MX_ERR_ALIGN;
-  if (a->lens_out && overlap(a->lens_out, 4 * a->batch, a->seq_lens, 4 * a->batch)) return MX_ERR_STRIDE;
+  if (outputs_meet({{a->lens_out, 4 * a->batch}},
+                   {{a->seq_lens, 4 * a->batch}, {a->count, 4 * a->batch}, {a->q_starts, 4 * (a->batch + 1)},
+                    {a->path, 4 * a->batch * a->width},
+                    {a->page_table, row_bytes(a->batch, a->table_stride, a->table_width, 4)}}))
+    return MX_ERR_STRIDE;
   if ((st = device_status()) != MX_OK) return st;
   KvAcceptProblem p;
   p.nodes = nodes(a->batch, a->total_q, a->max_q, a->q_starts);

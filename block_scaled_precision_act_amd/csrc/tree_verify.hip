@@ -431,7 +431,9 @@ struct Team {
   }
   // The last to leave clears what it leaves behind (nobody reads it any more).
   __device__ __forceinline__ void leave() const {
-    if (threadIdx.x != 0 || add(words + 3, 1u) + 1 != static_cast<uint32_t>(size)) return;
+    if (threadIdx.x != 0) return;
+    __builtin_amdgcn_s_waitcnt(kVmcntZero);          // what it wrote lies before what the last one clears
+    if (add(words + 3, 1u) + 1 != static_cast<uint32_t>(size)) return;
     for (int i = 1; i < 8; ++i) write(words + i, 0u);
   }
 };

@@ -18,7 +18,8 @@
  * i; a node whose parent is not in [0, i) has none.  seq_lens[b] counts the cached tokens of sequence b
  * with its nodes: node i is cached as token seq_lens[b] - n + i of n nodes, whatever its depth.
  * q_starts and seq_lens are read on the device and clamped to total_q, max_q and what a page table
- * covers.
+ * covers.  Outputs must not lie on each other, nor on inputs: MX_ERR_STRIDE (mx_attn_tree_fp4 does not look
+ * for the latter).
  */
 #ifndef MX_DRAFT_H_
 #define MX_DRAFT_H_
@@ -105,9 +106,9 @@ int mx_attn_tree_fp4(const mx_attn_tree_fp4_args* args, void* stream);
  *
  * path[b]: the accepted nodes, the root first, then -1.  tokens_out[b]: their tokens without the
  * root's, then the next token, then -1.  count[b]: the number of either, 0 for a sequence of no nodes.
- * `width` is that of both outputs; nodes deeper than width - 1 are not tried.
+ * `width` is that of both outputs, batch * width below 2^31; nodes deeper than width - 1 are not tried.
  * type: 0 fp32, 1 bf16, 2 fp16, of both matrices; row strides at least vocab (draft's 0: one row for
- * all); rows need no alignment past their type's.  max_q at most 1024, vocab in [1, 2^30].
+ * all), at most 2^30; rows need no alignment past their type's.  max_q at most 1024, vocab in [1, 2^30].
  * workspace: mx_tree_verify_workspace_size bytes, 256-byte aligned, zero before its first use and left
  * reusable; it may be one of mx_attn_fp4 that is as large.  Calls that may overlap need workspaces of
  * their own.
@@ -141,8 +142,7 @@ int64_t mx_tree_verify_workspace_size(int64_t batch);
  * rises strictly from 0 on, as mx_tree_verify writes it: then the rows are as if all were read before any
  * is written.  Entries outside [0, n), and tokens before 0 or past what the page table covers,
  * move nothing; page table entries outside [0, pages) neither.
- * lens_out (or NULL): first + count[b], at least 0: the sequences' lengths without what was rejected.  It
- * must not be seq_lens, which every layer's move reads.
+ * lens_out (or NULL): first + count[b], at least 0: the sequences' lengths without what was rejected.
  * Blocks of a cache must not lie on each other, nor those of two layers (the same cache twice is
  * refused); a page that holds nodes belongs to one sequence.  layers at most 1024.
  */

@@ -91,7 +91,7 @@ def _caches(*changes):
 
 S, N, AL, ST, W, OK = (mx.MX_ERR_SHAPE, mx.MX_ERR_NULL, mx.MX_ERR_ALIGN, mx.MX_ERR_STRIDE, mx.MX_ERR_WORKSPACE,
                        mx.MX_OK)
-MASK = dict(parents=A, seq_lens=A, mask=A, positions=A, mask_stride=2, mask_words=2, batch=2, total_q=80, max_q=40)
+MASK = dict(parents=A, seq_lens=A, mask=B, positions=2 * B, mask_stride=2, mask_words=2, batch=2, total_q=80, max_q=40)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -100,7 +100,8 @@ MASK = dict(parents=A, seq_lens=A, mask=A, positions=A, mask_stride=2, mask_word
     (dict(total_q=1 << 31, q_starts=A), S), (dict(mask_words=1), S), (dict(mask_words=-1), S), (dict(mask_words=1 << 31), S),
     (dict(mask_stride=1), ST), (dict(mask_stride=-2), ST), (dict(parents=0), N), (dict(mask=0), N),
     (dict(seq_lens=0), N), (dict(positions=0), N), (dict(parents=A + 2), AL), (dict(mask=A + 1), AL),
-    (dict(q_starts=A + 2), AL), (dict(positions=A + 2), AL), (dict(batch=0, total_q=0, parents=0), OK),
+    (dict(q_starts=A + 2), AL), (dict(positions=A + 2), AL), (dict(mask=A), ST), (dict(positions=A + 80 * 4 - 4), ST),
+    (dict(positions=B + 4), ST), (dict(positions=A + 80 * 4), "device"), (dict(batch=0, total_q=0, parents=0), OK),
     (dict(total_q=0, q_starts=A, mask=0), OK), ({}, "device"), (dict(seq_lens=0, positions=0), "device"),
     (dict(q_starts=A, max_q=64), "device")])
 def test_tree_mask(lib, change, status):
@@ -135,7 +136,7 @@ def test_attn_tree_refuses_what_a_cache_may_not_be(lib):
         assert _call(lib, "mx_attn_tree_fp4", {**ATTN, "cache": c}, {}) == status
 
 
-VERIFY = dict(target=A, draft=A, tokens=A, parents=A, accept_u=A, sample_u=A, path=A, tokens_out=A, count=A, workspace=A,
+VERIFY = dict(target=A, draft=A, tokens=A, parents=A, accept_u=A, sample_u=A, path=B, tokens_out=2 * B, count=3 * B, workspace=A,
               workspace_bytes=1 << 24, target_stride=100, draft_stride=100, batch=2, total_q=10, max_q=5, vocab=100,
               width=5)
 
@@ -146,7 +147,9 @@ VERIFY = dict(target=A, draft=A, tokens=A, parents=A, accept_u=A, sample_u=A, pa
     (dict(target_stride=99), ST), (dict(target_stride=0), ST), (dict(target_stride=-1), ST), (dict(draft_stride=99), ST),
     (dict(draft_stride=-100), ST), (dict(target=0), N), (dict(tokens=0), N), (dict(parents=0), N), (dict(accept_u=0), N),
     (dict(sample_u=0), N), (dict(path=0), N), (dict(tokens_out=0), N), (dict(count=0), N), (dict(target=A + 2), AL),
-    (dict(type=1, draft=A + 1), AL), (dict(path=A + 2), AL), (dict(accept_u=A + 1), AL), (dict(workspace=0), W),
+    (dict(type=1, draft=A + 1), AL), (dict(path=A + 2), AL), (dict(accept_u=A + 1), AL), (dict(path=A), ST), (dict(path=A + 3999), AL),
+    (dict(path=A + 3996), ST), (dict(tokens_out=B + 36), ST), (dict(tokens_out=B + 40), "device"), (dict(count=2 * B), ST),
+    (dict(target_stride=(1 << 30) + 1), ST), (dict(batch=3, total_q=15, width=1 << 30), S), (dict(workspace=0), W),
     (dict(workspace=A + 64), W), (dict(workspace_bytes=1 << 23), W), (dict(batch=0, total_q=0, path=0), OK),
     (dict(total_q=0, max_q=0, target=0, tokens=0), "device"), ({}, "device"), (dict(draft=0, draft_stride=0), "device"),
     (dict(draft_stride=0), "device"), (dict(type=2, target=A + 2, draft=A + 2), "device")])
@@ -172,8 +175,8 @@ ACCEPT = dict(page_table=A, seq_lens=A, path=A, count=A, lens_out=B, layers=2, t
                                                                                              table_stride=1 << 28), S),
     (dict(table_stride=7), ST), (dict(table_stride=-8), ST), (dict(seq_lens=0), N), (dict(count=0), N), (dict(path=0), N),
     (dict(page_table=0), N), (dict(path=A + 2), AL), (dict(lens_out=B + 1), AL), (dict(lens_out=A), ST),
-    (dict(lens_out=A + 4), ST), (dict(lens_out=A - 4), ST), (dict(layers=0, caches=0), OK), (dict(batch=0, total_q=0), OK),
-    ({}, "device"), (dict(lens_out=0), "device"), (dict(lens_out=A + 8), "device"),
+    (dict(lens_out=A + 4), ST), (dict(lens_out=A - 4), ST), (dict(lens_out=B, count=B), ST), (dict(lens_out=B, path=B - 36), ST), (dict(layers=0, caches=0), OK), (dict(batch=0, total_q=0), OK),
+    ({}, "device"), (dict(lens_out=0), "device"), (dict(lens_out=A + 64), "device"),
     (dict(table_width=0, page_table=0, table_stride=0), "device"), (dict(width=0, path=0), "device")])
 def test_accept(lib, change, status):
     keep, c = _caches({}, {})

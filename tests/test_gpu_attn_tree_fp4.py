@@ -66,6 +66,12 @@ def test_many_rows(mx, dim, n, group):
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
+def test_hundreds_of_nodes(mx, dim):
+    rng = np.random.default_rng(dim + 7)
+    compare(mx, rng, [650, 620, 700], [610, 20, 333], 1, 1, dim, 16)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("kind", ["chain", "star"])
 def test_other_shapes_of_trees(mx, dim, kind):
     rng = np.random.default_rng(dim)

@@ -264,6 +264,29 @@ def test_streams_graphs_and_an_attention_workspace(mx):
     assert not ws[:1 << 23].any()                          # the counters are zero again
 
 
+def test_calls_at_once_on_several_streams(mx):
+    # each with a workspace of its own; their workgroups share the chip, and some have to wait for others
+    rng = np.random.default_rng(25)
+    streams, calls = [torch.cuda.Stream() for _ in range(4)], []
+    for i, (sizes, V) in enumerate((([9] * 16, 30011), ([12] * 5, 60000), ([30] * 2, 100003), ([26] * 60, 5000))):
+        c = case(rng, sizes, V, "fp32", "distinct", apart=2.0)
+        dev = [c[0].cuda(), c[1].cuda(), ints(c[2]), ints(c[3]), torch.from_numpy(c[4]).cuda(),
+               torch.from_numpy(c[5]).cuda()]
+        outs = [ints(np.zeros((len(sizes), max(sizes)))) for _ in range(2)] + [ints(np.zeros(len(sizes)))]
+        want = D.verify(c[0].double().numpy(), c[1].double().numpy(), *c[2:6], c[6], max(sizes), False)
+        calls.append((dev, outs, workspace(mx, len(sizes)), want))
+    torch.cuda.synchronize()
+    note("verify on four streams")
+    for _ in range(20):
+        for (dev, outs, ws, _), st in zip(calls, streams):
+            with torch.cuda.stream(st):
+                mx.mx_tree_verify(*dev, *outs, ws, replacement=False)
+    torch.cuda.synchronize()
+    for dev, outs, ws, want in calls:
+        assert all(np.array_equal(t.cpu().numpy(), w) for t, w in zip(outs, want))
+        assert not ws[:1 << 23].any()
+
+
 def test_refusals(mx):
     t = torch.full((3, 8), 0.125, device="cuda")
     f = torch.zeros(3, device="cuda")
