@@ -654,9 +654,13 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
 template <int D, int MT>
 hipError_t launch(const AttnTreeProblem& p, const AttnPlan& plan, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(plan.groups)), block(kThreads);
-  const AttnProblem& plain = p;
-  if (p.tree) hipLaunchKernelGGL((attn_few_kernel<D, MT, true>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((attn_few_kernel<D, MT, false>), grid, block, 0, stream, plain);
+  if (p.tree) {
+    if constexpr (MT <= few_tree_tiles(D)) hipLaunchKernelGGL((attn_few_kernel<D, MT, true>), grid, block, 0, stream, p);
+    else return hipErrorInvalidValue;
+  } else {
+    const AttnProblem& plain = p;
+    hipLaunchKernelGGL((attn_few_kernel<D, MT, false>), grid, block, 0, stream, plain);
+  }
   return hipGetLastError();
 }
 

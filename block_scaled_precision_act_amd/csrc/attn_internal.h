@@ -128,6 +128,17 @@ struct AttnPlan {
 constexpr int few_waves(int head_dim, int row_tiles) {
   return head_dim * row_tiles <= 128 ? 3 : head_dim * row_tiles <= 256 ? 2 : 1;
 }
+// Tiles of 16 rows up to which a sequence and head goes with the few: 4 with heads of 64 and 128 (64
+// rows of 8000 keys: 71 us, 83 us with the many), 2 with heads of 256 (32 rows of 8000 keys: 45 us, 96
+// with the many).
+constexpr int few_tiles(int head_dim) { return head_dim == 256 ? 2 : 4; }
+// Of a tree, heads of 128: 2 (16 x 64 rows of 4000 to 8192 keys, 8 heads: 62 us with the many, 79 us with the
+// few; heads of 64, 32 x 64 rows of 1536 to 6144, 12 heads: 71 and 72).  Heads of 256: 1 (32 rows of 2 heads: 2000
+// keys 18 and 25 us, 100000 70 and 90, 4 x 20000 to 32768 49 and 64; 16 rows of the latter 49 and 40).
+constexpr int few_tree_tiles(int head_dim) { return head_dim == 64 ? 4 : head_dim == 128 ? 2 : 1; }
+static_assert(few_tree_tiles(64) <= few_tiles(64) && few_tree_tiles(128) <= few_tiles(128) &&
+                  few_tree_tiles(256) <= few_tiles(256),
+              "the workspace of a tree's parts covers theirs");
 // A deal among many rows (attn_many.hip) is looked at where a part of a unit may have more tiles of 64
 // tokens.
 constexpr int64_t kLeastDealTiles = 32;

@@ -1101,14 +1101,6 @@ hipError_t launch(const ProblemOf<TREE>& p, const AttnPlan& plan, hipStream_t st
 
 namespace {
 
-// Tiles of 16 rows up to which a sequence and head goes with the few: 4 with heads of 64 and 128 (64
-// rows of 8000 keys: 71 us, 83 us with the many), 2 with heads of 256 (32 rows of 8000 keys: 45 us, 96
-// with the many).
-constexpr int few_tiles(int head_dim) { return head_dim == 256 ? 2 : 4; }
-// Of a tree, heads of 128: 2 (16 x 64 rows of 4000 to 8192 keys, 8 heads: 62 us with the many, 79 us with the
-// few; heads of 64, 32 x 64 rows of 1536 to 6144, 12 heads: 71 and 72).
-constexpr int few_tree_tiles(int head_dim) { return head_dim == 64 ? 4 : 2; }
-
 constexpr int64_t few_part_bytes(int head_dim, int row_tiles) {
   return int64_t{2} * 256 * few_waves(head_dim, row_tiles) * 16 * row_tiles * (head_dim + 2) * 4;
 }
@@ -1151,11 +1143,10 @@ int64_t most_part_bytes(int64_t max_q, int64_t group, int head_dim) {
   int64_t most = 0;
   for (int t = 1; t <= few_tiles(head_dim); t *= 2)
     if (t == 1 || rows > 8 * t) most = std::max(most, few_part_bytes(head_dim, t));
-  // A tree's rows go with the many from fewer on, with two wavefronts to a part's rows there.
-  if (rows > 16 * few_tree_tiles(head_dim) && rows <= 16 * few_tiles(head_dim))
-    most = std::max(most, 4 * (kStartFloats + kChipThreads * (16 * (head_dim == 64 ? 2 : 4) + 1)));
-  if (rows > 16 * few_tiles(head_dim))
-    most = std::max(most, 4 * (kStartFloats + 2 * kChipThreads * (16 * (head_dim == 64 ? 2 : 4) + 1)));
+  // A tree's rows go with the many from fewer on than others do; pairs of wavefronts leave half of the parts.
+  if (rows > 16 * few_tree_tiles(head_dim))
+    most = std::max(most, 4 * (kStartFloats + (head_dim == 128 && rows <= 64 ? 1 : 2) * kChipThreads *
+                                                  (16 * (head_dim == 64 ? 2 : 4) + 1)));
   return most;
 }
 
