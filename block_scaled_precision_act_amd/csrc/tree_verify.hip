@@ -6,15 +6,20 @@
 // distribution r / S after a token of q / Q was rejected is max(r / S - q / Q, 0) = max(p - (c + S / Q) q,
 // 0) / S: its shape is kept in the one number c, and no row is ever written.)
 //
-// Bound by latency and by one pass over a row of p and one of q.  All that the tests need of the rows is
-// p(x) and q(x) of every child, loaded at once into LDS; then the walk costs no memory access until
-// the first sum.  For that one the rows are cut into slices, a workgroup each, which all take the same
-// walk to find out what to sum; the last to arrive has S and goes on alone: what remains for a chain is to
-// find the token within one slice.  A tree may need more sums, which that workgroup takes by itself: a
-// wait for other workgroups would need all of them resident.
+// Bound by latency, and by the sums: each is a pass over a row of p and one of q.  All that the tests need of
+// the rows is p(x) and q(x) of every child, loaded at once into LDS; then the walk costs no memory access until
+// the first sum.  For that one a row is cut into parts, a workgroup each, which all take the same walk to find
+// out what to sum; the last to arrive has S.  A chain is done then but for finding the token within one
+// 64th of its row.  A tree may need more sums: the same workgroups take parts of them (Team), as one CU reads
+// no more than 67 GB/s (100003 fp32 of both rows: 12 us by itself, 6.8 us so).
 //
-// In 64 bits, each product and sum rounded by itself: a token is decided by where a random number falls
-// between sums of up to 2^30 terms, and 32 bits would misplace it once in some hundred tokens.
+// Measured, whole calls in a graph: a chain of 4 over 32000 fp32, 9.6 us: launch 2, the children's
+// probabilities 1, walk 1.3, sum 2.5, arrival 1, the token 2.2.  16 trees of 26 nodes over 100003: 31 us, the
+// slowest of them four sums.  41 trees of 64 chosen drafts over 131072 bf16: 13 us.  Most of the code runs
+// once a call, and fetching it is much of that: loops stay rolled where unrolling would not feed more loads.
+//
+// In 64 bits: a token is decided by where a random number falls between sums of up to 2^30 terms, and 32 bits
+// would misplace it once in some hundred tokens.
 #include "draft_common.h"
 
 #include <type_traits>

@@ -101,8 +101,8 @@ int mx_attn_tree_fp4(const mx_attn_tree_fp4_args* args, void* stream);
  *
  * Entries that are negative, infinite or NaN count as 0, tokens outside [0, vocab) have probability 0.
  * Random numbers are meant to lie in [0, 1).  Probabilities are read in their type and computed with
- * in 64 bits, each product and sum rounded by itself; the order of the sums does not depend on
- * what else runs, so the same call gives the same tokens.
+ * in 64 bits; the order of the sums does not depend on what else runs, so the same call gives the same
+ * tokens.
  *
  * path[b]: the accepted nodes, the root first, then -1.  tokens_out[b]: their tokens without the
  * root's, then the next token, then -1.  count[b]: the number of either, 0 for a sequence of no nodes.
