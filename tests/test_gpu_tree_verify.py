@@ -122,6 +122,31 @@ def test_large_vocabularies_in_slices(mx, dtype, V, mode):
         compare(mx, c, 11, 11, mode, ws=ws)
 
 
+@pytest.mark.parametrize("mode", ["drawn", "distinct", "chosen"])
+def test_batches_whose_rows_are_not_cut(mx, mode):
+    rng = np.random.default_rng(31)
+    sizes = rng.integers(1, 6, 140).tolist()
+    c = case(rng, sizes, 20011, "bf16", mode, apart=2.0)
+    note(f"verify {mode} 140 sequences, whole rows")
+    compare(mx, c, 5, 5, mode)
+
+
+@pytest.mark.parametrize("dtype,least", [("fp32", 2.0 ** -149), ("bf16", 2.0 ** -133), ("fp16", 2.0 ** -24)])
+def test_the_smallest_probabilities(mx, dtype, least):
+    # rows of subnormal numbers alone: their sums are exact, and multiples of the smallest one
+    rng = np.random.default_rng(32)
+    V, n = 5003, 64
+    k = rng.integers(0, 8, (n, V))
+    t = torch.from_numpy(k * least).to(TYPES[dtype])
+    assert (t.double() == torch.from_numpy(k * least)).all()
+    s = (rng.integers(0, 1 << 10, n) / 1024).astype(np.float32)
+    upto = k.cumsum(-1)
+    want = [int(np.nonzero(upto[i] > float(s[i]) * upto[i, -1])[0][0]) for i in range(n)]
+    note(f"verify subnormal {dtype}")
+    got = run(mx, t.cuda(), None, np.zeros(n), -np.ones(n), np.zeros(n, np.float32), s, list(range(n + 1)), 1, 1)
+    assert got[1][:, 0].tolist() == want
+
+
 def test_where_the_next_token_falls(mx):
     # 2^12 equal probabilities: every sum is exact, the number 2^-12 k falls on a border
     V = 4096
