@@ -28,7 +28,7 @@
 // TREE: the queries are a tree's nodes, and a mask says which of the sequence's last tokens each sees; its words
 // are read where a step reaches those tokens.  32 sequences, 12 heads of 64, 26 nodes, a window of 4096: 41 us
 // (vector instructions 64% of the cycles, loads waited for in 41% of a wavefront's); 8 nodes of 32 heads of 128
-// on 8 behind 1000 tokens: 14 us, latency.
+// on 8 behind 1000 tokens: 12.6 us, latency.
 #include "attn_common.h"
 
 namespace mx {
@@ -144,8 +144,11 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
   constexpr int KS = D / 32;               // k steps of a score product
   constexpr int EPL = D / 16;              // head values a lane decodes of a token's value row
   constexpr int PAD = D + 4;
-  __shared__ float obuf[kWaves][16][PAD];
-  __shared__ float mbuf[kWaves][16], lbuf[kWaves][16];
+  // 16-row tiles that are joined at once: two of a tree (32 rows of 1000 tokens: 12.6
+  // us, 14.2 one after the other).
+  constexpr int G = TREE && MT > 1 ? 2 : 1;
+  __shared__ float obuf[G][kWaves][16][PAD];
+  __shared__ float mbuf[G][kWaves][16], lbuf[G][kWaves][16];
   __shared__ uint32_t scan[2 * kWaves + 2];
   __shared__ uint32_t flag;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -533,47 +536,57 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
             ll == 0.f ? -kInf : (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f;
     };
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt * 16 >= sq.rows) break;
-      float ls = l[mt];
-      ls += __shfl_xor(ls, 16, 64);
-      ls += __shfl_xor(ls, 32, 64);
-      if (g == 0) {
-        mbuf[wave][c] = m[mt];
-        lbuf[wave][c] = ls;
+    for (int mt0 = 0; mt0 < MT; mt0 += G) {
+      if (mt0 * 16 >= sq.rows) break;
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        float ls = l[mt0 + k];
+        ls += __shfl_xor(ls, 16, 64);
+        ls += __shfl_xor(ls, 32, 64);
+        if (g == 0) {
+          mbuf[k][wave][c] = m[mt0 + k];
+          lbuf[k][wave][c] = ls;
+        }
       }
       __syncthreads();
-      const float mall = fmaxf(fmaxf(mbuf[0][c], mbuf[1][c]), fmaxf(mbuf[2][c], mbuf[3][c]));
-      const float f = weight_of(m[mt], mall);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int k = 0; k < G; ++k) {
+        const int mt = mt0 + k;
+        const float mall = fmaxf(fmaxf(mbuf[k][0][c], mbuf[k][1][c]), fmaxf(mbuf[k][2][c], mbuf[k][3][c]));
+        const float f = weight_of(m[mt], mall);
 #pragma unroll
-        for (int e = 0; e < EPL; e += 4)
-          *reinterpret_cast<float4*>(&obuf[wave][c][value_of<D>(g * 4 + i) + e]) =
-              make_float4(acc[mt][e][i] * f, acc[mt][e + 1][i] * f, acc[mt][e + 2][i] * f,
-                          acc[mt][e + 3][i] * f);
-      __syncthreads();
-      const int r = mt * 16 + orow;
-      float o[EPL], mm = -kInf, ll = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, mbuf[w][orow]);
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w)
-        ll += lbuf[w][orow] * weight_of(mbuf[w][orow], mm);
-#pragma unroll
-      for (int e = 0; e < EPL; ++e)
-        o[e] = (obuf[0][orow][od + e] + obuf[1][orow][od + e]) +
-               (obuf[2][orow][od + e] + obuf[3][orow][od + e]);
-      if (r < sq.rows) {
-        if (whole) {
-          write_row(r, o, mm, ll);
-        } else {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < EPL; e += 4)
-            store_shared4(part + r * D + od + e, o[e], o[e + 1], o[e + 2], o[e + 3]);
-          if ((tid & 15) == 0) {
-            store_shared(part + RB * D + r, mm);
-            store_shared(part + RB * D + RB + r, ll);
+            *reinterpret_cast<float4*>(&obuf[k][wave][c][value_of<D>(g * 4 + i) + e]) =
+                make_float4(acc[mt][e][i] * f, acc[mt][e + 1][i] * f, acc[mt][e + 2][i] * f,
+                            acc[mt][e + 3][i] * f);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        const int r = (mt0 + k) * 16 + orow;
+        float o[EPL], mm = -kInf, ll = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, mbuf[k][w][orow]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+          ll += lbuf[k][w][orow] * weight_of(mbuf[k][w][orow], mm);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e)
+          o[e] = (obuf[k][0][orow][od + e] + obuf[k][1][orow][od + e]) +
+                 (obuf[k][2][orow][od + e] + obuf[k][3][orow][od + e]);
+        if (r < sq.rows) {
+          if (whole) {
+            write_row(r, o, mm, ll);
+          } else {
+#pragma unroll
+            for (int e = 0; e < EPL; e += 4)
+              store_shared4(part + r * D + od + e, o[e], o[e + 1], o[e + 2], o[e + 3]);
+            if ((tid & 15) == 0) {
+              store_shared(part + RB * D + r, mm);
+              store_shared(part + RB * D + RB + r, ll);
+            }
           }
         }
       }
@@ -583,74 +596,138 @@ __global__ __launch_bounds__(kThreads, (few_waves(D, MT))) void attn_few_kernel(
     // rows, and the parts by turns where rows leave lots over; the lots of a row are then joined.
     if (!whole && arrive_last(p.counters + (static_cast<int64_t>(b) * heads + h) * p.counter_stride, wg1 - wg0 + 1, &flag)) {
       const int lot = tid >> 4;
-      for (int mt = 0; mt < MT && mt * 16 < sq.rows; ++mt) {
-        const int live = min(16, sq.rows - mt * 16), turns = 16 / live;
-        const int turn = lot / live, r = mt * 16 + lot - turn * live;
-        float o[EPL], mm = -kInf, ll = 0.f;
+      if constexpr (G > 1) {
+        // Two of a tree's tiles at once, a row of each a lot.
+        constexpr int kBatch = 8;
+        for (int mt0 = 0; mt0 < MT && mt0 * 16 < sq.rows; mt0 += G) {
+          float o[G][EPL], mm[G], ll[G];
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-        if (turn < turns) {
-          constexpr int kBatch = D == 256 ? 4 : 8;
-          for (uint32_t w0 = wg0 + turn; w0 <= wg1; w0 += kBatch * turns) {
-            float pm[kBatch], pl[kBatch];
-            float4 v[kBatch][EPL / 4];
+          for (int k = 0; k < G; ++k) {
+            mm[k] = -kInf;
+            ll[k] = 0.f;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {     // past the last part: that part, with no weight
-              const uint32_t w = min(w0 + i * turns, wg1);
+            for (int e = 0; e < EPL; ++e) o[k][e] = 0.f;
+          }
+#pragma unroll 1
+          for (uint32_t w0 = wg0; w0 <= wg1; w0 += kBatch) {
+            float pm[G][kBatch], pl[G][kBatch];
+            float4 v[G][kBatch][EPL / 4];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {       // past the last part: that part, with no weight
+              const uint32_t w = min(w0 + i, wg1);
               const float* src = p.parts + (2 * static_cast<int64_t>(w) + (w == wg0)) * kPart;
-              pm[i] = src[RB * D + r];
-              pl[i] = src[RB * D + RB + r];
 #pragma unroll
-              for (int e = 0; e < EPL / 4; ++e) v[i][e] = *reinterpret_cast<const float4*>(src + r * D + od + 4 * e);
+              for (int k = 0; k < G; ++k) {          // past the last row: that row, not written
+                const int r = min((mt0 + k) * 16 + lot, sq.rows - 1);
+                pm[k][i] = src[RB * D + r];
+                pl[k][i] = src[RB * D + RB + r];
+#pragma unroll
+                for (int e = 0; e < EPL / 4; ++e)
+                  v[k][i][e] = *reinterpret_cast<const float4*>(src + r * D + od + 4 * e);
+              }
             }
-            float now = mm;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              if (w0 + i * turns > wg1) pm[i] = -kInf;
-              now = fmaxf(now, pm[i]);
-            }
-            const float fo = weight_of(mm, now);
-            mm = now;
-            ll *= fo;
+            for (int k = 0; k < G; ++k) {
+              float now = mm[k];
 #pragma unroll
-            for (int e = 0; e < EPL; ++e) o[e] *= fo;
+              for (int i = 0; i < kBatch; ++i) {
+                if (w0 + i > wg1) pm[k][i] = -kInf;
+                now = fmaxf(now, pm[k][i]);
+              }
+              const float fo = weight_of(mm[k], now);
+              mm[k] = now;
+              ll[k] *= fo;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              if (w0 + i * turns > wg1) break;
-              const float f = weight_of(pm[i], now);
-              ll += pl[i] * f;
+              for (int e = 0; e < EPL; ++e) o[k][e] *= fo;
 #pragma unroll
-              for (int e = 0; e < EPL / 4; ++e) {
-                o[4 * e] += v[i][e].x * f;
-                o[4 * e + 1] += v[i][e].y * f;
-                o[4 * e + 2] += v[i][e].z * f;
-                o[4 * e + 3] += v[i][e].w * f;
+              for (int i = 0; i < kBatch; ++i) {
+                if (w0 + i > wg1) break;
+                const float f = weight_of(pm[k][i], now);
+                ll[k] += pl[k][i] * f;
+#pragma unroll
+                for (int e = 0; e < EPL / 4; ++e) {
+                  o[k][4 * e] += v[k][i][e].x * f;
+                  o[k][4 * e + 1] += v[k][i][e].y * f;
+                  o[k][4 * e + 2] += v[k][i][e].z * f;
+                  o[k][4 * e + 3] += v[k][i][e].w * f;
+                }
               }
             }
           }
+#pragma unroll
+          for (int k = 0; k < G; ++k)
+            if ((mt0 + k) * 16 + lot < sq.rows) write_row((mt0 + k) * 16 + lot, o[k], mm[k], ll[k]);
         }
-        if (turns > 1) {
+      } else {
+        for (int mt = 0; mt < MT && mt * 16 < sq.rows; ++mt) {
+          const int live = min(16, sq.rows - mt * 16), turns = 16 / live;
+          const int turn = lot / live, r = mt * 16 + lot - turn * live;
+          float o[EPL], mm = -kInf, ll = 0.f;
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) obuf[0][lot][od + e] = o[e];
-          if ((tid & 15) == 0) {
-            mbuf[0][lot] = mm;
-            lbuf[0][lot] = ll;
-          }
-          __syncthreads();
-          if (turn == 0) {
-            for (int i = 1; i < turns; ++i) {
-              const int other = lot + i * live;
-              const float pm = mbuf[0][other], now = fmaxf(mm, pm);
-              const float fo = weight_of(mm, now), fn = weight_of(pm, now);
+          for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+          if (turn < turns) {
+            constexpr int kBatch = D == 256 ? 4 : 8;
+            for (uint32_t w0 = wg0 + turn; w0 <= wg1; w0 += kBatch * turns) {
+              float pm[kBatch], pl[kBatch];
+              float4 v[kBatch][EPL / 4];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {     // past the last part: that part, with no weight
+                const uint32_t w = min(w0 + i * turns, wg1);
+                const float* src = p.parts + (2 * static_cast<int64_t>(w) + (w == wg0)) * kPart;
+                pm[i] = src[RB * D + r];
+                pl[i] = src[RB * D + RB + r];
+#pragma unroll
+                for (int e = 0; e < EPL / 4; ++e) v[i][e] = *reinterpret_cast<const float4*>(src + r * D + od + 4 * e);
+              }
+              float now = mm;
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                if (w0 + i * turns > wg1) pm[i] = -kInf;
+                now = fmaxf(now, pm[i]);
+              }
+              const float fo = weight_of(mm, now);
               mm = now;
-              ll = ll * fo + lbuf[0][other] * fn;
+              ll *= fo;
 #pragma unroll
-              for (int e = 0; e < EPL; ++e) o[e] = o[e] * fo + obuf[0][other][od + e] * fn;
+              for (int e = 0; e < EPL; ++e) o[e] *= fo;
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                if (w0 + i * turns > wg1) break;
+                const float f = weight_of(pm[i], now);
+                ll += pl[i] * f;
+#pragma unroll
+                for (int e = 0; e < EPL / 4; ++e) {
+                  o[4 * e] += v[i][e].x * f;
+                  o[4 * e + 1] += v[i][e].y * f;
+                  o[4 * e + 2] += v[i][e].z * f;
+                  o[4 * e + 3] += v[i][e].w * f;
+                }
+              }
             }
           }
+          if (turns > 1) {
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) obuf[0][0][lot][od + e] = o[e];
+            if ((tid & 15) == 0) {
+              mbuf[0][0][lot] = mm;
+              lbuf[0][0][lot] = ll;
+            }
+            __syncthreads();
+            if (turn == 0) {
+              for (int i = 1; i < turns; ++i) {
+                const int other = lot + i * live;
+                const float pm = mbuf[0][0][other], now = fmaxf(mm, pm);
+                const float fo = weight_of(mm, now), fn = weight_of(pm, now);
+                mm = now;
+                ll = ll * fo + lbuf[0][0][other] * fn;
+#pragma unroll
+                for (int e = 0; e < EPL; ++e) o[e] = o[e] * fo + obuf[0][0][other][od + e] * fn;
+              }
+            }
+          }
+          if (turn == 0) write_row(r, o, mm, ll);
+          __syncthreads();
         }
-        if (turn == 0) write_row(r, o, mm, ll);
-        __syncthreads();
       }
     }
   }

@@ -99,7 +99,7 @@ struct AttnTreeProblem : AttnProblem {
 };
 
 // Tokens past a sequence's length that the kernels' token numbers may reach (the rounding to a tile, and
-// the next tiles' places, looked up before it is known whether they are needed): 384 at most.
+// the next tiles' places, looked up before it is known whether they are needed): 128 and 256 at most.
 constexpr int64_t kLookAhead = 1024;
 
 // A workspace begins with the arrival counters of few rows, one per (sequence, key/value head), zero

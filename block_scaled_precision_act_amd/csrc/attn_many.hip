@@ -770,7 +770,6 @@ template <int D, int NW, bool DEALT, bool TREE, int SPLIT>
 __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const ProblemOf<TREE> args, int row_blocks,
                                                                int splits, int groups) {
   constexpr int KS = D / 16, DT = D / 32, kThreads = 64 * NW;
-  constexpr int kAhead = SPLIT;            // tiles whose codes are loaded before they are decoded
   constexpr int kTiles = NW / SPLIT, kHalves = 2 / SPLIT;     // of rows; of a tile's tokens, a wavefront's
   __shared__ uint4 kl[2][2 * KS * 64];
   __shared__ uint4 vl[2][4 * DT * 64];
@@ -796,9 +795,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const ProblemOf<T
     float slack = kSlack;                    // what a row's maximum may rise by before it is moved
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] = v16f(0.f);
-    // A wavefront that decodes one of the two holds one share; of two tiles where the registers are there.
-    Raw rk[kAhead], rv_own[NW == 4 ? kAhead : 1];
-    Raw* const rv = NW == 4 ? rv_own : rk;
+    // A wavefront that decodes one of the two holds one share.
+    Raw rk, rv_own;
+    Raw& rv = NW == 4 ? rv_own : rk;
     Place next_k, next_v_own;
     Place& next_v = NW == 4 ? next_v_own : next_k;
 
@@ -848,16 +847,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const ProblemOf<T
           scores(sn[q >> 1], kl[B ^ 1] + (half + (q >> 1)) * KS * 64, qf, (q & 1) * (KS / 2), ((q & 1) + 1) * (KS / 2));
       }
       if constexpr (!LAST) {
-        constexpr int R = kAhead == 2 ? B : 0;
         if (keys) {
-          dec.decode_keys(rk[R], kl[B]);
-          dec.load_keys(rk[R], next_k);
-          next_k = dec.place(t0 + (3 + kAhead) * kTok);
+          dec.decode_keys(rk, kl[B]);
+          dec.load_keys(rk, next_k);
+          next_k = dec.place(t0 + 4 * kTok);
         }
         if (values) {
-          dec.decode_values(rv[R], t0 + kTok, vl[B ^ 1]);
-          dec.load_values(rv[R], next_v);
-          next_v = dec.place(t0 + (2 + kAhead) * kTok);
+          dec.decode_values(rv, t0 + kTok, vl[B ^ 1]);
+          dec.load_values(rv, next_v);
+          next_v = dec.place(t0 + 3 * kTok);
         }
         lds_barrier();
       }
@@ -866,28 +864,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const ProblemOf<T
     if (w.tiles > 0) {
       v16f sa[kHalves], sb[kHalves];
       if (keys) {
-        dec.load_keys(rk[0], dec.place(w.t_begin));
-        if constexpr (kAhead == 2) {
-          dec.load_keys(rk[1], dec.place(w.t_begin + kTok));
-          if constexpr (NW == 4) dec.load_first_values(rv[0], w);
-          dec.decode_keys(rk[0], kl[0]);
-          dec.load_keys(rk[0], dec.place(w.t_begin + 2 * kTok));
-          dec.decode_keys(rk[1], kl[1]);
-          dec.load_keys(rk[1], dec.place(w.t_begin + 3 * kTok));
-        } else {
-          dec.decode_keys(rk[0], kl[0]);
-          dec.load_keys(rk[0], dec.place(w.t_begin + kTok));
-          dec.decode_keys(rk[0], kl[1]);
-          dec.load_keys(rk[0], dec.place(w.t_begin + 2 * kTok));
-        }
-        next_k = dec.place(w.t_begin + (2 + kAhead) * kTok);
+        dec.load_keys(rk, dec.place(w.t_begin));
+        dec.decode_keys(rk, kl[0]);
+        dec.load_keys(rk, dec.place(w.t_begin + kTok));
+        dec.decode_keys(rk, kl[1]);
+        dec.load_keys(rk, dec.place(w.t_begin + 2 * kTok));
+        next_k = dec.place(w.t_begin + 3 * kTok);
       }
       if (values) {
-        if (kAhead == 1 || NW == 8) dec.load_first_values(rv[0], w);
-        if constexpr (kAhead == 2) dec.load_values(rv[1], dec.place(w.t_begin + 2 * kTok));
-        dec.decode_values(rv[0], w.t_begin, vl[0]);
-        dec.load_values(rv[0], dec.place(w.t_begin + kTok));
-        next_v = dec.place(w.t_begin + (1 + kAhead) * kTok);
+        dec.load_first_values(rv, w);
+        dec.decode_values(rv, w.t_begin, vl[0]);
+        dec.load_values(rv, dec.place(w.t_begin + kTok));
+        next_v = dec.place(w.t_begin + 2 * kTok);
       }
       lds_barrier();
 #pragma unroll
