@@ -108,15 +108,16 @@ def _workspace(fn: str, ws, dev: int):
 
 def _table(fn: str, page_table, dev: int):
     """Pointer and row stride of a page table, sequences, pages of a sequence."""
-    _need(fn, page_table, "page_table", _i32, dev)
+    if isinstance(page_table, _Tensor) and page_table.dtype is _i32 and page_table.get_device() == dev >= 0:
+        sh, st = page_table.shape, page_table.stride()
+        if len(sh) == 2 and (st[1] == 1 or sh[1] <= 1):
+            return page_table.data_ptr(), st[0] if sh[0] > 1 else sh[1], *sh
+    _need(fn, page_table, "page_table", _i32, dev)            # what is wrong with it
     if page_table.dim() != 2:
         raise MxError(fn, MX_ERR_SHAPE, f"page_table has shape {tuple(page_table.shape)}, expected "
                                         "[batch, pages of a sequence]")
-    B, width = page_table.shape
-    if width > 1 and page_table.stride(1) != 1:
-        raise MxError(fn, MX_ERR_STRIDE, f"page_table's rows are not contiguous "
-                                         f"({page_table.stride()})")
-    return page_table.data_ptr(), page_table.stride(0) if B > 1 else width, B, width
+    raise MxError(fn, MX_ERR_STRIDE, f"page_table's rows are not contiguous "
+                                     f"({page_table.stride()})")
 
 
 def _starts(fn: str, q_starts, max_q, rows: int, B: int, dev: int):

@@ -28,7 +28,10 @@ _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 def _nodes(fn: str, t, what: str, dtype, dev: int):
     """Pointer and length of a contiguous tensor [nodes]."""
-    _need(fn, t, what, dtype, dev)
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 and t.dim() == 1 and \
+            t.is_contiguous():
+        return t.data_ptr(), t.numel()
+    _need(fn, t, what, dtype, dev)                # what is wrong with it
     if t.dim() != 1:
         raise MxError(fn, MX_ERR_SHAPE, f"{what} has shape {tuple(t.shape)}, expected [nodes]")
     return _flat(fn, t, what, dtype, dev, t.shape), t.shape[0]
@@ -47,13 +50,36 @@ def _batch(fn: str, q_starts, max_q, nodes: int):
 
 def _mask(fn: str, mask, nodes: int, dev: int):
     """Pointer, row stride and words of a mask [nodes, words]."""
-    _need(fn, mask, "mask", _i32, dev)
+    if isinstance(mask, _Tensor) and mask.dtype is _i32 and mask.get_device() == dev >= 0:
+        sh, st = mask.shape, mask.stride()
+        if len(sh) == 2 and sh[0] == nodes and (st[1] == 1 or sh[1] <= 1):
+            return mask.data_ptr(), st[0] if nodes > 1 else sh[1], sh[1]
+    _need(fn, mask, "mask", _i32, dev)            # what is wrong with it
     if mask.dim() != 2 or mask.shape[0] != nodes:
         raise MxError(fn, MX_ERR_SHAPE, f"mask has shape {tuple(mask.shape)}, expected [{nodes}, words]")
-    words = mask.shape[1]
-    if words > 1 and mask.stride(1) != 1:
-        raise MxError(fn, MX_ERR_STRIDE, f"mask's rows are not contiguous ({mask.stride()})")
-    return mask.data_ptr(), mask.stride(0) if nodes > 1 else words, words
+    raise MxError(fn, MX_ERR_STRIDE, f"mask's rows are not contiguous ({mask.stride()})")
+
+
+def _rows(fn: str, t, what: str, dtype, dev: int, shape=None):
+    """Pointer and row stride of probabilities [nodes, vocab]."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev >= 0:
+        sh, st = t.shape, t.stride()
+        if len(sh) == 2 and (shape is None or sh == shape) and (st[1] == 1 or sh[1] <= 1):
+            return t.data_ptr(), st[0] if sh[0] > 1 else sh[1]
+    _need(fn, t, what, dtype, dev)                # what is wrong with it
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        want = "[nodes, vocab]" if shape is None else list(shape)
+        raise MxError(fn, MX_ERR_SHAPE, f"{what} has shape {tuple(t.shape)}, expected {want}")
+    raise MxError(fn, MX_ERR_STRIDE, f"{what}'s rows are not contiguous ({t.stride()})")
+
+
+def _path(fn: str, path, B: int, dev: int):
+    """Pointer and shape of a path [batch, width]."""
+    if not isinstance(path, _Tensor) or path.dim() != 2 or path.shape[0] != B:
+        _need(fn, path, "path", _i32, dev)
+        raise MxError(fn, MX_ERR_SHAPE, f"path has shape {tuple(path.shape)}, expected [{B}, width]")
+    sh = path.shape
+    return _flat(fn, path, "path", _i32, dev, sh), sh
 
 
 def mx_tree_mask(parents, mask, seq_lens=None, positions=None, q_starts=None, max_q=None, stream=None):
@@ -116,33 +142,23 @@ def mx_tree_verify(target, draft, tokens, parents, accept_u, sample_u, path, tok
     fn, dev = "mx_tree_verify", _current_device()
     if not isinstance(target, _Tensor) or target.dtype not in _TYPES:
         raise TypeError(f"{fn}: target must be a torch tensor of fp32, bf16 or fp16")
-    rows = []
-    for t, what in ((target, "target"), (draft, "draft")):
-        if t is None and what == "draft":
-            rows += [0, 0]
-            continue
-        _need(fn, t, what, target.dtype, dev)
-        if t.dim() != 2 or t.shape != target.shape:
-            raise MxError(fn, MX_ERR_SHAPE, f"{what} has shape {tuple(t.shape)}, expected "
-                                            f"{list(target.shape) if t is not target else '[nodes, vocab]'}")
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise MxError(fn, MX_ERR_STRIDE, f"{what}'s rows are not contiguous ({t.stride()})")
-        rows += [t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]]
-    N, V = target.shape
-    tp, pp, up = (_flat(fn, t, what, dt, dev, (N,)) for t, what, dt in
-                  ((tokens, "tokens", _i32), (parents, "parents", _i32), (accept_u, "accept_u", _f32)))
+    gp, gs = _rows(fn, target, "target", target.dtype, dev)
+    shape = target.shape
+    N, V = shape
+    dp, ds = (0, 0) if draft is None else _rows(fn, draft, "draft", target.dtype, dev, shape)
+    nodes = (N,)
+    tp = _flat(fn, tokens, "tokens", _i32, dev, nodes)
+    pp = _flat(fn, parents, "parents", _i32, dev, nodes)
+    up = _flat(fn, accept_u, "accept_u", _f32, dev, nodes)
     sp, B = _nodes(fn, sample_u, "sample_u", _f32, dev)
     starts, max_q = _starts(fn, q_starts, max_q, N, B, dev)
-    _need(fn, path, "path", _i32, dev)
-    if path.dim() != 2 or path.shape[0] != B:
-        raise MxError(fn, MX_ERR_SHAPE, f"path has shape {tuple(path.shape)}, expected [{B}, width]")
-    op = _flat(fn, path, "path", _i32, dev, path.shape)
-    np_ = _flat(fn, tokens_out, "tokens_out", _i32, dev, path.shape)
+    op, sh = _path(fn, path, B, dev)
+    np_ = _flat(fn, tokens_out, "tokens_out", _i32, dev, sh)
     cp = _flat(fn, count, "count", _i32, dev, (B,))
     wp, wb = _workspace(fn, workspace, dev)
     st = load().mx_tree_verify(
-        _VERIFY.pack(rows[0], rows[2], tp, pp, up, sp, starts, op, np_, cp, wp, wb, rows[1], rows[3], B, N,
-                     max_q, V, path.shape[1], _TYPES[target.dtype], bool(replacement)), _stream(stream, dev))
+        _VERIFY.pack(gp, dp, tp, pp, up, sp, starts, op, np_, cp, wp, wb, gs, ds, B, N, max_q, V, sh[1],
+                     _TYPES[target.dtype], bool(replacement)), _stream(stream, dev))
     if st != MX_OK:
         raise MxError(fn, st)
 
@@ -165,10 +181,7 @@ def mx_kv_accept_fp4(caches, page_table, seq_lens, path, count, lens_out=None, q
     packed = [c._packed for c in caches]
     tp, stride, B, width = _table(fn, page_table, dev)
     lens = _flat(fn, seq_lens, "seq_lens", _i32, dev, (B,))
-    _need(fn, path, "path", _i32, dev)
-    if path.dim() != 2 or path.shape[0] != B:
-        raise MxError(fn, MX_ERR_SHAPE, f"path has shape {tuple(path.shape)}, expected [{B}, width]")
-    pp = _flat(fn, path, "path", _i32, dev, path.shape)
+    pp, sh = _path(fn, path, B, dev)
     cp = _flat(fn, count, "count", _i32, dev, (B,))
     op = 0 if lens_out is None else _flat(fn, lens_out, "lens_out", _i32, dev, (B,))
     if max_q is None:
@@ -178,6 +191,6 @@ def mx_kv_accept_fp4(caches, page_table, seq_lens, path, count, lens_out=None, q
     array = ctypes.create_string_buffer(b"".join(packed))
     st = load().mx_kv_accept_fp4(
         _ACCEPT.pack(ctypes.addressof(array), tp, lens, starts, pp, cp, op, len(packed), stride, width, B,
-                     rows, max_q, path.shape[1]), _stream(stream, dev))
+                     rows, max_q, sh[1]), _stream(stream, dev))
     if st != MX_OK:
         raise MxError(fn, st)

@@ -179,6 +179,26 @@ def test_strides_and_one_mask_for_all(mx, n, group):
         assert (rest == 42.0).all()
 
 
+@pytest.mark.parametrize("group", [1, 20])
+def test_masks_beyond_32_bits(mx, group):
+    # a mask whose last rows lie past 2^32 bytes
+    rng = np.random.default_rng(14)
+    n, lens = 4, [90]
+    paged = Paged(rng, lens, 1, 128, 16)
+    parents, starts = forest(rng, [n])
+    rows, pos = D.tree_mask(parents, starts, 1, lens)
+    big = torch.zeros((n - 1) * (1 << 29) + 1, dtype=torch.int32, device="cuda")
+    mask = torch.as_strided(big, (n, 1), (1 << 29, 1))
+    mx.mx_tree_mask(ints(parents), mask, max_q=n)
+    torch.cuda.synchronize()
+    assert np.array_equal(mask.cpu().numpy(), rows)
+    q = bf16(rng.standard_normal((n, group, 128))).cuda()
+    note(f"attn tree mask 6 GiB group={group}")
+    out, lse = run(mx, paged, q, mask, starts, n)
+    ref = D.attention(f64(q), paged.k, paged.ks, paged.v, paged.vs, paged.table, lens, starts, 128 ** -0.5, rows)
+    attention_close(out, lse, ref)
+
+
 def test_rows_behind_the_last_sequence_are_left_alone(mx):
     rng = np.random.default_rng(10)
     for n, group in ((5, 4), (40, 4)):

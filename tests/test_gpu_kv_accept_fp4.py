@@ -140,6 +140,19 @@ def test_offsets_beyond_32_bits(mx):
     check(mx, cs, table, lens, sizes, path, count, 20, tensors=[ts])
 
 
+def test_more_wavefronts_than_a_grid_has(mx):
+    # 64 layers x 65535 sequences: the grid's wavefronts take several each
+    rng = np.random.default_rng(13)
+    B, n = 65535, 4
+    cs = caches(rng, 64, 4, 1, 16, 64)
+    lens, table = np.zeros(B, np.int32), np.full((B, 1), -1, np.int32)
+    path, count = np.full((B, n), -1, np.int32), np.zeros(B, np.int32)
+    for b, page in ((0, 0), (40000, 2), (B - 1, 3)):
+        lens[b], table[b, 0], path[b, :2], count[b] = 16, page, [0, 3], 2
+    note("accept 64 layers x 65535 sequences")
+    check(mx, cs, table, lens, [n] * B, path, count, n, ragged=False)
+
+
 def test_graph_and_stream(mx):
     rng = np.random.default_rng(11)
     sizes, lens = [12, 30], [40, 45]
