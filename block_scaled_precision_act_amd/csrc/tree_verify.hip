@@ -84,15 +84,12 @@ struct Chunk {
       }
     }
   }
-  // Element e of a clean chunk, times 2^-896 (fp16: 2^-1008): its exponent and fraction moved to where a
-  // double has them, subnormal ones too.  (The conversion instruction takes four times as long as two shifts.)
-  static constexpr double kUnscale = TYPE == 2 ? 0x1p1008 : 0x1p896;
+  // Element e of a clean chunk.
   __device__ __forceinline__ double get(int e) const {
-    if constexpr (TYPE == 0)
-      return __builtin_bit_cast(double, uint64_t{x[e] >> 3} << 32 | uint64_t{x[e] << 29});
-    constexpr int kUp = TYPE == 1 ? 13 : 10;
-    const uint32_t hi = e & 1 ? x[e / 2] >> (16 - kUp) & 0xFFFFu << kUp : (x[e / 2] & 0xFFFFu) << kUp;
-    return __builtin_bit_cast(double, uint64_t{hi} << 32);
+    if constexpr (TYPE == 0) return __uint_as_float(x[e]);
+    const uint32_t w = x[e / 2];
+    if constexpr (TYPE == 1) return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(e & 1 ? w >> 16 : w & 0xFFFFu)));
   }
 };
 
@@ -273,7 +270,7 @@ struct Rest {
       if (DRAFT && c != 0.0) w.q.load_some(q, vocab);
     }
   }
-  // Its values, scaled as Chunk::get, element by element from `from`.  A wavefront's chunks lie one after
+  // Its values, element by element from `from`.  A wavefront's chunks lie one after
   // the other.
   __device__ __forceinline__ void values(Loaded& w, double (&r)[kSize]) const {
     const bool has_q = DRAFT && c != 0.0;
@@ -574,7 +571,7 @@ __global__ __launch_bounds__(kThreads) void tree_verify_kernel(const TreeVerifyP
     if (!leads) continue;
     if (parts > 1) seg_sum = team.load(lane);
     upto = wave_prefix(seg_sum);
-    w.s = lane_value(upto, 63) * Chunk<TYPE>::kUnscale;
+    w.s = lane_value(upto, 63);
     w.summed = 1;
   }
   if (team.size > 1) {
