@@ -92,8 +92,9 @@ int attend(const mx_attn_fp4_args& args, const Tree* tree, void* stream) {
   // are too few for it to gain what looking costs (the longest part's tiles; looking takes about 5 us, a
   // tile 2).
   const int64_t tiles = a->table_width * c.page_size / 64;
+  const int64_t slots = plan.split == mx::AttnPlan::kMixed ? mx::AttnPlan::kMixedSlots : 1;
   if (!plan.few && plan.groups > 0 &&
-      (tiles / plan.splits <= mx::kLeastDealTiles || !fits31(units * plan.row_blocks, tiles + 8)))
+      (tiles / plan.splits <= mx::kLeastDealTiles || !fits31(units * plan.row_blocks * slots, tiles + 8)))
     plan.groups = 0;
   if (plan.part_bytes > 0 && (!a->workspace || a->workspace_bytes < mx::kCounterBytes + plan.part_bytes ||
                               !aligned(a->workspace, 256)))

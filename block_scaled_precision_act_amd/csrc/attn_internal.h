@@ -120,6 +120,8 @@ struct AttnPlan {
   bool few;                  // few rows: the cache is what costs (attn_few.hip), else attn_many.hip
   int row_tiles;             // few: 16-row tiles of a workgroup
   int waves, split;          // many: wavefronts of a workgroup, and how many of them share 32 rows
+  static constexpr int kMixed = 3;         // split: of a block with half of its rows or fewer two, else one
+  static constexpr int kMixedSlots = 4;    // of a tile in the deal of such blocks, at most
   int groups;                // workgroups that the cached tokens are dealt to (many: 0: no deal)
   int row_blocks, splits;    // many: blocks of rows of each (sequence, head), parts of their keys at most
   int64_t part_bytes;        // of partial results

@@ -26,7 +26,7 @@
 //
 // TREE: the queries are a tree's nodes, and a mask says which of the sequence's last tokens each sees; its words
 // are read in the last tiles alone.  64 nodes of 4 sequences of up to 131073 tokens, 32 heads of 128 on 8: 534
-// us, 1001 TFLOP/s.  41 ragged trees of up to 12 nodes, 56 heads on 8: 119 us; 33 nodes of 16 heads of 256 on
+// us, 1001 TFLOP/s.  41 ragged trees of up to 12 nodes, 56 heads on 8: 101 us; 33 nodes of 16 heads of 256 on
 // 2, 2 sequences: 71 us, a third of it for the 120 rows that 264 leave empty in three blocks.
 #include "attn_common.h"
 
@@ -113,10 +113,11 @@ __device__ __forceinline__ Work unit_of(const AttnProblem& p, int block_rows, in
 //
 // Parts are joined by attn_join_kernel.
 constexpr int64_t kDealUnits = 4;
-constexpr uint32_t kUnitSlots = 2, kSnap = 2, kLeastShare = 4, kDealCost = 8;
+constexpr uint32_t kUnitSlots = 2, kSnap = 2, kLeastShare = 4, kDealCost = 8;      // tiles
 constexpr int kLeastPart = 4;
 constexpr int kMostEntries = 2048;         // (sequence, block) pairs of a deal
 constexpr int kMostGroups = 512;
+constexpr uint32_t kMixedSlots = AttnPlan::kMixedSlots;
 
 __device__ __forceinline__ int parts_of(int tiles, int splits) {
   return max(1, min(splits, tiles / kLeastPart));
@@ -130,7 +131,19 @@ struct RunStart {
 };
 constexpr int64_t kStartFloats = kMostGroups * sizeof(RunStart) / 4;
 
+// Whether two wavefronts share 32 of the unit's rows where a kernel takes such and others (MIXED).
+__device__ __forceinline__ bool shares(const Work& w, int block_rows) { return w.rows - w.r0 <= block_rows / 2; }
+
+// The slots of a tile: one; or, where units' tiles differ (MIXED), as many as their times are to each other.
+// (Three of four: 5 or 7 of 8 and 2 of 3 leave the runs less even, by 0 to 8 us of 80 to 110.)
+template <bool MIXED>
+__device__ __forceinline__ uint32_t tile_slots(const Work& w, int block_rows) {
+  return !MIXED ? 1 : shares(w, block_rows) ? kMixedSlots - 1 : kMixedSlots;
+}
+
+template <bool MIXED>
 struct Deal {
+  static constexpr uint32_t kScale = MIXED ? kMixedSlots : 1;
   const uint32_t* first;     // of each (sequence, block): its first slot in a head's, in LDS
   uint32_t entries, heads, groups;
 
@@ -154,23 +167,26 @@ struct Deal {
     if (x >= total) return RunStart{total, total, total, 0};
     const uint32_t head = x / per, base = head * per, e = entry(x - base);
     const uint32_t s = base + slot_of(e), end = base + slot_of(e + 1);
-    return RunStart{s, end, x <= s + kUnitSlots + kSnap ? s : x + kSnap >= end ? end : x, head * entries + e};
+    return RunStart{s, end, x <= s + kScale * (kUnitSlots + kSnap) ? s : x + kScale * kSnap >= end ? end : x,
+                    head * entries + e};
   }
 };
 
 // Called by all THREADS of a workgroup; `first` has room for kMostEntries + 3.  The slots of all heads
 // number less than 2^31.
-template <int THREADS, bool TREE>
-__device__ __forceinline__ Deal deal(const AttnProblem& p, int block_rows, int row_blocks, int splits,
-                                     int groups, uint32_t* first) {
-  Deal d;
+template <int THREADS, bool TREE, bool MIXED>
+__device__ __forceinline__ Deal<MIXED> deal(const AttnProblem& p, int block_rows, int row_blocks, int splits,
+                                            int groups, uint32_t* first) {
+  constexpr uint32_t kScale = Deal<MIXED>::kScale;
+  Deal<MIXED> d;
   d.first = first;
   d.entries = p.batch * row_blocks;
   d.heads = p.cache.heads;
   for (uint32_t e = threadIdx.x; e < d.entries; e += THREADS) {
     const uint32_t b = e / row_blocks;
     const Work w = unit_of<TREE>(p, block_rows, 0, b, e - b * row_blocks);
-    first[e + 1] = w.any ? static_cast<uint32_t>(w.tiles) + kUnitSlots : 0u;
+    first[e + 1] =
+        w.any ? static_cast<uint32_t>(w.tiles) * tile_slots<MIXED>(w, block_rows) + kScale * kUnitSlots : 0u;
   }
   __syncthreads();
   if (threadIdx.x < 64) {
@@ -202,11 +218,11 @@ __device__ __forceinline__ Deal deal(const AttnProblem& p, int block_rows, int r
   __syncthreads();
   const uint32_t total = d.per_head() * d.heads, units = max(1u, d.slot_of(d.entries + 2) * d.heads);
   const uint32_t longest = d.slot_of(d.entries + 1);
-  const uint32_t span = max(longest / parts_of(static_cast<int>(longest), splits),
+  const uint32_t span = max(longest / parts_of(static_cast<int>(longest / kScale), splits),
                             (units + groups - 1) / groups * (splits == 1 ? total / units : 0));
-  d.groups = span <= total / groups + kDealCost
+  d.groups = span <= total / groups + kScale * kDealCost
                  ? 0
-                 : max(1u, min(static_cast<uint32_t>(groups), total / kLeastShare));
+                 : max(1u, min(static_cast<uint32_t>(groups), total / (kScale * kLeastShare)));
   return d;
 }
 
@@ -226,7 +242,7 @@ __device__ __forceinline__ ProblemOf<TREE> argument() {
 __device__ __forceinline__ uint32_t group_number() { return blockIdx.y * gridDim.x + blockIdx.x; }
 
 // A workgroup's units or parts, one after the other.  `groups`: runs of a deal (DEALT).
-template <int THREADS, bool DEALT, bool TREE>
+template <int THREADS, bool DEALT, bool TREE, bool MIXED = false>
 struct Walk {
   uint32_t g, x, end;
   bool dealt;
@@ -237,7 +253,7 @@ struct Walk {
     end = 1;
     dealt = false;
     if constexpr (DEALT) {
-      const Deal d = deal<THREADS, TREE>(p, block_rows, row_blocks, splits, groups, first);
+      const Deal<MIXED> d = deal<THREADS, TREE, MIXED>(p, block_rows, row_blocks, splits, groups, first);
       RunStart* const starts = reinterpret_cast<RunStart*>(p.parts);
       if (blockIdx.x == 0 && threadIdx.x == 0) starts[0] = RunStart{0, 0, 0, d.groups};
       if (d.groups == 0) {
@@ -278,13 +294,15 @@ struct Walk {
       w->t_begin += tile0 * kTok;
       return true;
     }
-    const Deal d = {first, static_cast<uint32_t>(p.batch * row_blocks), 0, 0};
+    constexpr uint32_t kScale = Deal<MIXED>::kScale;
+    const Deal<MIXED> d = {first, static_cast<uint32_t>(p.batch * row_blocks), 0, 0};
     const uint32_t per = d.per_head(), head = x / per, base = head * per, e = d.entry(x - base);
     *w = unit_of<TREE>(p, block_rows, head, e / row_blocks, e % row_blocks);
     const uint32_t s = base + d.slot_of(e), stop = base + d.slot_of(e + 1), upto = min(end, stop);
-    const uint32_t tile0 = x > s ? x - s - kUnitSlots : 0;
+    const uint32_t each = tile_slots<MIXED>(*w, block_rows);   // a tile that a run ends inside of is the next run's
+    const uint32_t tile0 = x > s ? (x - s - kScale * kUnitSlots) / each : 0;
     if (x > s || upto < stop) *slot = 2 * g + (x == s);
-    w->tiles = upto - s - kUnitSlots - tile0;
+    w->tiles = (upto - s - kScale * kUnitSlots) / each - tile0;
     w->t_begin += tile0 * kTok;
     x = upto;
     return true;
@@ -298,7 +316,8 @@ struct Row {
 };
 
 template <bool TREE>
-__device__ __forceinline__ Row row_of(const ProblemOf<TREE>& p, const Work& w, int tile, uint32_t thread = threadIdx.x) {
+__device__ __forceinline__ Row row_of(const ProblemOf<TREE>& p, const Work& w, int tile,
+                                      uint32_t thread = threadIdx.x) {
   Row r;
   const int32_t i = w.r0 + tile * 32 + (thread & 31);
   r.live = i < w.rows;
@@ -313,10 +332,10 @@ __device__ __forceinline__ Row row_of(const ProblemOf<TREE>& p, const Work& w, i
 // Its values, as B operands.
 template <int KS>
 __device__ __forceinline__ void load_query(const AttnProblem& p, const Work& w, const Row& r,
-                                           bf16x8 (&qf)[KS]) {
+                                           bf16x8 (&qf)[KS], uint32_t thread = threadIdx.x) {
   const uint16_t* row = p.q.p + static_cast<int64_t>(w.q0 + r.tok) * p.q.token_stride +
                         static_cast<int64_t>(w.h * p.group + r.hg) * p.q.head_stride +
-                        8 * ((threadIdx.x & 63) >> 5);
+                        8 * ((thread & 63) >> 5);
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     uint4 x = r.live ? *reinterpret_cast<const uint4*>(row + 16 * s) : make_uint4(0, 0, 0, 0);
@@ -351,8 +370,9 @@ struct Decoder {
   uint32_t page16, turn_k;
   int sub, k16, kq, vc, vh;
 
-  __device__ __forceinline__ Decoder(const AttnProblem& p_, const Work& w, int sub_) : p(p_), sub(sub_) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ Decoder(const AttnProblem& p_, const Work& w, int sub_, uint32_t thread = threadIdx.x)
+      : p(p_), sub(sub_) {
+    const int lane = thread & 63;
     kbase = p.cache.k + w.h * p.cache.code_head;
     vbase = p.cache.v + w.h * p.cache.code_head;
     ksbase = p.cache.ks + w.h * p.cache.scale_head;
@@ -475,11 +495,12 @@ struct Decoder {
 
 // K steps [j0, j1) of the scores of one 32-token half.
 template <int KS>
-__device__ __forceinline__ void scores(v16f& s, const uint4* keys, const bf16x8 (&qf)[KS], int j0, int j1) {
+__device__ __forceinline__ void scores(v16f& s, const uint4* keys, const bf16x8 (&qf)[KS], int j0, int j1,
+                                       uint32_t thread = threadIdx.x) {
 #pragma unroll
   for (int j = j0; j < j1; ++j)
     s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-        __builtin_bit_cast(bf16x8, keys[j * 64 + (threadIdx.x & 63)]), qf[j], j == 0 ? v16f(0.f) : s, 0, 0, 0);
+        __builtin_bit_cast(bf16x8, keys[j * 64 + (thread & 63)]), qf[j], j == 0 ? v16f(0.f) : s, 0, 0, 0);
 }
 
 // Orders what follows in a block of code: N reads from LDS, or N matrix products.
@@ -490,8 +511,9 @@ __device__ __forceinline__ void then() { __builtin_amdgcn_sched_group_barrier(KI
 // Masks the lane's 16 scores of the 32 tokens from t0.  A tree's window takes of what lies before the
 // tree; of the tree the mask alone does.
 template <bool TREE>
-__device__ __forceinline__ void mask(v16f& s, const ProblemOf<TREE>& p, const Work& w, const Row& r, int32_t t0) {
-  const int32_t half = 4 * ((threadIdx.x & 63) >> 5), at = t0 + half;
+__device__ __forceinline__ void mask(v16f& s, const ProblemOf<TREE>& p, const Work& w, const Row& r, int32_t t0,
+                                     uint32_t thread = threadIdx.x) {
+  const int32_t half = 4 * ((thread & 63) >> 5), at = t0 + half;
   uint32_t bits = ~0u;
   if constexpr (TREE) bits = tree_bits(p, w.q0 + r.tok, t0 - w.first) >> half;
 #pragma unroll
@@ -765,141 +787,154 @@ __device__ __forceinline__ void join_pair(bool second, int pair, v16f (&acc)[DT]
 
 // NW wavefronts.  Of 8, the first four decode keys and the others values (one of each to a SIMD); of 4,
 // all decode both.  Each has 32 query rows and all 64 tokens of a tile (SPLIT 1); or two share 32 rows,
-// with 32 tokens each (SPLIT 2), so that few rows keep every wavefront at work.
+// with 32 tokens each (SPLIT 2), so that few rows keep every wavefront at work; or each unit in the way that
+// its rows ask for (SPLIT kMixed).  The two ways' code is kept apart, for heads of 128: what both derive from
+// the lane's number is derived twice, as kept for both it took registers from the loops (41 x 70 rows of
+// up to 8192 tokens: 166 us, 129 so).
 template <int D, int NW, bool DEALT, bool TREE, int SPLIT>
 __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const ProblemOf<TREE> args, int row_blocks,
                                                                int splits, int groups) {
   constexpr int KS = D / 16, DT = D / 32, kThreads = 64 * NW;
-  constexpr int kTiles = NW / SPLIT, kHalves = 2 / SPLIT;     // of rows; of a tile's tokens, a wavefront's
+  constexpr bool kMixed = SPLIT == AttnPlan::kMixed;
+  constexpr int kBlock = SPLIT == 2 ? 16 * NW : 32 * NW;      // rows
   __shared__ uint4 kl[2][2 * KS * 64];
   __shared__ uint4 vl[2][4 * DT * 64];
-  __shared__ float stats[SPLIT == 2 ? kTiles : 1][2][64];
+  __shared__ float stats[SPLIT != 1 ? NW / 2 : 1][2][64];
   __shared__ uint32_t first[DEALT ? kMostEntries + 3 : 1];
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rows_of = SPLIT == 1 ? wave : wave % kTiles, half = SPLIT == 1 ? 0 : wave / kTiles;
   const bool keys = NW == 4 || wave < 4, values = NW == 4 || wave >= 4;
-  Walk<kThreads, DEALT, TREE> walk(args, 32 * kTiles, row_blocks, splits, groups, first);
+  Walk<kThreads, DEALT, TREE, kMixed> walk(args, kBlock, row_blocks, splits, groups, first);
   for (;;) {
     const ProblemOf<TREE> p = DEALT ? argument<TREE>() : args;
     Work w;
     int slot;
-    if (!walk.next(p, 32 * kTiles, row_blocks, splits, first, &w, &slot)) return;
-    const Row row = row_of<TREE>(p, w, rows_of);
-    bf16x8 qf[KS];
-    load_query(p, w, row, qf);
-    const Decoder<D> dec(p, w, wave & 3);
+    if (!walk.next(p, kBlock, row_blocks, splits, first, &w, &slot)) return;
+    auto attend = [&](auto sharing) __attribute__((always_inline)) {
+      constexpr int kShare = decltype(sharing)::value;
+      constexpr int kTiles = NW / kShare, kHalves = 2 / kShare;   // of rows; of a tile's tokens, a wavefront's
+      const int rows_of = kShare == 1 ? wave : wave % kTiles, half = kShare == 1 ? 0 : wave / kTiles;
+      const uint32_t thread = kMixed && D == 128 ? again(threadIdx.x) : threadIdx.x;
+      const int lane = thread & 63;
+      const Row row = row_of<TREE>(p, w, rows_of, thread);
+      bf16x8 qf[KS];
+      load_query(p, w, row, qf, thread);
+      const Decoder<D> dec(p, w, wave & 3, thread);
 
-    v16f acc[DT];
-    float m = -kInf, l = 0.f;
-    float slack = kSlack;                    // what a row's maximum may rise by before it is moved
+      v16f acc[DT];
+      float m = -kInf, l = 0.f;
+      float slack = kSlack;                    // what a row's maximum may rise by before it is moved
 #pragma unroll
-    for (int d = 0; d < DT; ++d) acc[d] = v16f(0.f);
-    // A wavefront that decodes one of the two holds one share.
-    Raw rk, rv_own;
-    Raw& rv = NW == 4 ? rv_own : rk;
-    Place next_k, next_v_own;
-    Place& next_v = NW == 4 ? next_v_own : next_k;
+      for (int d = 0; d < DT; ++d) acc[d] = v16f(0.f);
+      // A wavefront that decodes one of the two holds one share.
+      Raw rk, rv_own;
+      Raw& rv = NW == 4 ? rv_own : rk;
+      Place next_k, next_v_own;
+      Place& next_v = NW == 4 ? next_v_own : next_k;
 
-    // Tile i: its scores `s` are there; while its weights and products are made, the next tile's scores
-    // are (into `sn`), the keys after those and the next tile's values are decoded, and the ones after
-    // them loaded.  One barrier a tile: K(i + 2) goes where K(i) was, V(i + 1) where V(i - 1) was, both
-    // read by every wavefront before the last barrier.
-    auto step = [&](v16f (&s)[kHalves], v16f (&sn)[kHalves], auto odd, auto final, int32_t i) {
-      constexpr int B = decltype(odd)::value;
-      constexpr bool LAST = decltype(final)::value;
-      const int32_t t0 = w.t_begin + i * kTok;
-      if (t0 + kTok > w.full_hi || t0 < w.full_lo) {
+      // Tile i: its scores `s` are there; while its weights and products are made, the next tile's scores
+      // are (into `sn`), the keys after those and the next tile's values are decoded, and the ones after
+      // them loaded.  One barrier a tile: K(i + 2) goes where K(i) was, V(i + 1) where V(i - 1) was, both
+      // read by every wavefront before the last barrier.
+      auto step = [&](v16f (&s)[kHalves], v16f (&sn)[kHalves], auto odd, auto final, int32_t i) {
+        constexpr int B = decltype(odd)::value;
+        constexpr bool LAST = decltype(final)::value;
+        const int32_t t0 = w.t_begin + i * kTok;
+        if (t0 + kTok > w.full_hi || t0 < w.full_lo) {
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) mask<TREE>(s[h], p, w, row, t0 + (half + h) * 32);
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int e = 1; e < 16 * kHalves; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
-      top = max_halves(top) * p.scale_log2;
-      float scale = p.scale_log2;
-      if (__any(top > m + slack)) {
-        const float now = fmaxf(m, top);
-        const float f = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
-        m = now;
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[d][e] *= f;
-        slack = kSlack;
-        if (large_scores(now)) {
-#pragma unroll
-          for (int e = 0; e < 16 * kHalves; ++e) s[e >> 4][e & 15] = rounded_product(s[e >> 4][e & 15], scale);
-          scale = 1.f;
-          slack = -kInf;
+          for (int h = 0; h < kHalves; ++h) mask<TREE>(s[h], p, w, row, t0 + (half + h) * 32, thread);
         }
-      }
-      const float sub = m == -kInf ? 0.f : m;
+        float top = s[0][0];
 #pragma unroll
-      for (int q = 0; q < 2 * kHalves; ++q) {  // 16 tokens each
-        const bf16x8 pf = weights(s[q >> 1], 8 * (q & 1), scale, sub, l);
+        for (int e = 1; e < 16 * kHalves; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
+        top = max_halves(top) * p.scale_log2;
+        float scale = p.scale_log2;
+        if (__any(top > m + slack)) {
+          const float now = fmaxf(m, top);
+          const float f = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - now);
+          m = now;
+          l *= f;
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-          acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(bf16x8, vl[B][((2 * half + q) * DT + d) * 64 + lane]), pf, acc[d], 0, 0, 0);
-        if constexpr (!LAST)
-          scores(sn[q >> 1], kl[B ^ 1] + (half + (q >> 1)) * KS * 64, qf, (q & 1) * (KS / 2), ((q & 1) + 1) * (KS / 2));
-      }
-      if constexpr (!LAST) {
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+          slack = kSlack;
+          if (large_scores(now)) {
+#pragma unroll
+            for (int e = 0; e < 16 * kHalves; ++e) s[e >> 4][e & 15] = rounded_product(s[e >> 4][e & 15], scale);
+            scale = 1.f;
+            slack = -kInf;
+          }
+        }
+        const float sub = m == -kInf ? 0.f : m;
+#pragma unroll
+        for (int q = 0; q < 2 * kHalves; ++q) {  // 16 tokens each
+          const bf16x8 pf = weights(s[q >> 1], 8 * (q & 1), scale, sub, l);
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8, vl[B][((2 * half + q) * DT + d) * 64 + lane]), pf, acc[d], 0, 0, 0);
+          if constexpr (!LAST)
+            scores(sn[q >> 1], kl[B ^ 1] + (half + (q >> 1)) * KS * 64, qf, (q & 1) * (KS / 2),
+                   ((q & 1) + 1) * (KS / 2), thread);
+        }
+        if constexpr (!LAST) {
+          if (keys) {
+            dec.decode_keys(rk, kl[B]);
+            dec.load_keys(rk, next_k);
+            next_k = dec.place(t0 + 4 * kTok);
+          }
+          if (values) {
+            dec.decode_values(rv, t0 + kTok, vl[B ^ 1]);
+            dec.load_values(rv, next_v);
+            next_v = dec.place(t0 + 3 * kTok);
+          }
+          lds_barrier();
+        }
+      };
+
+      if (w.tiles > 0) {
+        v16f sa[kHalves], sb[kHalves];
         if (keys) {
-          dec.decode_keys(rk, kl[B]);
-          dec.load_keys(rk, next_k);
-          next_k = dec.place(t0 + 4 * kTok);
+          dec.load_keys(rk, dec.place(w.t_begin));
+          dec.decode_keys(rk, kl[0]);
+          dec.load_keys(rk, dec.place(w.t_begin + kTok));
+          dec.decode_keys(rk, kl[1]);
+          dec.load_keys(rk, dec.place(w.t_begin + 2 * kTok));
+          next_k = dec.place(w.t_begin + 3 * kTok);
         }
         if (values) {
-          dec.decode_values(rv, t0 + kTok, vl[B ^ 1]);
-          dec.load_values(rv, next_v);
-          next_v = dec.place(t0 + 3 * kTok);
+          dec.load_first_values(rv, w);
+          dec.decode_values(rv, w.t_begin, vl[0]);
+          dec.load_values(rv, dec.place(w.t_begin + kTok));
+          next_v = dec.place(w.t_begin + 2 * kTok);
         }
         lds_barrier();
-      }
-    };
-
-    if (w.tiles > 0) {
-      v16f sa[kHalves], sb[kHalves];
-      if (keys) {
-        dec.load_keys(rk, dec.place(w.t_begin));
-        dec.decode_keys(rk, kl[0]);
-        dec.load_keys(rk, dec.place(w.t_begin + kTok));
-        dec.decode_keys(rk, kl[1]);
-        dec.load_keys(rk, dec.place(w.t_begin + 2 * kTok));
-        next_k = dec.place(w.t_begin + 3 * kTok);
-      }
-      if (values) {
-        dec.load_first_values(rv, w);
-        dec.decode_values(rv, w.t_begin, vl[0]);
-        dec.load_values(rv, dec.place(w.t_begin + kTok));
-        next_v = dec.place(w.t_begin + 2 * kTok);
-      }
-      lds_barrier();
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h) scores(sa[h], kl[0] + (half + h) * KS * 64, qf, 0, KS);
-      lds_barrier();                           // K(0) is read before K(2) overwrites it
-      int32_t i = 0;
-      for (; i + 2 < w.tiles; i += 2) {
-        step(sa, sb, IntC<0>{}, IntC<0>{}, i);
-        step(sb, sa, IntC<1>{}, IntC<0>{}, i + 1);
+        for (int h = 0; h < kHalves; ++h) scores(sa[h], kl[0] + (half + h) * KS * 64, qf, 0, KS, thread);
+        lds_barrier();                           // K(0) is read before K(2) overwrites it
+        int32_t i = 0;
+        for (; i + 2 < w.tiles; i += 2) {
+          step(sa, sb, IntC<0>{}, IntC<0>{}, i);
+          step(sb, sa, IntC<1>{}, IntC<0>{}, i + 1);
+        }
+        if (i + 1 < w.tiles) {
+          step(sa, sb, IntC<0>{}, IntC<0>{}, i);
+          step(sb, sa, IntC<1>{}, IntC<1>{}, i + 1);
+        } else {
+          step(sa, sb, IntC<0>{}, IntC<1>{}, i);
+        }
       }
-      if (i + 1 < w.tiles) {
-        step(sa, sb, IntC<0>{}, IntC<0>{}, i);
-        step(sb, sa, IntC<1>{}, IntC<1>{}, i + 1);
-      } else {
-        step(sa, sb, IntC<0>{}, IntC<1>{}, i);
-      }
-    }
-    l += __shfl_xor(l, 32, 64);
+      l += __shfl_xor(l, 32, 64);
 
-    if constexpr (SPLIT == 2) {
-      lds_barrier();                         // the last tile's values are read
-      join_pair<DT, kTiles>(half == 1, rows_of, acc, m, l, reinterpret_cast<float*>(vl), stats);
-    }
-    if (SPLIT == 1 || half == 0) finish<DT, 64 * kTiles, TREE>(p, w, row, slot, acc, m, l, 0);
+      if constexpr (kShare == 2) {
+        lds_barrier();                         // the last tile's values are read
+        join_pair<DT, kTiles>(half == 1, rows_of, acc, m, l, reinterpret_cast<float*>(vl), stats);
+      }
+      if (kShare == 1 || half == 0) finish<DT, 2 * kBlock, TREE>(p, w, row, slot, acc, m, l, 0);
+    };
+    if constexpr (!kMixed) attend(IntC<SPLIT>{});
+    else if (!shares(w, kBlock)) attend(IntC<1>{});
+    else attend(IntC<2>{});
     if constexpr (!DEALT) return;
     lds_barrier();                           // before the next one's keys and values
   }
@@ -1060,7 +1095,7 @@ __global__ __launch_bounds__(512, 2) void attn_wide_kernel(const ProblemOf<TREE>
 template <int D, int NW, bool TREE, int SPLIT = 1>
 hipError_t launch(const ProblemOf<TREE>& p, const AttnPlan& plan, hipStream_t stream) {
   constexpr int DT = D / 32, kThreads = D == 256 ? 512 : 64 * NW, N = D == 256 ? DT / 2 : DT;
-  constexpr int kOwners = D == 256 ? 512 : kThreads / SPLIT;           // threads that a part's rows are left by
+  constexpr int kOwners = SPLIT == 2 ? kThreads / 2 : kThreads;        // threads that a part's rows are left by
   const int64_t units = static_cast<int64_t>(plan.row_blocks) * p.batch * p.cache.heads;
   const int64_t most = std::max<int64_t>(units * plan.splits, plan.groups);
   if (most > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
@@ -1116,18 +1151,22 @@ AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
   // Eight wavefronts of 32 rows share the decoding where there are rows for them; with heads of 256,
   // eight share 128 rows.
   a.waves = head_dim == 256 || rows <= 128 ? 4 : 8;
+  const int64_t block_rows = 32 * a.waves;
   a.split = 1;
-  // A tree's 33 to 64 rows: two wavefronts share 32.  (65 to 128 rows, eight wavefronts in pairs: 87 to 90 us
-  // where four with rows of their own take 83 to 89.)
+  // Of a tree's blocks with half of their rows or fewer two wavefronts share 32: all blocks are (up to 64 rows, heads
+  // of 128), or it is looked at, unit by unit.  Without and so, heads of 128: 41 sequences of up to 84 rows and 8192
+  // tokens, 118 us and 101; 16 of up to 132 rows, 100 and 80; 16 of 264 rows, 174 and 157; full blocks 113 and 112.
+  // Heads of 64: 24 sequences of up to 96 rows and 8192 tokens, 80 and 73; full blocks 87 and 89.
   if (tree && head_dim == 128 && rows <= 64) a.split = 2;
-  const int64_t block_rows = 32 * (a.waves / a.split), threads = head_dim == 256 ? 512 : 64 * a.waves;
-  const int64_t blocks = (rows + block_rows - 1) / block_rows;
+  else if (tree && head_dim <= 128) a.split = AttnPlan::kMixed;
+  const int64_t threads = head_dim == 256 ? 512 : 64 * a.waves, owners = a.split == 2 ? threads / 2 : threads;
+  const int64_t blocks = a.split == 2 ? 1 : (rows + block_rows - 1) / block_rows;
   a.row_blocks = static_cast<int>(blocks);
   const int64_t groups = kChipThreads / threads, fit = groups / (blocks * units);
   a.splits = static_cast<int>(fit < 1 ? 1 : fit > 64 ? 64 : fit);
   if (batch > 1 && blocks * units < kDealUnits * groups) a.groups = static_cast<int>(groups);
   if (a.splits > 1 || a.groups > 0)
-    a.part_bytes = 4 * (kStartFloats + (a.groups ? 2 : 1) * groups * part_floats(threads / a.split, head_dim == 64 ? 2 : 4));
+    a.part_bytes = 4 * (kStartFloats + (a.groups ? 2 : 1) * groups * part_floats(owners, head_dim == 64 ? 2 : 4));
   return a;
 }
 
@@ -1147,14 +1186,15 @@ namespace {
 
 template <bool TREE>
 hipError_t launch_any(const ProblemOf<TREE>& p, const AttnPlan& plan, hipStream_t stream) {
+  constexpr int kSplit = TREE ? AttnPlan::kMixed : 1;
   const bool eight = plan.waves == 8;
   if constexpr (TREE) {
     if (plan.split == 2) return launch<128, 4, true, 2>(p, plan, stream);
   }
   if (p.cache.head_dim == 64)
-    return eight ? launch<64, 8, TREE>(p, plan, stream) : launch<64, 4, TREE>(p, plan, stream);
+    return eight ? launch<64, 8, TREE, kSplit>(p, plan, stream) : launch<64, 4, TREE, kSplit>(p, plan, stream);
   if (p.cache.head_dim == 128)
-    return eight ? launch<128, 8, TREE>(p, plan, stream) : launch<128, 4, TREE>(p, plan, stream);
+    return eight ? launch<128, 8, TREE, kSplit>(p, plan, stream) : launch<128, 4, TREE, kSplit>(p, plan, stream);
   return launch<256, 4, TREE>(p, plan, stream);
 }
 

@@ -132,6 +132,20 @@ def test_batches_that_are_dealt_and_joined(mx, dim, n, hk, group, window):
     out, lse, _ = compare(mx, rng, lens, sizes, hk, group, dim, 32, window=window)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,group", [(60, 2), (105, 2), (50, 6)])
+def test_few_rows_beside_many(mx, dim, n, group):
+    # blocks with all, half, one more than half, few and none of their rows, of short texts and of long ones that
+    # are dealt to all workgroups: 120 rows are a block of 128, 210 one of 256, 300 one and a part of the next
+    rng = np.random.default_rng(dim + n)
+    half = (64 if n * group <= 128 else 128) // group
+    sizes = [n, 1, 0, half, half + 1, 5, n, 3]
+    lens = [2300, 2200, 30, 1500, 700, 64, 129, 40]
+    compare(mx, rng, lens, sizes, 37, group, dim, 32, what="dealt")
+    compare(mx, rng, [130, 1, 7, 200, 90, 64, 300, 40], sizes, 3, group, dim, 16, what="not dealt")
+    compare(mx, rng, [3100, 900], [half, n], 1, group, dim, 64, what="split", window=800 if n == 60 else 0)
+
+
 def test_one_long_sequence_is_split(mx):
     rng = np.random.default_rng(8)
     compare(mx, rng, [4001], [26], 1, 8, 128, 64)
