@@ -788,9 +788,9 @@ __device__ __forceinline__ void join_pair(bool second, int pair, v16f (&acc)[DT]
 // NW wavefronts.  Of 8, the first four decode keys and the others values (one of each to a SIMD); of 4,
 // all decode both.  Each has 32 query rows and all 64 tokens of a tile (SPLIT 1); or two share 32 rows,
 // with 32 tokens each (SPLIT 2), so that few rows keep every wavefront at work; or each unit in the way that
-// its rows ask for (SPLIT kMixed).  The two ways' code is kept apart, for heads of 128: what both derive from
-// the lane's number is derived twice, as kept for both it took registers from the loops (41 x 70 rows of
-// up to 8192 tokens: 166 us, 129 so).
+// its rows ask for (SPLIT kMixed).  The two ways' code is kept apart: what both derive from the argument and, for
+// heads of 128, from the lane's number is derived twice, as kept for both it took registers from the loops (41 x
+// 70 rows of up to 8192 tokens: 166 us, 129 so).
 template <int D, int NW, bool DEALT, bool TREE, int SPLIT>
 __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const ProblemOf<TREE> args, int row_blocks,
                                                                int splits, int groups) {
@@ -801,20 +801,22 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const ProblemOf<T
   __shared__ uint4 vl[2][4 * DT * 64];
   __shared__ float stats[SPLIT != 1 ? NW / 2 : 1][2][64];
   __shared__ uint32_t first[DEALT ? kMostEntries + 3 : 1];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool keys = NW == 4 || wave < 4, values = NW == 4 || wave >= 4;
+  const int the_lane = threadIdx.x & 63;
+  const int the_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Walk<kThreads, DEALT, TREE, kMixed> walk(args, kBlock, row_blocks, splits, groups, first);
   for (;;) {
     const ProblemOf<TREE> p = DEALT ? argument<TREE>() : args;
     Work w;
     int slot;
     if (!walk.next(p, kBlock, row_blocks, splits, first, &w, &slot)) return;
-    auto attend = [&](auto sharing) __attribute__((always_inline)) {
+    auto attend = [&](auto sharing, const ProblemOf<TREE>& p) __attribute__((always_inline)) {
       constexpr int kShare = decltype(sharing)::value;
       constexpr int kTiles = NW / kShare, kHalves = 2 / kShare;   // of rows; of a tile's tokens, a wavefront's
-      const int rows_of = kShare == 1 ? wave : wave % kTiles, half = kShare == 1 ? 0 : wave / kTiles;
       const uint32_t thread = kMixed && D == 128 ? again(threadIdx.x) : threadIdx.x;
-      const int lane = thread & 63;
+      const int lane = kMixed ? thread & 63 : the_lane;
+      const int wave = kMixed ? __builtin_amdgcn_readfirstlane(thread >> 6) : the_wave;
+      const int rows_of = kShare == 1 ? wave : wave % kTiles, half = kShare == 1 ? 0 : wave / kTiles;
+      const bool keys = NW == 4 || wave < 4, values = NW == 4 || wave >= 4;
       const Row row = row_of<TREE>(p, w, rows_of, thread);
       bf16x8 qf[KS];
       load_query(p, w, row, qf, thread);
@@ -932,9 +934,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_many_kernel(const ProblemOf<T
       }
       if (kShare == 1 || half == 0) finish<DT, 2 * kBlock, TREE>(p, w, row, slot, acc, m, l, 0);
     };
-    if constexpr (!kMixed) attend(IntC<SPLIT>{});
-    else if (!shares(w, kBlock)) attend(IntC<1>{});
-    else attend(IntC<2>{});
+    if constexpr (!kMixed) attend(IntC<SPLIT>{}, p);
+    else if (!shares(w, kBlock)) attend(IntC<1>{}, argument<TREE>());
+    else attend(IntC<2>{}, argument<TREE>());
     if constexpr (!DEALT) return;
     lds_barrier();                           // before the next one's keys and values
   }
