@@ -26,7 +26,7 @@
 //
 // TREE: the queries are a tree's nodes, and a mask says which of the sequence's last tokens each sees; its words
 // are read in the last tiles alone.  64 nodes of 4 sequences of up to 131073 tokens, 32 heads of 128 on 8: 534
-// us, 1001 TFLOP/s.  41 ragged trees of up to 12 nodes, 56 heads on 8: 101 us; 33 nodes of 16 heads of 256 on
+// us, 1001 TFLOP/s.  41 ragged trees of up to 12 nodes, 56 heads on 8: 99 us; 33 nodes of 16 heads of 256 on
 // 2, 2 sequences: 71 us, a third of it for the 120 rows that 264 leave empty in three blocks.
 #include "attn_common.h"
 
@@ -1157,8 +1157,8 @@ AttnPlan plan_attn(int64_t batch, int64_t max_q, int64_t q_heads, int64_t kv_hea
   a.split = 1;
   // Of a tree's blocks with half of their rows or fewer two wavefronts share 32: all blocks are (up to 64 rows, heads
   // of 128), or it is looked at, unit by unit.  Without and so, heads of 128: 41 sequences of up to 84 rows and 8192
-  // tokens, 118 us and 101; 16 of up to 132 rows, 100 and 80; 16 of 264 rows, 174 and 157; full blocks 113 and 112.
-  // Heads of 64: 24 sequences of up to 96 rows and 8192 tokens, 80 and 73; full blocks 87 and 89.
+  // tokens, 118 us and 99; 16 of up to 132 rows, 100 and 79; 16 of 264 rows, 174 and 157; full blocks 113 and 112.
+  // Heads of 64: 24 sequences of up to 96 rows and 8192 tokens, 81 and 70; full blocks 85 and 87, 93 and 97.
   if (tree && head_dim == 128 && rows <= 64) a.split = 2;
   else if (tree && head_dim <= 128) a.split = AttnPlan::kMixed;
   const int64_t threads = head_dim == 256 ? 512 : 64 * a.waves, owners = a.split == 2 ? threads / 2 : threads;
