@@ -51,9 +51,10 @@ bool outputs_meet(std::initializer_list<Range> outputs, std::initializer_list<Ra
   return false;
 }
 
-// Bytes of `rows` rows.
+// Bytes of `rows` rows, or what no memory holds where they are more.
 int64_t row_bytes(int64_t rows, int64_t stride, int64_t width, int64_t unit) {
-  return rows > 0 ? ((rows - 1) * stride + width) * unit : 0;
+  const __int128 n = rows > 0 ? (static_cast<__int128>(rows - 1) * stride + width) * unit : 0;
+  return static_cast<int64_t>(std::min<__int128>(n, int64_t{1} << 62));
 }
 
 }  // namespace
@@ -157,10 +158,13 @@ int mx_kv_accept_fp4(const mx_kv_accept_fp4_args* a, void* stream) {
     if (x.code_page_stride != c.code_page_stride || x.code_head_stride != c.code_head_stride ||
         x.scale_page_stride != c.scale_page_stride || x.scale_head_stride != c.scale_head_stride)
       return MX_ERR_STRIDE;
-    // One layer's moves must not meet another's.
-    for (int64_t j = 0; c.pages > 0 && j < i; ++j) {
+    // One layer's moves must not meet another's, nor keys' those of values.
+    for (int64_t j = 0; c.pages > 0 && j <= i; ++j) {
       const mx_kv_cache_fp4& y = a->caches[j];
-      if (x.k == y.k || x.v == y.v || x.k_scale == y.k_scale || x.v_scale == y.v_scale) return MX_ERR_STRIDE;
+      if (x.k == y.v || x.k_scale == y.v_scale) return MX_ERR_STRIDE;
+      if (j < i && (x.k == y.k || x.v == y.v || x.k_scale == y.k_scale || x.v_scale == y.v_scale || x.v == y.k ||
+                    x.v_scale == y.k_scale))
+        return MX_ERR_STRIDE;
     }
   }
   if (!fits31(a->batch, c.kv_heads) || !fits31(a->table_width, c.page_size)) return MX_ERR_SHAPE;

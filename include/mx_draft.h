@@ -144,7 +144,7 @@ int64_t mx_tree_verify_workspace_size(int64_t batch);
  * move nothing; page table entries outside [0, pages) neither.
  * lens_out (or NULL): first + count[b], at least 0: the sequences' lengths without what was rejected.
  * Blocks of a cache must not lie on each other, nor those of two layers (the same cache twice is
- * refused); a page that holds nodes belongs to one sequence.  layers at most 1024.
+ * refused), nor keys on values; a page that holds nodes belongs to one sequence.  layers at most 1024.
  */
 typedef struct mx_kv_accept_fp4_args {
   const mx_kv_cache_fp4* caches;                  /* host array of `layers`                   */

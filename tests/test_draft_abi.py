@@ -67,6 +67,7 @@ def _call(lib, fn, good, change, keep=()):
 
 
 def _expect(status):
+    """The status; to be asked for before the call, which goes on to the GPU where there is one."""
     if status == "device":
         if torch.cuda.is_available():
             pytest.skip("a GPU is visible: fake addresses must not reach it")
@@ -105,7 +106,8 @@ MASK = dict(parents=A, seq_lens=A, mask=B, positions=2 * B, mask_stride=2, mask_
     (dict(total_q=0, q_starts=A, mask=0), OK), ({}, "device"), (dict(seq_lens=0, positions=0), "device"),
     (dict(q_starts=A, max_q=64), "device")])
 def test_tree_mask(lib, change, status):
-    assert _call(lib, "mx_tree_mask", MASK, change) == _expect(status)
+    expected = _expect(status)
+    assert _call(lib, "mx_tree_mask", MASK, change) == expected
     assert lib.mx_tree_mask(None, None) == N
 
 
@@ -125,7 +127,8 @@ ATTN = dict(q=A, out=A, mask=A, page_table=A, seq_lens=A, workspace=A, workspace
     (dict(window=5, positions=A), "device"), (dict(q_starts=A, max_q=64), "device")])
 def test_attn_tree(lib, change, status):
     keep, c = _caches({})
-    assert _call(lib, "mx_attn_tree_fp4", {**ATTN, "cache": c}, change) == _expect(status)
+    expected = _expect(status)
+    assert _call(lib, "mx_attn_tree_fp4", {**ATTN, "cache": c}, change) == expected
     assert lib.mx_attn_tree_fp4(None, None) == N
 
 
@@ -154,7 +157,8 @@ VERIFY = dict(target=A, draft=A, tokens=A, parents=A, accept_u=A, sample_u=A, pa
     (dict(total_q=0, max_q=0, target=0, tokens=0), "device"), ({}, "device"), (dict(draft=0, draft_stride=0), "device"),
     (dict(draft_stride=0), "device"), (dict(type=2, target=A + 2, draft=A + 2), "device")])
 def test_verify(lib, change, status):
-    assert _call(lib, "mx_tree_verify", VERIFY, change) == _expect(status)
+    expected = _expect(status)
+    assert _call(lib, "mx_tree_verify", VERIFY, change) == expected
     assert lib.mx_tree_verify(None, None) == N
 
 
@@ -180,7 +184,8 @@ ACCEPT = dict(page_table=A, seq_lens=A, path=A, count=A, lens_out=B, layers=2, t
     (dict(table_width=0, page_table=0, table_stride=0), "device"), (dict(width=0, path=0), "device")])
 def test_accept(lib, change, status):
     keep, c = _caches({}, {})
-    assert _call(lib, "mx_kv_accept_fp4", {**ACCEPT, "caches": c}, change) == _expect(status)
+    expected = _expect(status)
+    assert _call(lib, "mx_kv_accept_fp4", {**ACCEPT, "caches": c}, change) == expected
     assert lib.mx_kv_accept_fp4(None, None) == N
 
 
@@ -190,7 +195,18 @@ def test_accept(lib, change, status):
     (dict(v=0), N), (dict(k=A + 65536 + 8), AL), ({}, "device")])
 def test_accept_layers_have_one_shape(lib, change, status):
     keep, c = _caches({}, change)
-    assert _call(lib, "mx_kv_accept_fp4", {**ACCEPT, "caches": c}, {}) == _expect(status)
+    expected = _expect(status)
+    assert _call(lib, "mx_kv_accept_fp4", {**ACCEPT, "caches": c}, {}) == expected
+
+
+@pytest.mark.parametrize("change", [dict(k=A + 8192 + 65536), dict(v=A), dict(v_scale=A + 4096), dict(k_scale=A + 12288)])
+def test_accept_refuses_keys_that_lie_on_values(lib, change):
+    keep, c = _caches({}, change)
+    assert _call(lib, "mx_kv_accept_fp4", {**ACCEPT, "caches": c}, {}) == ST
+
+
+def test_rows_longer_than_any_memory_meet_what_lies_behind_them(lib):
+    assert _call(lib, "mx_tree_mask", MASK, dict(mask=A - 4096, mask_stride=1 << 60)) == ST
 
 
 def test_accept_refuses_blocks_that_lie_on_each_other(lib):
