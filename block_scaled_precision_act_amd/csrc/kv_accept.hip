@@ -65,8 +65,8 @@ __global__ __launch_bounds__(kThreads) void kv_accept_kernel(const KvAcceptProbl
       }
       const bool moves = from < p.shape.pages && to < p.shape.pages;
       if (!__any(moves)) continue;
-      const int64_t at = from * p.shape.code_page + h0 * p.shape.code_head + from_off * (D / 2);
-      const int64_t scale_at = from * p.shape.scale_page + h0 * p.shape.scale_head + from_off * (D / 32);
+      const int64_t at = from * p.shape.code_page + h0 * p.shape.code_head + int64_t{from_off} * (D / 2);
+      const int64_t scale_at = from * p.shape.scale_page + h0 * p.shape.scale_head + int64_t{from_off} * (D / 32);
       v4u x[kHeads];
       Scales y[kHeads];
 #pragma unroll
@@ -80,8 +80,8 @@ __global__ __launch_bounds__(kThreads) void kv_accept_kernel(const KvAcceptProbl
       __builtin_amdgcn_s_waitcnt(kVmcntZero);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      const int64_t put = to * p.shape.code_page + h0 * p.shape.code_head + to_off * (D / 2);
-      const int64_t scale_put = to * p.shape.scale_page + h0 * p.shape.scale_head + to_off * (D / 32);
+      const int64_t put = to * p.shape.code_page + h0 * p.shape.code_head + int64_t{to_off} * (D / 2);
+      const int64_t scale_put = to * p.shape.scale_page + h0 * p.shape.scale_head + int64_t{to_off} * (D / 32);
 #pragma unroll
       for (int h = 0; h < kHeads; ++h) {
         if (moves && h < heads) {
