@@ -1,10 +1,12 @@
-"""mx_kv_accept_fp4 at the ends of what its arguments may be: pages of more than 4 GiB."""
+"""mx_kv_accept_fp4 at the ends of what its arguments may be: pages of more than 4 GiB, caches that can
+be gone over only once."""
 import numpy as np
 import pytest
 import torch
 
 from draft_util import ints
 from gpu_util import note
+from oracle import draft_oracle as D
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +35,28 @@ def test_pages_of_more_than_4_gib(mx, dim):
             assert torch.equal(t[0, 0, nodes], want)
             t[0, 0, nodes] = 0                                 # nothing else is written
             assert not any(bool(part.any()) for part in t.view(-1).split(1 << 30))
+
+
+@pytest.mark.parametrize("of", [iter, lambda cs: (c for c in cs), lambda cs: map(lambda c: c, cs), tuple,
+                                lambda cs: dict(enumerate(cs)).values()])
+def test_caches_from_any_iterable(mx, of):
+    rng = np.random.default_rng(1)
+    table, sizes, lens, path, count = np.array([[2, 0], [1, 3]]), [9, 5], [20, 25], [[0, 3, 8], [0, 2, 4]], [3, 2]
+    cs = [[rng.integers(0, 256, (4, 2, 16, w), dtype=np.uint8) for w in (64, 4) * 2] for _ in range(3)]
+    ts = [[torch.from_numpy(a).cuda() for a in c] for c in cs]
+    new = ints([-77, -77])
+    note("accept caches from an iterable")
+    mx.mx_kv_accept_fp4(of([mx.MxKvCacheFp4(*t) for t in ts]), ints(table), ints(lens), ints(path), ints(count),
+                        lens_out=new, q_starts=ints([0, 9, 14]), max_q=9)
+    torch.cuda.synchronize()
+    for c, t in zip(cs, ts):
+        want, lengths = D.accept(c, table, lens, [0, 9, 14], np.array(path), count)
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(t, want))
+    assert np.array_equal(new.cpu().numpy(), lengths)
+
+
+def test_iterables_of_what_is_no_cache_are_refused(mx):
+    good = mx.MxKvCacheFp4(*(torch.zeros((4, 2, 16, w), dtype=torch.uint8, device="cuda") for w in (64, 4) * 2))
+    for caches in (iter([good, None]), (c for c in (good, "k")), None, 5):
+        with pytest.raises(TypeError):
+            mx.mx_kv_accept_fp4(caches, ints([[0, 1]]), ints([20]), ints([[0, 2]]), ints([2]), max_q=4)
