@@ -147,9 +147,12 @@ int mx_kv_accept_fp4(const mx_kv_accept_fp4_args* a, void* stream) {
   if (st != MX_OK) return st;
   if (a->layers < 0 || a->layers > kMostLayers || a->width < 0 || !fits31(a->batch, a->width) || a->table_width < 0)
     return MX_ERR_SHAPE;
-  if (a->layers == 0 || a->batch == 0) return MX_OK;
+  if (a->batch == 0 || (a->layers == 0 && (!a->caches || !a->lens_out))) return MX_OK;
   if (!a->caches) return MX_ERR_NULL;
-  const mx_kv_cache_fp4& c = a->caches[0];
+  // Without layers the new lengths alone are written: one cache of no pages, and lengths that no table covers.
+  const bool none = a->layers == 0;
+  const mx_kv_cache_fp4 empty = {nullptr, nullptr, nullptr, nullptr, 0, 1, 1, 64, 0, 0, 0, 0};
+  const mx_kv_cache_fp4& c = none ? empty : a->caches[0];
   for (int64_t i = 0; i < a->layers; ++i) {
     const mx_kv_cache_fp4& x = a->caches[i];
     if ((st = cache_status(&x)) != MX_OK) return st;
@@ -188,11 +191,17 @@ int mx_kv_accept_fp4(const mx_kv_accept_fp4_args* a, void* stream) {
   p.shape = cache_of(c);
   p.table = a->page_table;
   p.table_stride = a->table_stride;
-  p.table_width = static_cast<int32_t>(a->table_width);
+  p.table_width = static_cast<int32_t>(none ? kMax31 : a->table_width);
   p.lens = a->seq_lens;
   p.path = a->path;
   p.count = a->count;
   p.width = static_cast<int32_t>(a->width);
+  if (none) {
+    p.layers = 1;
+    p.layer[0] = {};
+    p.lens_out = a->lens_out;
+    return status_of(launch_kv_accept_fp4(p, static_cast<hipStream_t>(stream)));
+  }
   for (int64_t at = 0; at < a->layers; at += kLayersALaunch) {
     p.layers = static_cast<int32_t>(std::min<int64_t>(kLayersALaunch, a->layers - at));
     p.lens_out = at == 0 ? a->lens_out : nullptr;

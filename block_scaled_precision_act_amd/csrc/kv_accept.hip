@@ -43,6 +43,7 @@ __global__ __launch_bounds__(kThreads) void kv_accept_kernel(const KvAcceptProbl
     const int32_t len = raw < 0 ? 0 : (raw < covered ? raw : static_cast<int32_t>(covered));
     const int32_t first = len - s.n, count = min(max(read_uniform(p.count, b), 0), min(s.n, p.width));
     if (p.lens_out && layer == 0 && h0 == 0 && lane == 0) p.lens_out[b] = max(first + count, 0);
+    if (p.shape.pages == 0) continue;      // nothing moves, and the table is not what `covered` says without layers
     const int32_t heads = min(static_cast<int32_t>(p.shape.heads - h0), kHeads);
     const int32_t* const path = p.path + static_cast<int64_t>(b) * p.width;
     const int32_t* const table = p.table + b * p.table_stride;

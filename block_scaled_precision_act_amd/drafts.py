@@ -171,7 +171,8 @@ def mx_kv_accept_fp4(caches, page_table, seq_lens, path, count, lens_out=None, q
     page_table (int32 [batch, width]).  seq_lens: int32 [batch], tokens cached with the nodes; path int32
     [batch, width] and count int32 [batch] as mx_tree_verify writes them.  Node path[i] becomes the i-th
     token after the text; lens_out (int32 [batch], not seq_lens, or None): the lengths with the accepted
-    nodes alone.  Without q_starts, max_q nodes each."""
+    nodes alone, written without any cache too (an empty sequence, on a stage that has no attention).  Without
+    q_starts, max_q nodes each."""
     fn, dev = "mx_kv_accept_fp4", _current_device()
     caches = (caches,) if isinstance(caches, MxKvCacheFp4) else tuple(caches)     # gone over more than once
     if any(type(c) is not MxKvCacheFp4 or c.device_index != dev for c in caches):

@@ -143,6 +143,9 @@ int64_t mx_tree_verify_workspace_size(int64_t batch);
  * is written.  Entries outside [0, n), and tokens before 0 or past what the page table covers,
  * move nothing; page table entries outside [0, pages) neither.
  * lens_out (or NULL): first + count[b], at least 0: the sequences' lengths without what was rejected.
+ * It is written without layers too (layers 0, say on a stage that has no attention; `caches` not NULL but
+ * not read): there is no page size then, so lengths are taken as they are, negative ones as 0.  With layers 0
+ * and caches NULL the call does nothing, lens_out or not.
  * Blocks of a cache must not lie on each other, nor those of two layers (the same cache twice is
  * refused), nor keys on values; a page that holds nodes belongs to one sequence.  layers at most 1024.
  */

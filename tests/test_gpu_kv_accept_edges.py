@@ -1,5 +1,5 @@
 """mx_kv_accept_fp4 at the ends of what its arguments may be: pages of more than 4 GiB, caches that can
-be gone over only once."""
+be gone over only once, no caches at all."""
 import numpy as np
 import pytest
 import torch
@@ -60,3 +60,48 @@ def test_iterables_of_what_is_no_cache_are_refused(mx):
     for caches in (iter([good, None]), (c for c in (good, "k")), None, 5):
         with pytest.raises(TypeError):
             mx.mx_kv_accept_fp4(caches, ints([[0, 1]]), ints([20]), ints([[0, 2]]), ints([2]), max_q=4)
+
+
+@pytest.mark.parametrize("caches", [list, tuple, lambda: iter(())])
+def test_new_lengths_are_written_without_layers(mx, caches):
+    sizes = [9, 0, 5, 30, 7, 4, 12, 3]
+    lens, count = [20, 11, 25, 12, -3, 2 ** 31 - 1, 40, 9], [3, 0, 5, 2, 1, 4, 100, -8]
+    starts = np.cumsum([0, *sizes])
+    path, table = np.tile(np.arange(6), (8, 1)), np.full((8, 1), 2 ** 31 - 1)       # a table of nothing
+    # no page size to clamp lengths by; counts as elsewhere
+    want = [max(max(L, 0) - n + min(max(k, 0), n, 6), 0) for L, n, k in zip(lens, sizes, count)]
+    new = ints([-77] * 9)
+    note("accept without layers")
+    mx.mx_kv_accept_fp4(caches(), ints(table), ints(lens), ints(path), ints(count), lens_out=new[:8], q_starts=ints(starts),
+                        max_q=30)
+    torch.cuda.synchronize()
+    assert new.tolist() == [*want, -77]
+
+
+def test_new_lengths_without_layers_of_many_sequences_in_a_graph(mx):
+    B, n = 65535, 4
+    rng = np.random.default_rng(2)
+    path, table = ints(np.tile([0, 1, 3, -1], (B, 1))), ints(np.zeros((B, 1)))
+    lens, count, new = ints(rng.integers(n, 1000, B)), ints(rng.integers(0, 4, B)), ints(np.full(B, -77))
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    note("accept without layers, captured")
+    with torch.cuda.graph(graph, stream=side):
+        mx.mx_kv_accept_fp4([], table, lens, path, count, lens_out=new, max_q=n)
+    for _ in range(3):
+        lens.add_(5)
+        count.copy_(ints(rng.integers(0, 4, B)))
+        new.fill_(-77)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(new, lens - n + count)
+
+
+def test_lengths_of_caches_of_no_pages(mx):
+    # nothing moves, whatever path and table say; lengths end where the table does
+    cache = mx.MxKvCacheFp4(*(torch.zeros((0, 2, 16, w), dtype=torch.uint8, device="cuda") for w in (64, 4) * 2))
+    new = ints([-77, -77])
+    note("accept of no pages")
+    mx.mx_kv_accept_fp4([cache], ints([[0, 1], [5, -1]]), ints([20, 99]), ints([[0, 2], [0, 3]]), ints([2, 1]), lens_out=new, max_q=4)
+    torch.cuda.synchronize()
+    assert new.tolist() == [18, 29]
