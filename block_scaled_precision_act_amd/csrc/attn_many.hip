@@ -25,9 +25,9 @@
 // of the CU) leave one wavefront a SIMD and nothing to cover its waits with, 595 us.
 //
 // TREE: the queries are a tree's nodes, and a mask says which of the sequence's last tokens each sees; its words
-// are read in the last tiles alone.  64 nodes of 4 sequences of up to 131073 tokens, 32 heads of 128 on 8: 534
-// us, 1001 TFLOP/s.  41 ragged trees of up to 12 nodes, 56 heads on 8: 99 us; 33 nodes of 16 heads of 256 on
-// 2, 2 sequences: 71 us, a third of it for the 120 rows that 264 leave empty in three blocks.
+// are read in the last tiles alone.  64 nodes of 4 sequences of up to 131073 tokens, 32 heads of 128 on 8: 533
+// to 562 us (by box), 950 to 1003 TFLOP/s.  41 ragged trees of up to 12 nodes, 56 heads on 8: 99 us; 33 nodes of
+// 16 heads of 256 on 2, 2 sequences: 71 us, a third of it for the 120 rows that 264 leave empty in three blocks.
 #include "attn_common.h"
 
 #include <algorithm>

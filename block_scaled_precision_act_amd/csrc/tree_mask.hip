@@ -4,8 +4,11 @@
 // takes a sequence's tree; its parents lie in LDS, and a thread makes one word of one node's mask by
 // following the parents down to it (they only fall, so a word's thread stops below its nodes).
 //
-// Bound by latency: the parents' load, a few LDS reads for each level, the stores.  26 nodes: 1.8 us, the launch;
-// 128 trees of up to 129 nodes: 3.8 us.
+// Bound by latency: the parents' load, the stores, and between them LDS reads one after the other, an ancestor each,
+// for every word that a thread makes: nodes x words / 256 words of up to `depth` reads.  That is little for trees as
+// deep as drafts are (26 nodes: 1.8 us, the launch; 128 trees of up to 129 nodes, 3.4 to 3.8 us; 1024 nodes, three
+// children each: 85 us), but it grows with the cube of a chain's length: 26 nodes 3.2 us, 64 5.5, 129 18, 200 44, 512
+// 541, 1024 4278 (128 chains of 1024 as long).
 #include "draft_common.h"
 
 namespace mx {

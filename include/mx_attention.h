@@ -177,7 +177,9 @@ int mx_kv_append_fp4(const mx_kv_append_fp4_args* args, void* stream);
  * workspace: mx_attn_fp4_workspace_size bytes, 256-byte aligned, zero before its first use and left
  * reusable by every call; the size depends on the sizes alone, not on lengths, and suffices for every
  * smaller max_q and batch too.  One workspace serves calls of any sizes it is large enough for;
- * calls that may overlap need workspaces of their own.  q and out rows must be 16-byte aligned
+ * calls that may overlap need workspaces of their own.  The size covers mx_attn_tree_fp4 (mx_draft.h) as well,
+ * which needs more of it with 33 to 64 rows of heads of 128 (43 MB, mx_attn_fp4 itself 26) and 17 to 32 of
+ * heads of 256 (77 and 26): mx_attn_fp4 is content with what it needs itself.  q and out rows must be 16-byte aligned
  * (bases 16-byte aligned, strides multiples of 8 elements).
  * At most 64 rows (queries of a sequence times q_heads / kv_heads; 32 with heads of 256) take a path
  * bound by reading the cache, for at most 2^21 sequences times kv_heads; more rows one bound by the

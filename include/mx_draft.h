@@ -37,6 +37,9 @@ extern "C" {
  * token would stand if its path were the text, as rotations and windows count it.
  * positions and seq_lens: both, or both NULL.  max_q at most 1024, mask_words at least max_q / 32
  * rounded up.  Rows of `mask` must not lie on each other.
+ * Every word of a mask follows the node's ancestors, so the time grows with depth times nodes times words: 2
+ * us for trees as deep as drafts are, but chains take 6 us with 64 nodes, 18 with 129, 0.54 ms with 512 and 4.3 ms
+ * with 1024.
  */
 typedef struct mx_tree_mask_args {
   const int32_t* parents;                         /* [total_q]                                */
@@ -59,7 +62,10 @@ int mx_tree_mask(const mx_tree_mask_args* args, void* stream);
  * window takes none of these).  mask rows may be the same one (mask_stride 0).  positions may be NULL
  * without a window.  max_q at most 65536, mask_words at least max_q / 32 rounded up.
  * Everything else (arguments, formulas, roundings, limits, what lies beyond lengths, rows that see
- * nothing, the workspace and its size) is as in mx_attn_fp4.
+ * nothing, the workspace and its size) is as in mx_attn_fp4.  A chain's nodes are off from what mx_attn_fp4's
+ * causal mask gives by the roundings at most: trees are summed in other runs.  Nodes that no query sees are hidden
+ * like other masked keys, any key bytes but values that are finite: where seq_lens counts padding nodes that are
+ * never appended, their places have to hold some (zeros will do).
  */
 typedef struct mx_attn_tree_fp4_args {
   const mx_kv_cache_fp4* cache;
